@@ -21,6 +21,12 @@
  *   pa_copy_blocks       Copy-on-write copy of whole blocks before a forked sequence
  *                        writes into a block it shares (concept card, 实现要点;
  *                        "深入解析 PagedAttention", 多序列共享).
+ *   pa_rope_and_cache    Rotary positions of the step's queries and keys, fused with the
+ *                        cache write.
+ *   pa_attention         Attention of prompts, chunks or single tokens over the paged cache,
+ *                        with capped or biased scores and window, prefix or document masks.
+ *   pa_beam_topk         Beam search's selection over beams and vocabulary, whose parents
+ *                        pa_alloc_beam_select (blocks) and pa_beam_gather (other states) apply.
  *   pa_alloc_*           Host-side block allocator with reference counts: on-demand
  *                        blocks, fork = share + refcount, free at refcount 0, copy on
  *                        write ("深入解析 PagedAttention", 核心创新 and 多序列共享;
@@ -82,7 +88,8 @@ typedef enum pa_status {
   PA_ERR_BAD_SLOT = 9,       /* device flag: slot >= num_blocks*block_size */
   PA_ERR_TIMEOUT = 10,       /* device flag: a bounded pipeline wait gave up */
   PA_ERR_SCRATCH_LIMIT = 11, /* pa_decode_no_alloc: the shape needs more than its static scratch */
-  PA_ERR_HOST_MEMORY = 12    /* allocator: a host allocation failed; state unchanged */
+  PA_ERR_HOST_MEMORY = 12,   /* allocator: a host allocation failed; state unchanged */
+  PA_ERR_BAD_PARENT = 13     /* device flag: a beam's parent outside [0, W) */
 } pa_status;
 
 typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1 } pa_dtype;
@@ -92,6 +99,7 @@ typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1 } pa_dtype;
 #define PA_DEVERR_BAD_SEQ_LEN 0x2
 #define PA_DEVERR_BAD_SLOT 0x4
 #define PA_DEVERR_TIMEOUT 0x8
+#define PA_DEVERR_BAD_PARENT 0x10
 
 /* Static, NUL-terminated description of a status. */
 const char* pa_status_string(pa_status status);
@@ -302,6 +310,133 @@ pa_status pa_reshape_and_cache(const void* key, const void* value, void* k_pool,
 pa_status pa_copy_blocks(void* k_pool, void* v_pool, const int32_t* pairs, int n,
                          int block_size, int Hkv, int D, int num_blocks, pa_dtype dtype,
                          int32_t* dev_err_flag, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions with the cache write
+ * ------------------------------------------------------------------------- */
+
+typedef enum pa_rope_layout {
+  PA_ROPE_HALF = 0,        /* pair i of a head: elements i and i + rotary_dim / 2 */
+  PA_ROPE_INTERLEAVED = 1  /* pair i: elements 2i and 2i + 1 */
+} pa_rope_layout;
+
+/* How the frequencies base^(-2i / rotary_dim) change for contexts `factor` times as long as
+ * the `original_len` positions a model was trained on. */
+typedef enum pa_rope_scaling {
+  PA_ROPE_SCALE_NONE = 0,
+  PA_ROPE_SCALE_LINEAR = 1, /* all divided by factor (positions interpolated) */
+  PA_ROPE_SCALE_BASE = 2,   /* base * factor^(R / (R - 2)): the slowest pair is interpolated by
+                               factor, the fastest not at all */
+  PA_ROPE_SCALE_RAMP = 3,   /* YaRN (Peng et al., 2023): a pair that turns at least `fast` times
+                               in original_len is kept, one that turns at most `slow` times is
+                               divided by factor, a linear ramp over the pair's index between;
+                               *attn_factor = 0.1 ln(factor) + 1 (factor > 1) */
+  PA_ROPE_SCALE_BANDS = 4   /* the same two ends, the ramp linear in the number of turns */
+} pa_rope_scaling;
+
+/* Host only: inv_freq[rotary_dim / 2] (host array, radians per position, 64 bits) and
+ * *attn_factor (the factor on cos and sin, 1 except for PA_ROPE_SCALE_RAMP).  factor,
+ * original_len, fast and slow are read by the scalings that use them. */
+pa_status pa_rope_frequencies(int rotary_dim, double base, pa_rope_scaling scaling, double factor,
+                              int original_len, double fast, double slow, double* inv_freq,
+                              float* attn_factor);
+
+/* For t < T, with theta_i = positions[t] * inv_freq[i] and f = attn_factor: the pairs (a, b) of
+ * the first rotary_dim elements of every head of q[t] and k[t] become
+ *   f * (a cos theta_i - b sin theta_i, a sin theta_i + b cos theta_i)
+ * and the elements from rotary_dim on stay.  q goes to q_out[t] ([T][Hq][D], contiguous; may be
+ * q itself where q is contiguous), k and the unchanged v to slot slot_mapping[t] of the pools
+ * (as pa_reshape_and_cache; a slot < 0 rotates q only).  Angles are formed and reduced in 64
+ * bits; the rotation is fp32, rounded once.
+ *   inv_freq      [rotary_dim / 2] DEVICE array (pa_rope_frequencies, copied there once)
+ *   positions     [T] int32 device
+ *   q/k/v_stride  elements between the tokens of q, k and v (>= heads * D), so that they may be
+ *                 parts of one projection's output; strides that are not multiples of 16 bytes
+ *                 take a slower kernel
+ * rotary_dim is even, 2 .. D.  Non-negative slots must be distinct within a call. */
+pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const void* v, void* k_pool,
+                            void* v_pool, const int32_t* positions, const int64_t* slot_mapping,
+                            const double* inv_freq, int T, int Hq, int Hkv, int D, int block_size,
+                            int num_blocks, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                            int rotary_dim, pa_rope_layout layout, float attn_factor, pa_dtype dtype,
+                            int32_t* dev_err_flag, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of prompts, chunks and single tokens over the paged cache
+ * ------------------------------------------------------------------------- */
+
+/* What is done to the scores, and which keys a query token sees.  All zero / NULL: the plain
+ * causal attention. */
+typedef struct pa_attention_mods {
+  float softcap;               /* > 0: x = softcap * tanh(x / softcap); 0: none */
+  int window;                  /* > 0: only the last `window` keys up to the token's own position
+                                  (and later ones of the prefix); 0: no limit */
+  const float* alibi_slopes;   /* [Hq] device, nullable: x -= slopes[h] * |p - j| (after the cap) */
+  const int32_t* prefix_lens;  /* [B] device, nullable: keys j < prefix_lens[b] are visible to
+                                  every query token of sequence b, earlier ones included */
+  const int32_t* first_keys;   /* [T] device, nullable: query token t sees no key before
+                                  first_keys[t] (documents packed into one sequence: the first
+                                  position of the token's document) */
+} pa_attention_mods;
+
+/* Query token i (of n) of sequence b stands at position p = seq_lens[b] - n + i of the sequence:
+ * its K/V and those of all tokens before it are in the cache already.  With
+ *   n = query_starts[b + 1] - query_starts[b], t = query_starts[b] + i
+ * and x_j = scale * q[t][h].k_j, capped and biased as mods says,
+ *   out[t][h] = sum_j softmax_j(x_j) v_j over the keys j < seq_lens[b] with
+ *   (j <= p or j < prefix_lens[b]) and (window == 0 or j > p - window) and j >= first_keys[t].
+ * A token that sees no key gets a zero row (an empty sequence, a position below 0, or a
+ * first key past it).  Rows of out from query_starts[B] on are left as they were.
+ *   q            [T] tokens of [Hq][D], q_stride elements apart (a multiple of 16 bytes, so q may
+ *                be part of a projection's output); out [T][Hq][D] contiguous
+ *   query_starts [B + 1] int32 device, not decreasing, query_starts[B] <= T
+ *   max_query_len  an upper bound on the query tokens of a sequence (chooses the kernel: 1 means
+ *                single tokens); a sequence with more raises PA_DEVERR_BAD_SEQ_LEN
+ * Table entries of blocks that hold no key visible to any token of the call are not read (a
+ * window's freed blocks may be -1).  Slots past seq_lens[b] may hold anything.  A key that some
+ * query token of the sequence sees must hold finite values: a NaN or infinity there may also
+ * reach up to 255 neighbouring (token, head) rows that do not see it.
+ * mods may be NULL.  Workspace: pa_attention_workspace_size bytes, 256-byte aligned; its contents
+ * need no initialisation, and calls whose kernels may overlap on the GPU must not share one.
+ * Any Hq / Hkv, D in {64, 128}, block_size in {4, 8, 16, 32}, bf16 or fp32. */
+size_t pa_attention_workspace_size(int T, int B, int max_query_len, int Hq, int Hkv, int D,
+                                   int block_size, int max_blocks);
+pa_status pa_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
+                       const int32_t* block_tables, const int32_t* seq_lens,
+                       const int32_t* query_starts, int T, int B, int max_query_len, int Hq, int Hkv,
+                       int D, int block_size, int max_blocks, int num_blocks, int64_t q_stride,
+                       float scale, const pa_attention_mods* mods, pa_dtype dtype, void* workspace,
+                       size_t workspace_bytes, int32_t* dev_err_flag, pa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Beam search: selection, and reordering of states
+ * ------------------------------------------------------------------------- */
+
+/* The k best candidates of each of N requests with W beams over a vocabulary of V tokens, best
+ * first: candidate (w, v) scores
+ *   cum_scores[n][w] + logits[n][w][v] - log(sum_v' exp(logits[n][w][v'])),
+ * ties go to the lowest w * V + v (within a beam equal scores mean equal logits).
+ *   logits      [N * W] rows of V, row_stride elements apart
+ *   cum_scores  [N][W] fp32 device; a beam at -inf (not yet in use) has no candidate above -inf
+ *   finished    [N][W] bytes, nullable: a beam with a non-zero byte only continues with
+ *               eos_token, its score unchanged
+ *   scores [N][k] fp32, parents and tokens [N][k] int32: outputs
+ * Sums and scores are 64-bit, rounded once to fp32.  A beam whose logits hold a NaN or +inf, or
+ * nothing but -inf, has no candidate above -inf.  Candidates at -inf rank by index.
+ * 1 <= k <= 32, k <= W * V, W * V < 2^31.  The parents are what pa_alloc_beam_select takes
+ * (k == W).  Workspace as pa_beam_topk_workspace_size, 256-byte aligned, no initialisation;
+ * not shared by calls that may overlap. */
+size_t pa_beam_topk_workspace_size(int N, int W, int V, int k);
+pa_status pa_beam_topk(float* scores, int32_t* parents, int32_t* tokens, const void* logits,
+                       const float* cum_scores, const uint8_t* finished, int eos_token, int N, int W,
+                       int V, int k, int64_t row_stride, pa_dtype dtype, void* workspace,
+                       size_t workspace_bytes, pa_stream_t stream);
+
+/* dst[n][i] = src[n][parents[n][i]] for rows of row_bytes bytes (dst [N][k], src [N][W]): the
+ * reordering of per-beam states that are not in the paged cache.  dst and src must not overlap.
+ * A parent outside [0, W) raises PA_DEVERR_BAD_PARENT and leaves its row as it was. */
+pa_status pa_beam_gather(void* dst, const void* src, const int32_t* parents, int N, int W, int k,
+                         int64_t row_bytes, int32_t* dev_err_flag, pa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Host block allocator (opaque, library-owned; destroy with pa_alloc_destroy)

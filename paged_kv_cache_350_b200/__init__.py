@@ -20,6 +20,10 @@ _BINDING_NAMES = {
     "pa_decode_append",
     "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_size",
     "pa_reshape_and_cache", "pa_status_from_device_flag", "lib",
+    "PA_ROPE_HALF", "PA_ROPE_INTERLEAVED", "PA_ROPE_SCALE_NONE", "PA_ROPE_SCALE_LINEAR",
+    "PA_ROPE_SCALE_BASE", "PA_ROPE_SCALE_RAMP", "PA_ROPE_SCALE_BANDS", "pa_rope_frequencies",
+    "pa_rope_and_cache", "pa_attention", "pa_attention_workspace_size", "pa_beam_topk",
+    "pa_beam_topk_workspace_size", "pa_beam_gather",
 }
 
 __all__ = sorted(_BINDING_NAMES | {"PagedKVCache"})

@@ -32,6 +32,7 @@ PA_ERR_BAD_SLOT = 9
 PA_ERR_TIMEOUT = 10
 PA_ERR_SCRATCH_LIMIT = 11
 PA_ERR_HOST_MEMORY = 12
+PA_ERR_BAD_PARENT = 13
 
 # pa_dtype
 PA_F32 = 0
@@ -47,6 +48,7 @@ PA_DEVERR_BAD_BLOCK_ID = 0x1
 PA_DEVERR_BAD_SEQ_LEN = 0x2
 PA_DEVERR_BAD_SLOT = 0x4
 PA_DEVERR_TIMEOUT = 0x8
+PA_DEVERR_BAD_PARENT = 0x10
 
 
 class PAError(RuntimeError):
@@ -62,6 +64,17 @@ PA_KERNEL_GENERIC = 1
 PA_KERNEL_TC_PARTITION = 2
 PA_KERNEL_TC_STREAM = 3
 
+# pa_rope_layout
+PA_ROPE_HALF = 0
+PA_ROPE_INTERLEAVED = 1
+
+# pa_rope_scaling
+PA_ROPE_SCALE_NONE = 0
+PA_ROPE_SCALE_LINEAR = 1
+PA_ROPE_SCALE_BASE = 2
+PA_ROPE_SCALE_RAMP = 3
+PA_ROPE_SCALE_BANDS = 4
+
 
 class pa_decode_opts(ctypes.Structure):
     _fields_ = [("partition_tokens", ctypes.c_int), ("path", ctypes.c_int),
@@ -71,6 +84,12 @@ class pa_decode_opts(ctypes.Structure):
 class pa_decode_plan_info(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int), ("partition_tokens", ctypes.c_int),
                 ("max_parts", ctypes.c_int), ("grid", ctypes.c_int), ("launches", ctypes.c_int)]
+
+
+class pa_attention_mods(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int),
+                ("alibi_slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+                ("first_keys", ctypes.c_void_p)]
 
 
 class pa_pipeline_desc(ctypes.Structure):
@@ -121,6 +140,19 @@ def _load():
         "pa_selftest_bounded_wait": (i32, [vp, ctypes.c_uint, vp]),
         "pa_reshape_and_cache": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]),
         "pa_copy_blocks": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]),
+        "pa_rope_frequencies": (i32, [i32, ctypes.c_double, i32, ctypes.c_double, i32,
+                                      ctypes.c_double, ctypes.c_double,
+                                      ctypes.POINTER(ctypes.c_double), ctypes.POINTER(f32)]),
+        "pa_rope_and_cache": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+                                    i32, i64, i64, i64, i32, i32, f32, i32, vp, vp]),
+        "pa_attention_workspace_size": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
+        "pa_attention": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32,
+                               i32, i64, f32, ctypes.POINTER(pa_attention_mods), i32, vp, sz, vp,
+                               vp]),
+        "pa_beam_topk_workspace_size": (sz, [i32, i32, i32, i32]),
+        "pa_beam_topk": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i64, i32, vp, sz,
+                               vp]),
+        "pa_beam_gather": (i32, [vp, vp, vp, i32, i32, i32, i64, vp, vp]),
         "pa_alloc_create": (i32, [i32, i32, ctypes.c_uint64, ctypes.POINTER(vp)]),
         "pa_alloc_create_ordered": (i32, [i32, i32, pi32, ctypes.POINTER(vp)]),
         "pa_alloc_destroy": (None, [vp]),
@@ -164,7 +196,9 @@ EXPORTED = (
     "pa_status_string", "pa_status_from_device_flag", "pa_version", "pa_decode_workspace_size",
     "pa_decode", "pa_decode_ex", "pa_decode_append", "pa_decode_plan", "pa_decode_no_alloc",
     "pa_decode_shared_prefix_workspace_size", "pa_decode_shared_prefix", "pa_alloc_prefix_groups",
-    "pa_reshape_and_cache", "pa_copy_blocks", "pa_selftest_bounded_wait", "pa_alloc_create",
+    "pa_reshape_and_cache", "pa_copy_blocks", "pa_rope_frequencies", "pa_rope_and_cache",
+    "pa_attention_workspace_size", "pa_attention", "pa_beam_topk_workspace_size", "pa_beam_topk",
+    "pa_beam_gather", "pa_selftest_bounded_wait", "pa_alloc_create",
     "pa_alloc_create_ordered", "pa_alloc_destroy", "pa_alloc_add_seq", "pa_alloc_fork",
     "pa_alloc_append_slot", "pa_alloc_append_slots", "pa_alloc_free_seq", "pa_alloc_truncate",
     "pa_alloc_beam_select", "pa_alloc_block_table",
@@ -437,6 +471,152 @@ def pa_copy_blocks(k_pool, v_pool, pairs, err_flag=None, stream=None):
     st = lib.pa_copy_blocks(_ptr(k_pool), _ptr(v_pool), _ptr(pairs), n, bs, Hkv, D, NB,
                             _dtype_of(k_pool), _ptr(err_flag), _stream(stream))
     _check(st, "pa_copy_blocks")
+
+
+# ---------------------------------------------------------------------------
+# rotary positions, attention of ragged query tokens, beam selection
+# ---------------------------------------------------------------------------
+
+def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=PA_ROPE_SCALE_NONE, factor=1.0,
+                        original_len=0, fast=32.0, slow=1.0):
+    """(inv_freq float64 [rotary_dim / 2] numpy, attn_factor) for pa_rope_and_cache."""
+    out = np.empty(max(int(rotary_dim), 2) // 2, np.float64)
+    f = ctypes.c_float()
+    _check(lib.pa_rope_frequencies(int(rotary_dim), float(base), scaling, float(factor),
+                                   int(original_len), float(fast), float(slow),
+                                   out.ctypes.data_as(ctypes.POINTER(ctypes.c_double)),
+                                   ctypes.byref(f)), "pa_rope_frequencies")
+    return out, f.value
+
+
+def _token_rows(t, name):
+    """Elements between the tokens of [T, H, D] rows whose heads lie side by side."""
+    _need(t.dim() == 3, f"{name} must be [T, heads, D]")
+    T, H, D = t.shape
+    _need((t.stride(2) == 1 or D == 1) and (t.stride(1) == D or H == 1),
+          f"{name}: the heads of a token must be contiguous")
+    # (the stride of a single token is arbitrary)
+    _need(T <= 1 or t.stride(0) >= H * D, f"{name}: tokens must not overlap")
+    return t.stride(0) if T > 1 else H * D
+
+
+def pa_rope_and_cache(q_out, q, k, v, k_pool, v_pool, positions, slot_mapping, inv_freq,
+                      layout=PA_ROPE_HALF, attn_factor=1.0, err_flag=None, stream=None):
+    """Rotate q [T,Hq,D] into q_out and k [T,Hkv,D] into its slots, v unchanged into its own
+    (see include/pa.h); the rotated part of a head is 2 * inv_freq.numel() elements."""
+    import torch
+    _need(k_pool.dim() == 4 and v_pool.shape == k_pool.shape, "pools must be [NB, bs, Hkv, D]")
+    NB, bs, Hkv, D = k_pool.shape
+    strides = [_token_rows(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    T, Hq = q.shape[:2]
+    _need(q.shape[2] == D and k.shape == (T, Hkv, D) and v.shape == k.shape, "q/k/v shape mismatch")
+    _need(q_out.shape == q.shape, "q_out must have q's shape")
+    _need(positions.dtype == torch.int32 and positions.numel() == T, "positions int32 [T]")
+    _need(slot_mapping.dtype == torch.int64 and slot_mapping.numel() == T, "slot_mapping int64 [T]")
+    _need(inv_freq.dtype == torch.float64 and inv_freq.dim() == 1, "inv_freq float64 [rotary_dim / 2]")
+    _need(q.dtype == k.dtype == v.dtype == q_out.dtype == k_pool.dtype == v_pool.dtype,
+          "q, k, v, q_out and pools share a dtype")
+    for t in (q_out, k_pool, v_pool, positions, slot_mapping, inv_freq):
+        _need(t.is_contiguous(), "q_out, pools and index tensors must be contiguous")
+    _on_device(q_out, q, k, v, k_pool, v_pool, positions, slot_mapping, inv_freq, err_flag=err_flag)
+    st = lib.pa_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool),
+                               _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq), T, Hq, Hkv, D,
+                               bs, NB, *strides, 2 * inv_freq.numel(), layout, float(attn_factor),
+                               _dtype_of(q), _ptr(err_flag), _stream(stream))
+    _check(st, "pa_rope_and_cache")
+
+
+def pa_attention_workspace_size(T, B, max_query_len, Hq, Hkv, D, block_size, max_blocks):
+    n = lib.pa_attention_workspace_size(T, B, max_query_len, Hq, Hkv, D, block_size, max_blocks)
+    if n == ctypes.c_size_t(-1).value:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_attention_workspace_size")
+    return n
+
+
+def pa_attention(out, q, k_pool, v_pool, block_tables, seq_lens, query_starts, max_query_len, scale,
+                 softcap=0.0, alibi_slopes=None, window=0, prefix_lens=None, first_keys=None,
+                 workspace=None, err_flag=None, stream=None):
+    """out[T,Hq,D] = attention of q's ragged query tokens over the paged cache (see
+    include/pa.h): sequence b's tokens are rows query_starts[b] .. query_starts[b + 1] - 1."""
+    import torch
+    stride = _token_rows(q, "q")
+    _need(out.shape == q.shape, "out must have q's shape")
+    _need(k_pool.dim() == 4 and v_pool.shape == k_pool.shape, "pools must be [NB, bs, Hkv, D]")
+    _need(block_tables.dim() == 2 and block_tables.dtype == torch.int32, "block_tables int32 [B, MB]")
+    T, Hq, D = q.shape
+    NB, bs, Hkv, D2 = k_pool.shape
+    B = block_tables.shape[0]
+    _need(D2 == D, "head dim mismatch")
+    _need(seq_lens.dtype == torch.int32 and seq_lens.numel() == B, "seq_lens int32 [B]")
+    _need(query_starts.dtype == torch.int32 and query_starts.numel() == B + 1, "query_starts int32 [B + 1]")
+    for t, n, dt, name in ((alibi_slopes, Hq, torch.float32, "alibi_slopes float32 [Hq]"),
+                           (prefix_lens, B, torch.int32, "prefix_lens int32 [B]"),
+                           (first_keys, T, torch.int32, "first_keys int32 [T]")):
+        _need(t is None or (t.dtype == dt and t.numel() == n and t.is_contiguous()), name)
+    for t in (out, k_pool, v_pool, block_tables, seq_lens, query_starts):
+        _need(t.is_contiguous(), "out, pools and index tensors must be contiguous")
+    _need(q.dtype == out.dtype == k_pool.dtype == v_pool.dtype, "q, out and pools share a dtype")
+    _on_device(out, q, k_pool, v_pool, block_tables, seq_lens, query_starts, alibi_slopes, prefix_lens,
+               first_keys, workspace, err_flag=err_flag)
+    mods = pa_attention_mods(float(softcap), int(window), *(t.data_ptr() if t is not None else None
+                                                            for t in (alibi_slopes, prefix_lens, first_keys)))
+    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = lib.pa_attention(_ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables),
+                          _ptr(seq_lens), _ptr(query_starts), T, B, int(max_query_len), Hq, Hkv, D, bs,
+                          block_tables.shape[1], NB, stride, float(scale), ctypes.byref(mods),
+                          _dtype_of(q), _ptr(workspace), wbytes, _ptr(err_flag), _stream(stream))
+    _check(st, "pa_attention")
+    return out
+
+
+def pa_beam_topk_workspace_size(N, W, V, k):
+    n = lib.pa_beam_topk_workspace_size(N, W, V, k)
+    if n == ctypes.c_size_t(-1).value:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_beam_topk_workspace_size")
+    return n
+
+
+def pa_beam_topk(scores, parents, tokens, logits, cum_scores, finished=None, eos_token=0,
+                 workspace=None, stream=None):
+    """The k best candidates of every request (scores, parents, tokens: [N, k]) from logits
+    [N, W, V] and the beams' scores so far [N, W] (see include/pa.h)."""
+    import torch
+    _need(logits.dim() == 3, "logits must be [N, W, V]")
+    N, W, V = logits.shape
+    _need((logits.stride(2) == 1 or V == 1) and (N <= 1 or W <= 1 or logits.stride(0) == W * logits.stride(1)),
+          "logits: rows contiguous, at one stride")
+    row = logits.stride(1) if W > 1 else (logits.stride(0) if N > 1 else V)
+    _need(scores.dim() == 2 and scores.shape[0] == N and scores.dtype == torch.float32, "scores float32 [N, k]")
+    for t, name in ((parents, "parents"), (tokens, "tokens")):
+        _need(t.shape == scores.shape and t.dtype == torch.int32, f"{name} int32 [N, k]")
+    _need(cum_scores.dtype == torch.float32 and cum_scores.shape == (N, W), "cum_scores float32 [N, W]")
+    _need(finished is None or (finished.dtype in (torch.bool, torch.uint8) and finished.shape == (N, W)),
+          "finished bool or uint8 [N, W]")
+    for t in (scores, parents, tokens, cum_scores, finished):
+        _need(t is None or t.is_contiguous(), "tensors must be contiguous")
+    _on_device(scores, parents, tokens, logits, cum_scores, finished, workspace)
+    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = lib.pa_beam_topk(_ptr(scores), _ptr(parents), _ptr(tokens), _ptr(logits), _ptr(cum_scores),
+                          _ptr(finished), int(eos_token), N, W, V, scores.shape[1], row,
+                          _dtype_of(logits), _ptr(workspace), wbytes, _stream(stream))
+    _check(st, "pa_beam_topk")
+
+
+def pa_beam_gather(dst, src, parents, err_flag=None, stream=None):
+    """dst[n][i] = src[n][parents[n][i]]: per-beam states [N, W, ...] in the order of parents [N, k]."""
+    import torch
+    _need(parents.dim() == 2 and parents.dtype == torch.int32, "parents int32 [N, k]")
+    N, k = parents.shape
+    _need(src.dim() >= 2 and src.shape[0] == N, "src must be [N, W, ...]")
+    _need(dst.dtype == src.dtype and tuple(dst.shape) == (N, k, *src.shape[2:]), "dst must be [N, k, ...]")
+    for t in (dst, src, parents):
+        _need(t.is_contiguous(), "tensors must be contiguous")
+    _on_device(dst, src, parents, err_flag=err_flag)
+    row = src[0, 0].numel() * src.element_size() if src.numel() else 0
+    st = lib.pa_beam_gather(_ptr(dst), _ptr(src), _ptr(parents), N, max(src.shape[1], 1), max(k, 1) if row else 1,
+                            row if k else 0, _ptr(err_flag), _stream(stream))
+    _check(st, "pa_beam_gather")
+    return dst
 
 
 def pa_selftest_bounded_wait(err_flag, limit_us, stream=None):

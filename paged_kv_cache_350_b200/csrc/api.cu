@@ -63,6 +63,7 @@ const char* pa_status_string(pa_status s) {
     case PA_ERR_TIMEOUT: return "a bounded device wait expired";
     case PA_ERR_SCRATCH_LIMIT: return "shape needs more scratch than the static no-alloc buffer";
     case PA_ERR_HOST_MEMORY: return "out of host memory";
+    case PA_ERR_BAD_PARENT: return "beam parent outside [0, W)";
   }
   return "unknown status";
 }
@@ -73,6 +74,7 @@ pa_status pa_status_from_device_flag(int32_t flag) {
   if (flag & PA_DEVERR_BAD_SEQ_LEN) return PA_ERR_BAD_SEQ_LEN;
   if (flag & PA_DEVERR_BAD_SLOT) return PA_ERR_BAD_SLOT;
   if (flag & PA_DEVERR_TIMEOUT) return PA_ERR_TIMEOUT;
+  if (flag & PA_DEVERR_BAD_PARENT) return PA_ERR_BAD_PARENT;
   return PA_ERR_INVALID_ARG;
 }
 

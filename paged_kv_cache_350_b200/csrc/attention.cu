@@ -1,0 +1,528 @@
+// Attention of ragged query tokens over the paged cache (sm_100a): the work plan, the CUDA-core
+// kernel and the join of units that are cut between CTAs.
+//
+// For query token i of a sequence of L cached tokens with n query tokens, at position
+// p = L - n + i, and head h:
+//   x_j = scale * q.k_j;  c * tanh(x_j / c) with a cap c;  x_j - slope_h |p - j| with a bias;
+//   out = softmax over the visible j of x_j, times v_j;  0 where nothing is visible.
+// The visible keys of a token are one interval [lo, hi) (attention.h), so a mask is two numbers
+// per row, and tiles of keys outside an item's interval are never read.
+//
+// Work plan.  An item is RT consecutive rows ((token, head of the group) pairs) of a sequence;
+// with one KV head it is a unit of nt = tiles of KT keys that its rows may see.  All units lie
+// end to end (item, then KV head, then tile) and every CTA of one wave takes an equal contiguous
+// range, whatever mixture of lengths and masks the batch is: a long axis with few rows is split
+// and a short one is not by the same rule.  A unit cut by a range's end leaves partials (max,
+// sum, unnormalised output; base 2) that attention_join_kernel merges by log-sum-exp.
+//
+// CUDA-core kernel: fp32 inputs (no TF32), bf16 with blocks of 4 tokens.  A CTA holds a tile
+// of RT rows of Q, and K and V tiles of 64 keys as fp32 in shared memory; a thread computes MR x 4
+// scores and MR x D/16 outputs in registers.  With 16 rows or fewer per sequence and KV head
+// (single tokens) the 16-row variant reads the cache at the same rate with a quarter of the
+// arithmetic.
+
+#include <cuda_bf16.h>
+#include <limits.h>
+
+#include "attention.h"
+
+namespace pa {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kPlanThreads = 1024;
+
+// ---- plan --------------------------------------------------------------------------------
+
+// Exclusive scan over the CTA's threads; returns the total too.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(kFull, incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int w = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
+    int s = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(kFull, s, off);
+      if (lane >= off) s += o;
+    }
+    warp_sums[lane] = s - w;
+    if (lane == 31) warp_sums[32] = s;
+  }
+  __syncthreads();
+  const int r = warp_sums[warp] + incl - v;
+  total = warp_sums[32];
+  __syncthreads();
+  return r;
+}
+
+// Query tokens of sequence b: [q0, q0 + n); none where the span is malformed or longer than
+// the caller said.
+__device__ __forceinline__ int query_span(const AttnParams& p, int b, bool flag, int& q0) {
+  const int s0 = __ldg(p.query_starts + b), s1 = __ldg(p.query_starts + b + 1);
+  const bool bad = s0 < 0 || s1 < s0 || s1 > p.T || s1 - s0 > p.max_query_len;
+  if (bad && flag) flag_error(p.err, PA_DEVERR_BAD_SEQ_LEN);
+  q0 = s0;
+  return bad ? 0 : s1 - s0;
+}
+
+// One CTA.  Sequences' item counts are scanned, then each item's interval and tile count,
+// then the tile counts; last, where each CTA of the main kernel begins.
+__global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const AttnParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ int sums[33];
+  int items = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    int n = 0, q0;
+    if (b < p.B) n = (static_cast<int64_t>(query_span(p, b, true, q0)) * p.G + p.RT - 1) / p.RT;
+    int total;
+    const int at = block_scan(n, sums, total);
+    if (b < p.B) p.seq_items[b] = items + at;
+    items += total;
+  }
+  // overlapping spans (malformed) could exceed the host's bound
+  if (items > p.max_items) {
+    if (threadIdx.x == 0) flag_error(p.err, PA_DEVERR_BAD_SEQ_LEN);
+    items = p.max_items;
+  }
+  __syncthreads();
+  int tiles = 0;
+  for (int i0 = 0; i0 < items; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    int nt = 0;
+    if (i < items) {
+      int a = 0, z = p.B;  // the last sequence whose items begin at or before i
+      while (z - a > 1) {
+        const int mid = (a + z) >> 1;
+        if (p.seq_items[mid] <= i) a = mid; else z = mid;
+      }
+      AttnItem it;
+      it.b = a;
+      const int n = query_span(p, a, false, it.q0);
+      const int nrows = n * p.G;
+      it.row0 = (i - p.seq_items[a]) * p.RT;
+      it.rows = min(p.RT, nrows - it.row0);
+      it.L = attn_len(p, a, true);
+      it.pos0 = it.L - n;
+      const int pre = p.prefix_lens ? __ldg(p.prefix_lens + a) : 0;
+      const int t0 = it.row0 / p.G, t1 = (it.row0 + it.rows - 1) / p.G;
+      int lo = INT_MAX, hi = 0;
+      // without first_keys the ends of the interval are monotone in the token
+      const int step = p.first_keys ? 1 : max(1, t1 - t0);
+      for (int t = t0; t <= t1; t += step) {
+        int l, h;
+        attn_visible(p, it.pos0 + t, it.L, pre, p.first_keys ? __ldg(p.first_keys + it.q0 + t) : 0, l, h);
+        if (l < h) {
+          lo = min(lo, l);
+          hi = max(hi, h);
+        }
+      }
+      // (the first token of the item may see nothing where the last does: its own start then)
+      it.lo = hi > 0 ? lo : 0;
+      if (hi > 0 && !p.first_keys && it.pos0 + t0 < 0) it.lo = 0;
+      it.hi = hi;
+      p.items[i] = it;
+      nt = hi > 0 ? (hi - 1) / p.KT - it.lo / p.KT + 1 : 0;
+    }
+    int total;
+    const int at = block_scan(nt, sums, total);
+    if (i < items) p.tile_sum[i] = tiles + at;
+    tiles += total;
+  }
+  if (threadIdx.x == 0) {
+    p.tile_sum[items] = tiles;
+    p.header[0] = items;
+    p.header[1] = tiles;
+  }
+  __syncthreads();
+  const int64_t T = static_cast<int64_t>(tiles) * p.Hkv;
+  const int64_t per = (T + p.ctas - 1) / p.ctas;
+  for (int s = threadIdx.x; s < p.ctas; s += kPlanThreads) {
+    const int64_t beg = min(T, s * per), end = min(T, beg + per);
+    AttnStart st{0, 0, 0, static_cast<int>(end - beg)};
+    if (beg < end) {
+      const int v = static_cast<int>(beg / p.Hkv);
+      int a = 0, z = items;  // the last item whose tiles begin at or before v (and has some)
+      while (z - a > 1) {
+        const int mid = (a + z) >> 1;
+        if (p.tile_sum[mid] <= v) a = mid; else z = mid;
+      }
+      const int nt = p.tile_sum[a + 1] - p.tile_sum[a];
+      const int off = static_cast<int>(beg - static_cast<int64_t>(p.tile_sum[a]) * p.Hkv);
+      st.item = a;
+      st.kvh = off / nt;
+      st.tile = off - st.kvh * nt;
+    }
+    p.starts[s] = st;
+  }
+}
+
+// ---- CUDA-core kernel -----------------------------------------------------------------------
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+constexpr int kGenKT = 64;
+constexpr int kGenThreads = 256;
+
+template <int D, int MR>
+struct GenCfg {
+  static constexpr int RT = 16 * MR;
+  static constexpr int KS = D + 4;       // row stride of Q and K: 16 rows fall on 16 bank groups
+  static constexpr int PS = kGenKT + 4;  // row stride of P
+  static constexpr int SMEM = (RT * KS + kGenKT * KS + kGenKT * D + RT * PS) * 4;
+};
+
+template <typename T, int D, int MR>
+__global__ void __launch_bounds__(kGenThreads) attention_generic_kernel(const AttnParams p) {
+  using C = GenCfg<D, MR>;
+  constexpr int RT = C::RT, KS = C::KS, PS = C::PS, NC = D / 64;  // NC float4 of output per row
+  // the join may launch; it waits for this grid to complete
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  extern __shared__ float smem_f[];
+  float* Qs = smem_f;
+  float* Ks = Qs + RT * KS;
+  float* Vs = Ks + kGenKT * KS;
+  float* Ps = Vs + kGenKT * D;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int s = blockIdx.x;
+  const int items = p.header[0];
+  const int64_t tiles = static_cast<int64_t>(p.header[1]) * p.Hkv;
+  const int64_t per = (tiles + p.ctas - 1) / p.ctas;
+  const AttnStart st = p.starts[s];
+  T* out = static_cast<T*>(p.out);
+  const T* q = static_cast<const T*>(p.q);
+  const T* kp = static_cast<const T*>(p.k_pool);
+  const T* vp = static_cast<const T*>(p.v_pool);
+
+  // items whose rows see nothing have no tile: their rows are zero
+  for (int i = s; i < items; i += p.ctas) {
+    if (p.tile_sum[i + 1] != p.tile_sum[i]) continue;
+    const AttnItem it = p.items[i];
+    const int n4 = it.rows * D / 4;
+    for (int h = 0; h < p.Hkv; ++h)
+      for (int e = tid; e < n4; e += kGenThreads) {
+        const int r = it.row0 + e / (D / 4);
+        store4(out + (static_cast<int64_t>(it.q0 + r / p.G) * p.Hq + h * p.G + r % p.G) * D + e % (D / 4) * 4,
+               make_float4(0.f, 0.f, 0.f, 0.f));
+      }
+  }
+
+  int own_item = -1, own_kvh = 0, own_slot = 0, own_n = 0;
+  int left = st.count, item = st.item, kvh = st.kvh, tile = st.tile;
+  bool first_piece = true;
+  while (left > 0) {
+    const AttnItem it = p.items[item];
+    const int nt = p.tile_sum[item + 1] - p.tile_sum[item];
+    if (nt == 0) {
+      ++item;
+      continue;
+    }
+    const int cnt = min(left, nt - tile);
+    const int pre = p.prefix_lens ? __ldg(p.prefix_lens + it.b) : 0;
+    __syncthreads();  // the last piece's reads of Q are done
+    for (int e = tid; e < RT * (D / 4); e += kGenThreads) {
+      const int r = e / (D / 4), c = e % (D / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < it.rows) {
+        const int f = it.row0 + r;
+        v = load4(q + static_cast<int64_t>(it.q0 + f / p.G) * p.q_stride +
+                  static_cast<int64_t>(kvh * p.G + f % p.G) * D + c);
+      }
+      *reinterpret_cast<float4*>(Qs + r * KS + c) = v;
+    }
+    // this thread's rows
+    int lo[MR], hi[MR], pos[MR];
+    float slope[MR], m[MR], l[MR];
+    float4 acc[MR][NC];
+#pragma unroll
+    for (int i = 0; i < MR; ++i) {
+      const int r = ty * MR + i, f = it.row0 + min(r, it.rows - 1);
+      const int t = f / p.G;
+      pos[i] = it.pos0 + t;
+      attn_visible(p, pos[i], it.L, pre, p.first_keys ? __ldg(p.first_keys + it.q0 + t) : 0, lo[i], hi[i]);
+      slope[i] = p.slopes ? __ldg(p.slopes + kvh * p.G + f % p.G) * kLog2e : 0.f;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const int32_t* tab = p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks;
+    const int kt0 = it.lo / kGenKT;
+    for (int j = 0; j < cnt; ++j) {
+      const int k0 = (kt0 + tile + j) * kGenKT;
+      __syncthreads();  // the tile before is consumed (and Q is written)
+      for (int e = tid; e < kGenKT * (D / 4); e += kGenThreads) {
+        const int r = e / (D / 4), c = e % (D / 4) * 4;
+        const int key = k0 + r;
+        float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+        if (key >= it.lo && key < it.hi) {
+          int phys = __ldg(tab + key / p.block_size);
+          if (phys < 0 || phys >= p.num_blocks) {
+            flag_error(p.err, PA_DEVERR_BAD_BLOCK_ID);
+            phys = 0;
+          }
+          const int64_t at = ((static_cast<int64_t>(phys) * p.block_size + key % p.block_size) * p.Hkv + kvh) * D + c;
+          kv = load4(kp + at);
+          vv = load4(vp + at);
+        }
+        *reinterpret_cast<float4*>(Ks + r * KS + c) = kv;
+        *reinterpret_cast<float4*>(Vs + r * D + c) = vv;
+      }
+      __syncthreads();
+      // scores of rows ty*MR + i and keys tx + 16 * u
+      float x[MR][4];
+#pragma unroll
+      for (int i = 0; i < MR; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[i][u] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 a[MR], b[4];
+#pragma unroll
+        for (int i = 0; i < MR; ++i) a[i] = *reinterpret_cast<const float4*>(Qs + (ty * MR + i) * KS + d);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) b[u] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * u) * KS + d);
+#pragma unroll
+        for (int i = 0; i < MR; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            x[i][u] = fmaf(a[i].x, b[u].x, x[i][u]);
+            x[i][u] = fmaf(a[i].y, b[u].y, x[i][u]);
+            x[i][u] = fmaf(a[i].z, b[u].z, x[i][u]);
+            x[i][u] = fmaf(a[i].w, b[u].w, x[i][u]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < MR; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int key = k0 + tx + 16 * u;
+          float y = p.cap_out > 0.f ? p.cap_out * tanhf(x[i][u] * p.cap_in) : x[i][u] * p.scale_log2;
+          y -= slope[i] * fabsf(static_cast<float>(pos[i] - key));
+          x[i][u] = key >= lo[i] && key < hi[i] ? y : -INFINITY;
+          mx = fmaxf(mx, x[i][u]);
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+        const float mn = fmaxf(m[i], mx);
+        const float ref = mn == -INFINITY ? 0.f : mn;  // no key yet: every p is 0
+        const float alpha = exp2f(m[i] - ref);
+        m[i] = mn;
+        l[i] *= alpha;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float e = exp2f(x[i][u] - ref);
+          l[i] += e;
+          Ps[(ty * MR + i) * PS + tx + 16 * u] = e;
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          acc[i][c].x *= alpha;
+          acc[i][c].y *= alpha;
+          acc[i][c].z *= alpha;
+          acc[i][c].w *= alpha;
+        }
+      }
+      __syncwarp();  // a row's P is written and read by one half-warp
+#pragma unroll 2
+      for (int k = 0; k < kGenKT; k += 4) {
+        float4 a[MR];
+#pragma unroll
+        for (int i = 0; i < MR; ++i) a[i] = *reinterpret_cast<const float4*>(Ps + (ty * MR + i) * PS + k);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float4 v = *reinterpret_cast<const float4*>(Vs + (k + kk) * D + c * 64 + tx * 4);
+#pragma unroll
+            for (int i = 0; i < MR; ++i) {
+              const float w = kk == 0 ? a[i].x : kk == 1 ? a[i].y : kk == 2 ? a[i].z : a[i].w;
+              acc[i][c].x = fmaf(w, v.x, acc[i][c].x);
+              acc[i][c].y = fmaf(w, v.y, acc[i][c].y);
+              acc[i][c].z = fmaf(w, v.z, acc[i][c].z);
+              acc[i][c].w = fmaf(w, v.w, acc[i][c].w);
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MR; ++i)
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) l[i] += __shfl_xor_sync(kFull, l[i], off);
+    const bool whole = tile == 0 && cnt == nt;
+    const int slot = first_piece ? 0 : 1;
+#pragma unroll
+    for (int i = 0; i < MR; ++i) {
+      const int r = ty * MR + i;
+      if (r >= it.rows) continue;
+      if (whole) {
+        const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);  // NaN stays
+        const int f = it.row0 + r;
+        T* o = out + (static_cast<int64_t>(it.q0 + f / p.G) * p.Hq + kvh * p.G + f % p.G) * D;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          store4(o + c * 64 + tx * 4, make_float4(acc[i][c].x * inv, acc[i][c].y * inv, acc[i][c].z * inv,
+                                                  acc[i][c].w * inv));
+      } else {
+        const int64_t base = static_cast<int64_t>(s) * 2 + slot;
+        if (tx == 0) reinterpret_cast<float2*>(p.part_ml)[base * RT + r] = make_float2(m[i], l[i]);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          reinterpret_cast<float4*>(p.part_acc)[(base * (D / 4) + c * 16 + tx) * RT + r] = acc[i][c];
+      }
+    }
+    if (!whole && tile == 0) {  // the unit begins here: its pieces follow in the next CTAs
+      own_item = item;
+      own_kvh = kvh;
+      own_slot = slot;
+      const int64_t ubeg = static_cast<int64_t>(p.tile_sum[item]) * p.Hkv + static_cast<int64_t>(kvh) * nt;
+      own_n = static_cast<int>((ubeg + nt - 1) / per) - s + 1;
+    }
+    left -= cnt;
+    first_piece = false;
+    tile = 0;
+    if (++kvh == p.Hkv) {
+      kvh = 0;
+      ++item;
+    }
+  }
+  if (tid == 0) reinterpret_cast<int4*>(p.cuts)[s] = make_int4(own_item, own_kvh, own_slot, own_n);
+}
+
+// ---- join -----------------------------------------------------------------------------------
+
+// Merge the pieces of the unit that begins in CTA s and continues in the next ones: piece 0 in
+// the slot that CTA recorded, the others in slot 0.  32 rows per block (lanes), warps over the
+// columns; partials lie [D/4][RT] so that a warp reads 512 consecutive bytes.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attention_join_kernel(const AttnParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int s = blockIdx.x;
+  const int4 cut = reinterpret_cast<const int4*>(p.cuts)[s];
+  if (cut.x < 0) return;
+  const AttnItem it = p.items[cut.x];
+  const int RT = p.RT;
+  const int r = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+  if (r >= it.rows) return;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  const float4* acc = reinterpret_cast<const float4*>(p.part_acc);
+  auto base = [&](int i) { return static_cast<int64_t>(s + i) * 2 + (i == 0 ? cut.z : 0); };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int i = 0; i < cut.w; ++i) M = fmaxf(M, ml[base(i) * RT + r].x);
+  const float ref = M == -INFINITY ? 0.f : M;
+  constexpr int NC = D / 4 / 8;
+  float4 a[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < cut.w; ++i) {
+    const float2 v = ml[base(i) * RT + r];
+    const float w = exp2f(v.x - ref);
+    l += v.y * w;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const float4 o = acc[(base(i) * (D / 4) + warp + 8 * c) * RT + r];
+      a[c].x = fmaf(o.x, w, a[c].x);
+      a[c].y = fmaf(o.y, w, a[c].y);
+      a[c].z = fmaf(o.z, w, a[c].z);
+      a[c].w = fmaf(o.w, w, a[c].w);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const int f = it.row0 + r;
+  T* o = static_cast<T*>(p.out) +
+         (static_cast<int64_t>(it.q0 + f / p.G) * p.Hq + cut.y * p.G + f % p.G) * D;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    store4(o + (warp + 8 * c) * 4, make_float4(a[c].x * inv, a[c].y * inv, a[c].z * inv, a[c].w * inv));
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                   Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+template <typename T, int D, int MR>
+cudaError_t run_generic(const AttnParams& p, cudaStream_t stream) {
+  using C = GenCfg<D, MR>;
+  cudaError_t e = cudaFuncSetAttribute(attention_generic_kernel<T, D, MR>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch(attention_generic_kernel<T, D, MR>, dim3(static_cast<unsigned>(p.ctas)), kGenThreads, C::SMEM,
+                stream, p);
+}
+
+template <typename T>
+cudaError_t run_generic_t(const AttnParams& p, cudaStream_t stream) {
+  if (p.RT == 16) return p.D == 64 ? run_generic<T, 64, 1>(p, stream) : run_generic<T, 128, 1>(p, stream);
+  return p.D == 64 ? run_generic<T, 64, 4>(p, stream) : run_generic<T, 128, 4>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_plan(const AttnParams& p, cudaStream_t stream) {
+  return launch(attention_plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
+}
+
+cudaError_t launch_attention_generic(const AttnParams& p, pa_dtype dtype, cudaStream_t stream) {
+  return dtype == PA_BF16 ? run_generic_t<__nv_bfloat16>(p, stream) : run_generic_t<float>(p, stream);
+}
+
+cudaError_t launch_attention_join(const AttnParams& p, pa_dtype dtype, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.ctas), static_cast<unsigned>((p.RT + 31) / 32));
+  if (dtype == PA_BF16)
+    return p.D == 64 ? launch(attention_join_kernel<__nv_bfloat16, 64>, grid, 256, 0, stream, p)
+                     : launch(attention_join_kernel<__nv_bfloat16, 128>, grid, 256, 0, stream, p);
+  return p.D == 64 ? launch(attention_join_kernel<float, 64>, grid, 256, 0, stream, p)
+                   : launch(attention_join_kernel<float, 128>, grid, 256, 0, stream, p);
+}
+
+// By shared memory (228 KB per SM, 1 KB reserved per CTA), at most 4.
+int attention_generic_ctas_per_sm(int RT, int D) {
+  const int bytes = D == 64 ? (RT == 16 ? GenCfg<64, 1>::SMEM : GenCfg<64, 4>::SMEM)
+                            : (RT == 16 ? GenCfg<128, 1>::SMEM : GenCfg<128, 4>::SMEM);
+  const int n = 228 * 1024 / (bytes + 1024);
+  return n < 4 ? n : 4;
+}
+
+}  // namespace pa

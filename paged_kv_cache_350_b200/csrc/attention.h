@@ -1,0 +1,48 @@
+// Attention of ragged query tokens over the paged cache: the parameter block, the work plan
+// and the visibility rule that its kernels share (device code).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+// One item: RT consecutive rows of a sequence, for one KV head.  A row is a (query token, head
+// of the group) pair, numbered token * G + head, so a tile is full whatever G is.
+struct AttnItem {
+  int b, q0;         // sequence; its first query token (row of q and out)
+  int row0, rows;    // first row of the item within the sequence, rows
+  int L, pos0;       // cached tokens; position of the sequence's first query token (L - n)
+  int lo, hi;        // keys that any row may see: [lo, hi)
+};
+
+// The first piece of one CTA's range.
+struct AttnStart {
+  int item, kvh, tile, count;  // count: tiles of the whole range
+};
+
+__device__ __forceinline__ int attn_len(const AttnParams& p, int b, bool flag) {
+  const int L = __ldg(p.seq_lens + b);
+  const int most = p.max_blocks * p.block_size;
+  if (L < 0 || L > most) {
+    if (flag) flag_error(p.err, PA_DEVERR_BAD_SEQ_LEN);
+    return L < 0 ? 0 : most;
+  }
+  return L;
+}
+
+// Keys visible to the query token at position pos of a sequence of L tokens: [lo, hi) with
+//   key j visible iff j < L, (j <= pos or j < prefix), j > pos - window (if any), j >= first.
+// A position below 0 (more query tokens than cached ones) sees nothing.
+__device__ __forceinline__ void attn_visible(const AttnParams& p, int pos, int L, int prefix,
+                                             int first, int& lo, int& hi) {
+  hi = min(max(pos + 1, prefix), L);
+  lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  lo = max(lo, first);
+  if (pos < 0 || lo >= hi) lo = hi = 0;
+}
+
+}  // namespace pa

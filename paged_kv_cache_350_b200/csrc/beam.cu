@@ -1,0 +1,376 @@
+// Beam search's selection over beams and vocabulary, and the reordering of per-beam states
+// (sm_100a).
+//
+// A candidate (w, v) of request n scores cum[n][w] + x[n][w][v] - lse(x[n][w]); the best k of
+// the W * V candidates are wanted, in order of (score, then lowest w * V + v).  Within a beam
+// the order is that of the logits, so one pass over the logits keeps a running (max, sum of
+// exponentials) and the k largest logits, and the scores are formed for those alone.
+//
+// Bound by reading the logits once.  Row chunks go to one CTA each; a warp walks its part
+// of the chunk in 16-byte vectors and keeps the k best so far sorted across its lanes (lane i
+// holds the i-th).  A batch none of whose values reaches the k-th best costs one comparison of
+// its maximum, which the softmax needs anyway.  A second, small kernel joins the chunks of each
+// beam and then the beams of each request.
+//
+// lse and scores are 64-bit from the chunk sums on: the chosen indices compare scores of
+// different beams, which a 32-bit subtraction would round into ties.
+
+#include <cuda_bf16.h>
+#include <limits.h>
+#include <math_constants.h>
+
+#include <type_traits>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+
+// The k best (value, index) pairs, sorted over the lanes of a warp: lane i holds the i-th;
+// ranked by value, then by lower index.  Empty places hold (-inf, INT_MAX).
+template <typename F>
+struct TopList {
+  F v;
+  int idx;
+  F thr_v;    // the k-th entry
+  int thr_i;
+
+  __device__ __forceinline__ void init() {
+    v = thr_v = static_cast<F>(-CUDART_INF);
+    idx = thr_i = INT_MAX;
+  }
+  __device__ __forceinline__ static bool before(F a, int ia, F b, int ib) {
+    return a > b || (a == b && ia < ib);
+  }
+  // Insert one pair, the same in every lane.
+  __device__ __forceinline__ void insert(F nv, int ni, int k, int lane) {
+    const int pos = __popc(__ballot_sync(kFull, before(v, idx, nv, ni)));
+    const F pv = __shfl_up_sync(kFull, v, 1);
+    const int pi = __shfl_up_sync(kFull, idx, 1);
+    if (lane > pos) {
+      v = pv;
+      idx = pi;
+    } else if (lane == pos) {
+      v = nv;
+      idx = ni;
+    }
+    thr_v = __shfl_sync(kFull, v, k - 1);
+    thr_i = __shfl_sync(kFull, idx, k - 1);
+  }
+  // Offer one pair per lane (`have`: the lane has one).
+  __device__ __forceinline__ void offer(F nv, int ni, bool have, int k, int lane) {
+    unsigned m = __ballot_sync(kFull, have && before(nv, ni, thr_v, thr_i));
+    while (m) {
+      const int src = __ffs(m) - 1;
+      insert(__shfl_sync(kFull, nv, src), __shfl_sync(kFull, ni, src), k, lane);
+      m &= m - 1;
+      m &= __ballot_sync(kFull, have && before(nv, ni, thr_v, thr_i));
+    }
+  }
+};
+
+template <typename T>
+struct Load;
+template <>
+struct Load<float> {
+  static constexpr int N = 4;
+  __device__ static void vec(const float* p, float* x) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+    x[0] = a.x;
+    x[1] = a.y;
+    x[2] = a.z;
+    x[3] = a.w;
+  }
+  __device__ static float one(const float* p) { return __ldcs(p); }
+};
+template <>
+struct Load<__nv_bfloat16> {
+  static constexpr int N = 8;
+  __device__ static void vec(const __nv_bfloat16* p, float* x) {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16_lo(w[i]);
+      x[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+  __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+};
+
+// Running (max, sum of 2^((x - max) log2 e)) of one lane.  NaN and +inf in a row end in a
+// NaN sum, which marks the row as one without candidates.
+struct Sum {
+  float m = -INFINITY, s = 0.f;
+  __device__ __forceinline__ void raise(float mx) {
+    if (mx > m) {
+      s = m == -INFINITY ? s : s * exp2f((m - mx) * kLog2e);
+      m = mx;
+    }
+  }
+  __device__ __forceinline__ void add(float x) {
+    // the difference first: it is exact next to the maximum, where the sum's weight lies (a
+    // product with log2 e of each term would shift the whole sum by its rounding).  A lane that
+    // has seen nothing but -inf keeps the reference 0: 2^-inf = 0, NaN stays.
+    s += ex2_approx((x - (m == -INFINITY ? 0.f : m)) * kLog2e);
+  }
+};
+
+// One chunk of one row per CTA: blockIdx.x = row * chunks + chunk.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p) {
+  constexpr int N = VEC ? Load<T>::N : 1;
+  constexpr int U = VEC ? 32 / Load<T>::N / 2 : 4;  // vectors in flight per lane
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int beg = chunk * p.chunk_len, end = min(p.V, beg + p.chunk_len);
+  const T* x = static_cast<const T*>(p.logits) + static_cast<int64_t>(row) * p.row_stride;
+  const int k = p.k;
+
+  TopList<float> top;
+  top.init();
+  Sum sum;
+  // warps interleave: batch i of the chunk (32 * N * U values) goes to warp i % kWarps
+  constexpr int BATCH = 32 * N * U;
+  for (int b0 = beg + warp * BATCH; b0 < end; b0 += kWarps * BATCH) {
+    float e[U][N];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = b0 + (u * 32 + lane) * N;
+      if (VEC && at + N <= end) {
+        Load<T>::vec(x + at, e[u]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) e[u][j] = at + j < end ? Load<T>::one(x + at + j) : -INFINITY;
+      }
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < N; ++j) mx = fmaxf(mx, e[u][j]);
+    sum.raise(mx);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < N; ++j) sum.add(e[u][j]);
+    if (__any_sync(kFull, mx >= top.thr_v)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int at = b0 + (u * 32 + lane) * N + j;
+          top.offer(e[u][j], at, at < end, k, lane);
+        }
+    }
+  }
+
+  // join the lanes' sums, then the warps'
+  __shared__ float sm_m[kWarps];
+  __shared__ double sm_s[kWarps];
+  __shared__ float sm_v[kWarps][32];
+  __shared__ int sm_i[kWarps][32];
+  float m = sum.m;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+  double s = sum.s;
+  if (sum.m != -INFINITY) s *= exp2(static_cast<double>(sum.m - m) * 1.4426950408889634);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+  if (lane == 0) {
+    sm_m[warp] = m;
+    sm_s[warp] = s;
+  }
+  sm_v[warp][lane] = top.v;
+  sm_i[warp][lane] = top.idx;
+  __syncthreads();
+  if (warp != 0) return;
+  float M = -INFINITY;
+  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w]);
+  double S = 0.0;
+  for (int w = 0; w < kWarps; ++w)
+    S += sm_m[w] == -INFINITY ? sm_s[w]
+                              : sm_s[w] * exp2(static_cast<double>(sm_m[w] - M) * 1.4426950408889634);
+  for (int w = 1; w < kWarps; ++w)
+    top.offer(sm_v[w][lane], sm_i[w][lane], lane < k && sm_i[w][lane] != INT_MAX, k, lane);
+  const int64_t at = static_cast<int64_t>(blockIdx.x);
+  if (lane == 0) {
+    p.ws_max[at] = M;
+    p.ws_sum[at] = S;
+  }
+  if (lane < k) {
+    p.ws_val[at * k + lane] = top.v;
+    p.ws_idx[at * k + lane] = top.idx;
+  }
+}
+
+// One request per CTA.  Warp w joins the chunks of beams w, w + kWarps, ... and merges them
+// into its list by score; warp 0 joins the warps' lists.
+__global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int k = p.k;
+  TopList<double> best;
+  best.init();
+  for (int w = warp; w < p.W; w += kWarps) {
+    const int row = n * p.W + w;
+    const int64_t c0 = static_cast<int64_t>(row) * p.chunks;
+    const float cum = __ldg(p.cum + row);
+    const bool done = p.finished && __ldg(p.finished + row) != 0;
+    const int base = w * p.V;
+    if (!done) {
+      float m = -INFINITY;
+      for (int c = lane; c < p.chunks; c += 32) m = fmaxf(m, p.ws_max[c0 + c]);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+      double s = 0.0;
+      for (int c = lane; c < p.chunks; c += 32) {
+        const float mc = p.ws_max[c0 + c];
+        s += mc == -INFINITY ? p.ws_sum[c0 + c]
+                             : p.ws_sum[c0 + c] * exp2(static_cast<double>(mc - m) * 1.4426950408889634);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+      const double lse = static_cast<double>(m) + log(s);
+      if (isfinite(lse) && isfinite(cum)) {
+        TopList<float> top;
+        top.init();
+        for (int c = 0; c < p.chunks; ++c) {
+          const bool in = lane < k;
+          const float v = in ? p.ws_val[(c0 + c) * k + lane] : -INFINITY;
+          const int i = in ? p.ws_idx[(c0 + c) * k + lane] : INT_MAX;
+          top.offer(v, i, in && i != INT_MAX, k, lane);
+        }
+        best.offer(static_cast<double>(cum) + (static_cast<double>(top.v) - lse), base + top.idx,
+                   lane < k && top.idx != INT_MAX, k, lane);
+        continue;
+      }
+    }
+    // a beam without an ordinary candidate: finished (its score stays, at the end token), dead
+    // (score -inf) or with a sum that is not finite.  All its other candidates score -inf and
+    // rank by index.
+    if (done && isfinite(cum))
+      best.offer(static_cast<double>(cum), base + p.eos, lane == 0 && p.eos >= 0 && p.eos < p.V, k, lane);
+    const bool skip = done && isfinite(cum) && lane == p.eos;
+    // k + 1 of them: one may be the end token, ranked above already
+    best.offer(-CUDART_INF, base + lane, lane < p.V && !skip, k, lane);
+    if (done && k == 32) best.offer(-CUDART_INF, base + 32, lane == 0 && 32 < p.V && p.eos != 32, k, lane);
+  }
+  __shared__ double sm_v[kWarps][32];
+  __shared__ int sm_i[kWarps][32];
+  sm_v[warp][lane] = best.v;
+  sm_i[warp][lane] = best.idx;
+  __syncthreads();
+  if (warp != 0) return;
+  for (int w = 1; w < min(kWarps, p.W); ++w)
+    best.offer(sm_v[w][lane], sm_i[w][lane], lane < k && sm_i[w][lane] != INT_MAX, k, lane);
+  if (lane < k) {
+    const int64_t at = static_cast<int64_t>(n) * k + lane;
+    p.scores[at] = static_cast<float>(best.v);
+    p.parents[at] = best.idx / p.V;
+    p.tokens[at] = best.idx % p.V;
+  }
+}
+
+// dst[n][i] = src[n][parents[n][i]], rows of `row_bytes`; one CTA row per (n, i).
+template <typename V>
+__global__ void __launch_bounds__(kThreads) beam_gather_kernel(V* __restrict__ dst, const V* __restrict__ src,
+                                                               const int32_t* __restrict__ parents, int W, int k,
+                                                               int64_t vecs, int32_t* err) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t row = blockIdx.x;
+  const int par = __ldg(parents + row);
+  if (par < 0 || par >= W) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) flag_error(err, PA_DEVERR_BAD_PARENT);
+    return;
+  }
+  const V* s = src + (row / k * W + par) * vecs;
+  V* d = dst + row * vecs;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * kThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x; i < vecs; i += step) d[i] = s[i];
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+template <typename T>
+cudaError_t launch_rows(const BeamParams& p, cudaStream_t stream) {
+  const bool vec = p.row_stride % Load<T>::N == 0 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
+  const dim3 grid(static_cast<unsigned>(p.N * p.W * p.chunks));
+  return vec ? launch(beam_rows_kernel<T, true>, grid, stream, p)
+             : launch(beam_rows_kernel<T, false>, grid, stream, p);
+}
+
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+// Chunks per row: enough CTAs for four per SM, none below 2048 values (a shorter chunk is
+// all reduction); a multiple of 8 values, so that chunks start on vector boundaries.
+void beam_plan(BeamParams* p) {
+  const int64_t rows = static_cast<int64_t>(p->N) * p->W;
+  const int64_t want = (148 * 4 + rows - 1) / (rows > 0 ? rows : 1);
+  int64_t len = (p->V + want - 1) / want;
+  if (len < 2048) len = 2048;
+  len = (len + 7) / 8 * 8;
+  p->chunk_len = static_cast<int>(len < p->V ? len : (p->V + 7) / 8 * 8);
+  p->chunks = (p->V + p->chunk_len - 1) / p->chunk_len;
+}
+
+size_t beam_workspace_bytes(const BeamParams& p) {
+  const int64_t n = static_cast<int64_t>(p.N) * p.W * p.chunks;
+  return static_cast<size_t>(up256(n * 8) + up256(n * 4) + 2 * up256(n * p.k * 4));
+}
+
+cudaError_t launch_beam_topk(BeamParams p, pa_dtype dtype, void* workspace, cudaStream_t stream) {
+  const int64_t n = static_cast<int64_t>(p.N) * p.W * p.chunks;
+  char* ws = static_cast<char*>(workspace);
+  p.ws_sum = reinterpret_cast<double*>(ws);
+  p.ws_max = reinterpret_cast<float*>(ws + up256(n * 8));
+  p.ws_val = reinterpret_cast<float*>(ws + up256(n * 8) + up256(n * 4));
+  p.ws_idx = reinterpret_cast<int32_t*>(ws + up256(n * 8) + up256(n * 4) + up256(n * p.k * 4));
+  cudaError_t e = dtype == PA_BF16 ? launch_rows<__nv_bfloat16>(p, stream) : launch_rows<float>(p, stream);
+  if (e != cudaSuccess) return e;
+  return launch(beam_join_kernel, dim3(static_cast<unsigned>(p.N)), stream, p);
+}
+
+cudaError_t launch_beam_gather(void* dst, const void* src, const int32_t* parents, int N, int W, int k,
+                               int64_t row_bytes, int32_t* err, cudaStream_t stream) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(src) |
+                      static_cast<uintptr_t>(row_bytes);
+  auto go = [&](auto* type) {
+    using V = std::remove_pointer_t<decltype(type)>;
+    const int64_t vecs = row_bytes / static_cast<int64_t>(sizeof(V));
+    int64_t gy = (vecs + kThreads * 4 - 1) / (kThreads * 4);
+    if (gy > 64) gy = 64;
+    return launch(beam_gather_kernel<V>, dim3(static_cast<unsigned>(N * k), static_cast<unsigned>(gy)), stream,
+                  static_cast<V*>(dst), static_cast<const V*>(src), parents, W, k, vecs, err);
+  };
+  if (a % 16 == 0) return go(static_cast<uint4*>(nullptr));
+  if (a % 4 == 0) return go(static_cast<uint32_t*>(nullptr));
+  return go(static_cast<uint8_t*>(nullptr));
+}
+
+}  // namespace pa

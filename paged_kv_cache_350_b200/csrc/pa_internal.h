@@ -106,6 +106,79 @@ cudaError_t launch_copy_blocks(void* k_pool, void* v_pool, const int32_t* pairs,
                                int64_t block_bytes, int num_blocks, int32_t* err,
                                cudaStream_t stream);
 
+// Rotary positions with the cache write (rope.cu).
+struct RopeParams {
+  void* q_out;              // [T][Hq][D]
+  const void *q, *k, *v;    // [T] tokens of Hq / Hkv / Hkv heads, `*_stride` elements apart
+  void *k_pool, *v_pool;
+  const int32_t* positions; // [T]
+  const int64_t* slots;     // [T]
+  const double* inv_freq;   // [R / 2] radians per position
+  int64_t q_stride, k_stride, v_stride, num_slots;
+  int T, Hq, Hkv, D, R;
+  int half;                 // pairs (i, i + R/2), else (2i, 2i + 1)
+  float factor;
+  int32_t* err;
+};
+cudaError_t launch_rope(const RopeParams& p, pa_dtype dtype, cudaStream_t stream);
+
+// Attention of ragged query tokens (attention.cu, attention_tc.cu).
+struct AttnItem;
+struct AttnStart;
+struct AttnParams {
+  void* out;                    // [T][Hq][D]
+  const void* q;                // [T] tokens of Hq heads, q_stride elements apart
+  const void *k_pool, *v_pool;
+  const int32_t* block_tables;  // [B][max_blocks]
+  const int32_t* seq_lens;      // [B]
+  const int32_t* query_starts;  // [B + 1]
+  const int32_t* prefix_lens;   // [B], nullable
+  const int32_t* first_keys;    // [T], nullable
+  const float* slopes;          // [Hq], nullable
+  int64_t q_stride;
+  float scale_log2;             // scale * log2(e)
+  float cap_in, cap_out;        // with a cap: scale / cap and cap * log2(e); cap_out 0: none
+  int window;                   // 0: none
+  int T, B, max_query_len, Hq, Hkv, G, D, block_size, max_blocks, num_blocks;
+  int32_t* err;
+  // the plan (in the workspace): rows per item, keys per tile, CTAs of the main kernel
+  int RT, KT, ctas, max_items;
+  int32_t* header;              // [2]: items, tiles (of one KV head)
+  int32_t* seq_items;           // [B] items before the sequence
+  AttnItem* items;              // [max_items]
+  int32_t* tile_sum;            // [max_items + 1] tiles before the item
+  AttnStart* starts;            // [ctas]
+  int32_t* cuts;                // [ctas][4]: item, KV head, slot, pieces of the cut unit that
+                                // begins in the CTA (item -1: none)
+  float* part_ml;               // [ctas][2][RT][2]: (max, sum) of a cut unit's piece, base 2
+  float* part_acc;              // [ctas][2][D / 4][RT][4]: its unnormalised output
+};
+cudaError_t launch_attention_plan(const AttnParams& p, cudaStream_t stream);
+cudaError_t launch_attention_generic(const AttnParams& p, pa_dtype dtype, cudaStream_t stream);
+cudaError_t launch_attention_join(const AttnParams& p, pa_dtype dtype, cudaStream_t stream);
+int attention_generic_ctas_per_sm(int RT, int D);
+
+// Beam search's selection (beam.cu).
+struct BeamParams {
+  float* scores;            // [N][k]
+  int32_t *parents, *tokens;
+  const void* logits;       // [N * W] rows of V, row_stride elements apart
+  const float* cum;         // [N][W]
+  const uint8_t* finished;  // [N][W], nullable
+  int64_t row_stride;
+  int N, W, V, k, eos;
+  int chunks, chunk_len;    // beam_plan
+  double* ws_sum;           // [N * W * chunks]
+  float* ws_max;
+  float* ws_val;            // [N * W * chunks][k]
+  int32_t* ws_idx;
+};
+void beam_plan(BeamParams* p);
+size_t beam_workspace_bytes(const BeamParams& p);
+cudaError_t launch_beam_topk(BeamParams p, pa_dtype dtype, void* workspace, cudaStream_t stream);
+cudaError_t launch_beam_gather(void* dst, const void* src, const int32_t* parents, int N, int W, int k,
+                               int64_t row_bytes, int32_t* err, cudaStream_t stream);
+
 // Tensor-core path eligibility (shape/dtype only; alignment is checked by the caller).
 bool tc_eligible(int G, int D, int block_size, pa_dtype dtype);
 
