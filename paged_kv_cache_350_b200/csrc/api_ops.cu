@@ -28,16 +28,30 @@ int sm_count() {
   return sms;
 }
 
-// The plan of a pa_attention call on `sms` multiprocessors: rows per item, keys per tile, CTAs.
+// The plan of a pa_attention call on `sms` multiprocessors: rows per item (and per softmax
+// group), keys per tile, CTAs.
 struct AttnShape {
-  int RT, KT, ctas, max_items;
+  int RT, HR, KT, ctas, max_items;
 };
 
-AttnShape attention_shape(int T, int B, int max_query_len, int G, int D, int sms) {
+// The tensor-core kernel takes bf16, blocks of whole swizzle atoms (8 rows) and groups of at
+// most the 128 rows of its M tile.
+bool attention_on_tc(int G, int block_size, pa_dtype dtype) {
+  return dtype == PA_BF16 && block_size >= 8 && G <= 128;
+}
+
+AttnShape attention_shape(int T, int B, int max_query_len, int G, int D, bool tc, int sms) {
   AttnShape s;
-  s.KT = 64;
-  s.RT = static_cast<int64_t>(max_query_len) * G <= 16 ? 16 : 64;
-  s.ctas = sms * pa::attention_generic_ctas_per_sm(s.RT, D);
+  if (tc) {
+    s.KT = 128;
+    s.RT = pa::attention_tc_rows(max_query_len, G);
+    s.HR = s.RT > 32 ? s.RT / 2 : s.RT;
+    s.ctas = sms;
+  } else {
+    s.KT = 64;
+    s.RT = s.HR = static_cast<int64_t>(max_query_len) * G <= 16 ? 16 : 64;
+    s.ctas = sms * pa::attention_generic_ctas_per_sm(s.RT, D);
+  }
   s.max_items = static_cast<int>(static_cast<int64_t>(T) * G / s.RT + std::min(B, T));
   return s;
 }
@@ -58,6 +72,7 @@ size_t attention_carve(const AttnShape& s, int B, int D, char* ws, pa::AttnParam
   const int64_t acc = take(int64_t(s.ctas) * 2 * s.RT * D * 4);
   if (p) {
     p->RT = s.RT;
+    p->HR = s.HR;
     p->KT = s.KT;
     p->ctas = s.ctas;
     p->max_items = s.max_items;
@@ -179,7 +194,11 @@ size_t pa_attention_workspace_size(int T, int B, int max_query_len, int Hq, int 
     return static_cast<size_t>(-1);
   if (T == 0 || B == 0) return 0;
   const int sms = sm_count() > 0 ? sm_count() : kSmBound;
-  return attention_carve(attention_shape(T, B, max_query_len, Hq / Hkv, D, sms), B, D, nullptr, nullptr);
+  size_t n = 0;  // enough for either type
+  for (int tc = attention_on_tc(Hq / Hkv, block_size, PA_BF16); tc >= 0; --tc)
+    n = std::max(n, attention_carve(attention_shape(T, B, std::max(max_query_len, 1), Hq / Hkv, D, tc != 0, sms), B, D,
+                                    nullptr, nullptr));
+  return n;
 }
 
 pa_status pa_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
@@ -212,7 +231,8 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
   const int sms = sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
   const int G = Hq / Hkv;
-  const AttnShape sh = attention_shape(T, B, max_query_len, G, D, sms);
+  const bool tc = attention_on_tc(G, block_size, dtype);
+  const AttnShape sh = attention_shape(T, B, max_query_len, G, D, tc, sms);
   // tile counts of one KV head are summed in 32 bits
   if (static_cast<int64_t>(sh.max_items) * (max_seq / sh.KT + 2) >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
   pa::AttnParams p{};
@@ -246,7 +266,7 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
   p.err = dev_err_flag;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = pa::launch_attention_plan(p, s);
-  if (e == cudaSuccess) e = pa::launch_attention_generic(p, dtype, s);
+  if (e == cudaSuccess) e = tc ? pa::launch_attention_tc(p, s) : pa::launch_attention_generic(p, dtype, s);
   if (e == cudaSuccess) e = pa::launch_attention_join(p, dtype, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

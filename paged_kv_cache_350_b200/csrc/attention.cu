@@ -115,24 +115,43 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
       it.L = attn_len(p, a, true);
       it.pos0 = it.L - n;
       const int pre = p.prefix_lens ? __ldg(p.prefix_lens + a) : 0;
-      const int t0 = it.row0 / p.G, t1 = (it.row0 + it.rows - 1) / p.G;
-      int lo = INT_MAX, hi = 0;
-      // without first_keys the ends of the interval are monotone in the token
-      const int step = p.first_keys ? 1 : max(1, t1 - t0);
-      for (int t = t0; t <= t1; t += step) {
-        int l, h;
-        attn_visible(p, it.pos0 + t, it.L, pre, p.first_keys ? __ldg(p.first_keys + it.q0 + t) : 0, l, h);
-        if (l < h) {
-          lo = min(lo, l);
-          hi = max(hi, h);
+      it.lo = INT_MAX;
+      it.hi = 0;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int r0 = it.row0 + g * p.HR, r1 = min(r0 + p.HR, it.row0 + it.rows);
+        int lo = INT_MAX, hi = 0;
+        if (r0 < r1) {
+          const int t0 = r0 / p.G, t1 = (r1 - 1) / p.G;
+          auto take = [&](int t, int first) {
+            int l, h;
+            attn_visible(p, it.pos0 + t, it.L, pre, first, l, h);
+            if (l < h) {
+              lo = min(lo, l);
+              hi = max(hi, h);
+            }
+          };
+          if (p.first_keys) {
+            for (int t = t0; t <= t1; t += 8) {
+              int first[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) first[u] = __ldg(p.first_keys + it.q0 + min(t + u, t1));
+#pragma unroll
+              for (int u = 0; u < 8; ++u) take(min(t + u, t1), first[u]);
+            }
+          } else {  // both ends are monotone in the token (from position 0 on, which sees key 0)
+            take(max(t0, min(-it.pos0, t1)), 0);
+            take(t1, 0);
+          }
         }
+        it.glo[g] = hi > 0 ? lo : 0;
+        it.ghi[g] = hi;
+        it.lo = min(it.lo, lo);
+        it.hi = max(it.hi, hi);
       }
-      // (the first token of the item may see nothing where the last does: its own start then)
-      it.lo = hi > 0 ? lo : 0;
-      if (hi > 0 && !p.first_keys && it.pos0 + t0 < 0) it.lo = 0;
-      it.hi = hi;
+      if (it.hi == 0) it.lo = 0;
       p.items[i] = it;
-      nt = hi > 0 ? (hi - 1) / p.KT - it.lo / p.KT + 1 : 0;
+      nt = it.hi > 0 ? (it.hi - 1) / p.KT - it.lo / p.KT + 1 : 0;
     }
     int total;
     const int at = block_scan(nt, sums, total);

@@ -17,6 +17,7 @@ struct AttnItem {
   int row0, rows;    // first row of the item within the sequence, rows
   int L, pos0;       // cached tokens; position of the sequence's first query token (L - n)
   int lo, hi;        // keys that any row may see: [lo, hi)
+  int glo[2], ghi[2];  // the same of its rows [0, HR) and [HR, 2 HR)
 };
 
 // The first piece of one CTA's range.

@@ -1,0 +1,860 @@
+// Attention of ragged query tokens over the paged cache on the 5th-generation tensor cores
+// (sm_100a, bf16).  The formula, the masks and the work plan are attention.cu's; a CTA of one
+// wave walks its equal contiguous range of (item, KV head, tile of 128 keys).
+//
+// Two shapes of the same kernel:
+//   wide    an item is two M tiles of whole tokens, HR = floor(128 / G) * G rows each.  Softmax
+//           group g serves M tile g; both read the same K and V tiles, so a tile of 128 keys is
+//           loaded once for up to 256 rows.  Group g skips the tiles that none of its rows sees.
+//   narrow  at most 32 rows (single tokens, a few speculative ones).  Q lies four times in
+//           the M tile, at rows 0, 32, 64 and 96, and softmax warp w of a group takes its columns
+//           32w .. 32w + 31 of a tile: four warps share the tile's exponentials where one
+//           would do them all, and a lane's P is zero outside its warp's columns, so that its O is
+//           the part of those columns.  Groups take alternate tiles.  The eight parts of a row
+//           (2 groups x 4 warps) are merged once per piece.
+//
+// Warps: 0-7 softmax (group g = warps 4g .. 4g + 3, a thread per row), 8 MMA, 9 K/V loads, 10
+// schedule, 11 Q loads.  The schedule warp writes records of the CTA's pieces (a piece is the part
+// of a unit in the range) into a small ring that all others follow.  K and V tiles share a ring
+// of slots in load order (K0 V0 K1 V1 ..), one TMA box per block and 64-column chunk.
+//
+// Tensor memory: S_g at column 128 g, overwritten by its P (bf16 pairs, 64 columns); O_g at
+// column 256 + 128 g.  Products are issued by one thread and run in order, so S_g of the next tile
+// is issued right behind the P.V that reads P_g.  While group 0 works on its S, the products of
+// group 1 run and the other way round.
+//
+// P is rounded to bf16 (half a step, 2^-8 of each weight, as the output is); row sums, maxima and
+// O stay in 32 bits.  The reference maximum moves lazily, by more than 2^8 only.
+//
+// Every wait is bounded in time; on expiry the kernel records PA_DEVERR_TIMEOUT, every role
+// stops, loads and products in flight are drained (bounded) and the tensor memory is freed.
+
+#include <atomic>
+
+#include "attention.h"
+#include "tc05.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kKT = 128;        // keys per tile
+constexpr int kThreads = 384;
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10, kQWarp = 11;
+constexpr int kPieces = 4;      // records in flight
+constexpr int kMaxSlots = 10;
+constexpr int kMergeFloats = 32 * 17;  // rows x (columns + 1) of a merge step, one part
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t kColS = 0, kColO = 256, kGroupCols = 128, kTmemCols = 512;
+// released by the MMA warp, the two load warps and each softmax warp
+constexpr int kPieceUsers = 3 + kSoftWarps;
+
+template <int D_, int BS_, bool WIDE_>
+struct TcAttn {
+  static constexpr int D = D_, BS = BS_;
+  static constexpr bool WIDE = WIDE_;
+  static constexpr int MT = WIDE ? 2 : 1;             // M tiles of an item
+  static constexpr int DCH = D / 64;
+  static constexpr int CHUNK = kKT * 128;             // one 64-column chunk of 128 rows
+  static constexpr int SLOT = DCH * CHUNK;            // a K or V tile; an M tile of Q
+  // the narrow shape's merge: (max, sum) of each part, and kSoftWarps * kMergeFloats of O
+  static constexpr int MERGE = WIDE ? 0 : kSoftWarps * (32 * 8 + kMergeFloats * 4);
+  static constexpr int BUDGET = 227 * 1024 - 1024 - 1536;  // alignment, static shared memory
+  static constexpr int FIT = (BUDGET - MT * SLOT - MERGE) / SLOT;
+  static constexpr int NST = FIT < kMaxSlots ? FIT : kMaxSlots;
+  static constexpr int SMEM = 1024 + MT * SLOT + NST * SLOT + MERGE;
+  static_assert(NST >= 5, "K and V of two tiles and one more");
+  static_assert(SMEM > 114 * 1024, "one CTA per SM: it holds all of the SM's tensor memory");
+};
+
+// A piece: tiles [0, cnt) of it are tiles kt0 .. of the sequence's keys.
+struct Piece {
+  int cnt;             // 0: no more pieces
+  int kt0;
+  int step0;           // tiles of the CTA's range before the piece
+  int kvh;
+  int b, q0, row0, rows, pos0, L, lo, hi;
+  int ga[2], gb[2];    // group g's tiles (wide)
+  int whole, slot;     // the whole unit; else the slot of its partial
+};
+
+struct Shared {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t qfull, qempty;
+  uint64_t sfull[2], pfull[2], ofull[2];
+  uint64_t pc_full[kPieces], pc_empty[kPieces];
+  uint64_t merge_bar, drain_bar;
+  Piece pc[kPieces];
+  uint32_t tmem;
+  volatile int abort_flag;
+};
+
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// What a row of a piece sees and how its scores are biased.
+struct Row {
+  int lo, hi;      // visible keys
+  int pos;
+  float slope;     // times log2 e
+};
+
+__device__ __forceinline__ Row row_of(const AttnParams& p, const Piece& pc, int f) {
+  Row r;
+  const int t = f / p.G;
+  r.pos = pc.pos0 + t;
+  const int pre = p.prefix_lens ? __ldg(p.prefix_lens + pc.b) : 0;
+  attn_visible(p, r.pos, pc.L, pre, p.first_keys ? __ldg(p.first_keys + pc.q0 + t) : 0, r.lo, r.hi);
+  r.slope = p.slopes ? __ldg(p.slopes + pc.kvh * p.G + (f - t * p.G)) * kLog2e : 0.f;
+  return r;
+}
+
+// Turn N raw scores (keys key0 .. of one row) into log2-domain scores in place and return their
+// maximum.  The plain case keeps raw scores, so that the scale and the subtraction of the maximum
+// become one operation.
+template <int N>
+__device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& p, const Row& r, int key0,
+                                               bool plain, bool masked) {
+  const int a = r.lo - key0, b = r.hi - key0;
+  if (p.cap_out > 0.f) {
+    if (masked) {  // what lies in masked columns must not choose the branch below
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = j >= a && j < b ? x[j] : 0.f;
+    }
+    float ax = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) ax = fmaxf(ax, fmaxf(fabsf(x[j]), fabsf(x[j + 1])));
+    // (a NaN fails the comparison only if it is all there is; both ways carry it through)
+    if (__all_sync(kFull, ax * fabsf(p.cap_in) <= 1.f)) {
+      // tanh(t) / t as a polynomial in t^2 (iterated reweighted least squares on |t| <= 1, where
+      // |t P(t^2) - tanh t| < 2.4e-7): on the FMA pipe alone, the exponentials need the other
+      const float2 ci = splat(p.cap_in), co = splat(p.cap_out);
+#pragma unroll
+      for (int j = 0; j < N; j += 2) {
+        const float2 t = __fmul2_rn(make_float2(x[j], x[j + 1]), ci);
+        const float2 u = __fmul2_rn(t, t);
+        float2 y = __ffma2_rn(u, splat(-0.0028394642286f), splat(0.01611417718f));
+        y = __ffma2_rn(y, u, splat(-0.0509728603065f));
+        y = __ffma2_rn(y, u, splat(0.132535248995f));
+        y = __ffma2_rn(y, u, splat(-0.333240032196f));
+        y = __ffma2_rn(y, u, splat(0.999996840954f));
+        y = __fmul2_rn(y, __fmul2_rn(t, co));
+        x[j] = y.x;
+        x[j + 1] = y.y;
+      }
+    } else {
+      // tanh t = 1 - 2 / (1 + e^2t)
+      const float c2 = p.cap_in * (2.f * kLog2e), m2 = -2.f * p.cap_out;
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = fmaf(m2, rcp_approx(1.f + ex2_approx(x[j] * c2)), p.cap_out);
+    }
+  } else if (!plain) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] *= p.scale_log2;
+  }
+  if (p.slopes) {
+    const float d0 = static_cast<float>(r.pos - key0);
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = fmaf(-r.slope, fabsf(d0 - static_cast<float>(j)), x[j]);
+  }
+  if (masked) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = j >= a && j < b ? x[j] : -INFINITY;
+  }
+  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < N; j += 4) {
+    m0 = fmaxf(m0, fmaxf(x[j], x[j + 1]));
+    m1 = fmaxf(m1, fmaxf(x[j + 2], x[j + 3]));
+  }
+  return fmaxf(m0, m1);
+}
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                        const __grid_constant__ CUtensorMap tmq, const AttnParams p) {
+  constexpr int D = C::D, BS = C::BS, DCH = C::DCH, NST = C::NST;
+  constexpr bool WIDE = C::WIDE;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* ring = smem + C::MT * C::SLOT;
+  float2* part_ml = reinterpret_cast<float2*>(ring + NST * C::SLOT);  // [kSoftWarps][32]
+  float* merge = reinterpret_cast<float*>(part_ml + kSoftWarps * 32);
+  __shared__ __align__(16) Shared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int s = blockIdx.x;
+  const int HR = WIDE ? p.RT / 2 : p.RT;  // rows of an M tile
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(smem_addr(&sh.full[i]), 1);
+      mbar_init(smem_addr(&sh.empty[i]), 1);
+    }
+    mbar_init(smem_addr(&sh.qfull), 1);
+    mbar_init(smem_addr(&sh.qempty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh.sfull[i]), 1);
+      mbar_init(smem_addr(&sh.pfull[i]), 128);
+      mbar_init(smem_addr(&sh.ofull[i]), 1);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(smem_addr(&sh.pc_full[i]), 1);
+      mbar_init(smem_addr(&sh.pc_empty[i]), kPieceUsers);
+    }
+    mbar_init(smem_addr(&sh.merge_bar), kSoftWarps * 32);
+    mbar_init(smem_addr(&sh.drain_bar), 1);
+    sh.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  if (warp == kMmaWarp) tc05::alloc(smem_addr(&sh.tmem), kTmemCols);
+  // rows of the Q tiles that no load covers: finite scores for them (their P is never used)
+  for (int e = threadIdx.x; e < C::MT * DCH * 128 * 8; e += kThreads) {
+    const int row = (e >> 3) & 127;
+    if ((WIDE ? row : row & 31) >= HR) *reinterpret_cast<uint4*>(smem + e * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  if (threadIdx.x == kLoadWarp * 32) {
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+    prefetch_tensormap(&tmq);
+  }
+  // the join may launch; it waits for this grid to complete
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc05::fence_before_sync();
+  __syncthreads();
+  tc05::fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+  volatile int* abort_flag = &sh.abort_flag;
+  // nothing above reads global memory; the plan is written by the kernel before
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  auto piece_wait = [&](int n) {  // record n is there; false: give up
+    return wait_warp(smem_addr(&sh.pc_full[n % kPieces]), (n / kPieces) & 1, p.err, abort_flag);
+  };
+  auto piece_done = [&](int n) {  // this warp will not read record n again
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&sh.pc_empty[n % kPieces]));
+  };
+
+  if (warp >= kSoftWarps) {
+    setmaxnreg_dec<88>();
+    if (warp == kPlanWarp) {
+      // ============================ schedule ============================
+      if (lane == 0) {
+        const int64_t per =
+            (static_cast<int64_t>(p.header[1]) * p.Hkv + p.ctas - 1) / p.ctas;
+        const AttnStart st = p.starts[s];
+        int left = st.count, item = st.item, kvh = st.kvh, tile = st.tile, step = 0, n = 0;
+        int4 cut = make_int4(-1, 0, 0, 0);
+        AttnItem it{};
+        int sum = 0, nt = 0;
+        auto load_item = [&] {  // the item at or after `item` that has tiles
+          sum = p.tile_sum[item];
+          while ((nt = p.tile_sum[item + 1] - sum) == 0) ++item;
+          it = p.items[item];
+        };
+        if (left > 0) load_item();
+        for (;; ++n) {
+          const int slot = n % kPieces;
+          if (n >= kPieces && !wait_or_abort(smem_addr(&sh.pc_empty[slot]), (n / kPieces - 1) & 1, p.err, abort_flag))
+            break;
+          Piece* pc = &sh.pc[slot];
+          if (left <= 0) {
+            pc->cnt = 0;
+            mbar_arrive(smem_addr(&sh.pc_full[slot]));
+            break;
+          }
+          const int cnt = min(left, nt - tile);
+          const int first = it.lo / kKT + tile;
+          pc->cnt = cnt;
+          pc->kt0 = first;
+          pc->step0 = step;
+          pc->kvh = kvh;
+          pc->b = it.b;
+          pc->q0 = it.q0;
+          pc->row0 = it.row0;
+          pc->rows = it.rows;
+          pc->pos0 = it.pos0;
+          pc->L = it.L;
+          pc->lo = it.lo;
+          pc->hi = it.hi;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int a = it.glo[g] / kKT - first, z = (it.ghi[g] + kKT - 1) / kKT - first;
+            pc->ga[g] = it.ghi[g] > 0 ? max(a, 0) : 0;
+            pc->gb[g] = it.ghi[g] > 0 ? min(z, cnt) : 0;
+          }
+          pc->whole = tile == 0 && cnt == nt;
+          pc->slot = n == 0 ? 0 : 1;
+          mbar_arrive(smem_addr(&sh.pc_full[slot]));
+          if (tile == 0 && cnt != nt) {  // the unit begins here and goes on in the next CTAs
+            const int64_t ubeg = static_cast<int64_t>(sum) * p.Hkv + static_cast<int64_t>(kvh) * nt;
+            cut = make_int4(item, kvh, n == 0 ? 0 : 1, static_cast<int>((ubeg + nt - 1) / per) - s + 1);
+          }
+          left -= cnt;
+          step += cnt;
+          tile = 0;
+          if (++kvh == p.Hkv) {
+            kvh = 0;
+            ++item;
+            if (left > 0) load_item();
+          }
+        }
+        reinterpret_cast<int4*>(p.cuts)[s] = cut;
+      }
+    } else if (warp == kLoadWarp) {
+      // ============================ K and V tiles ============================
+      constexpr int BPT = kKT / BS;  // blocks per tile, at most 16
+      const uint64_t policy = WIDE ? l2_policy_evict_normal() : l2_policy_evict_first();
+      bool ok = true;
+      int64_t n = 0;  // loads issued
+      for (int i = 0; ok; ++i) {
+        if (!(ok = piece_wait(i))) break;
+        const Piece& pc = sh.pc[i % kPieces];
+        const int cnt = pc.cnt;
+        if (cnt == 0) break;
+        const int kt0 = pc.kt0, lo = pc.lo, hi = pc.hi, kvh = pc.kvh;
+        const int32_t* tab = p.block_tables + static_cast<int64_t>(pc.b) * p.max_blocks;
+        piece_done(i);
+        // this lane's block of a tile; ids are read one tile ahead
+        auto live_at = [&](int j) {
+          const int k = (kt0 + j) * kKT + lane * BS;
+          return lane < BPT && j < cnt && k < hi && k + BS > lo;
+        };
+        auto id_at = [&](int j) { return live_at(j) ? __ldg(tab + (kt0 + j) * BPT + lane) : 0; };
+        int next = id_at(0);
+        for (int j = 0; j < cnt; ++j) {
+          int phys = next;
+          const bool live = live_at(j);
+          next = id_at(j + 1);
+          if (phys < 0 || phys >= p.num_blocks) {
+            flag_error(p.err, PA_DEVERR_BAD_BLOCK_ID);
+            phys = 0;
+          }
+          const uint32_t bytes = __popc(__ballot_sync(kFull, live)) * BS * D * 2;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const int slot = static_cast<int>(n % NST);
+            if (n >= NST &&
+                !(ok = wait_warp(smem_addr(&sh.empty[slot]), static_cast<uint32_t>(n / NST - 1) & 1, p.err, abort_flag)))
+              break;
+            const uint32_t bar = smem_addr(&sh.full[slot]);
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            __syncwarp();
+            if (live) {
+              const uint32_t dst = smem_addr(ring + slot * C::SLOT) + lane * BS * 128;
+#pragma unroll
+              for (int c = 0; c < DCH; ++c)
+                tma_load_4d(dst + c * C::CHUNK, kv ? &tmv : &tmk, c * 64, kvh, 0, phys, bar, policy);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
+      }
+      if (!ok)  // loads issued but perhaps never waited for
+        for (int64_t k = n > NST ? n - NST : 0; k < n; ++k)
+          mbar_wait(smem_addr(&sh.full[k % NST]), static_cast<uint32_t>(k / NST) & 1, nullptr);
+    } else if (warp == kQWarp) {
+      // ============================ Q tiles ============================
+      const uint64_t policy = l2_policy_evict_normal();
+      const int ht = HR / p.G;  // tokens of an M tile
+      const uint32_t box = static_cast<uint32_t>(HR) * 128;
+      bool ok = true;
+      int i = 0;
+      for (;; ++i) {
+        if (!(ok = piece_wait(i))) break;
+        const Piece& pc = sh.pc[i % kPieces];
+        if (pc.cnt == 0) break;
+        const int rows = pc.rows, kvh = pc.kvh, tok = pc.q0 + pc.row0 / p.G;
+        piece_done(i);
+        if (i > 0 && !(ok = wait_warp(smem_addr(&sh.qempty), (i - 1) & 1, p.err, abort_flag))) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_addr(&sh.qfull), q = smem_addr(smem);
+          const int tiles = WIDE ? (rows > HR ? 2 : 1) : 4;
+          mbar_arrive_expect_tx(bar, box * DCH * tiles);
+          for (int m = 0; m < tiles; ++m)
+#pragma unroll
+            for (int c = 0; c < DCH; ++c)
+              tma_load_3d(q + (WIDE ? m * C::SLOT : m * 4096) + c * C::CHUNK, &tmq, c * 64, kvh * p.G,
+                          tok + (WIDE ? m * ht : 0), bar, policy);
+        }
+        __syncwarp();
+      }
+      if (!ok && i > 0) mbar_wait(smem_addr(&sh.qfull), (i - 1) & 1, nullptr);
+    } else {
+      // ============================ products ============================
+      constexpr uint32_t id_s = tc05::instr_desc_bf16(128, kKT, 0);
+      constexpr uint32_t id_pv = tc05::instr_desc_bf16(128, D, 1);
+      // A cursor over the sub-steps: tile by tile, and for the wide shape group 0 then group 1.
+      struct Cursor {
+        int n = 0, j = 0, g = 0;  // piece, tile, group
+        int cnt = 0, step0 = 0;   // of that piece
+      };
+      Cursor sc, pv;
+      bool s_end = false, pv_end = false, ok = true;
+      int s_done[2] = {0, 0}, pv_done[2] = {0, 0};  // sub-steps issued per group
+      auto ready = [&](uint32_t bar, uint32_t parity) {  // lane 0's view, for the whole warp
+        return __shfl_sync(kFull, static_cast<int>(mbar_test_wait(bar, parity)), 0) != 0;
+      };
+      // the piece of a cursor at its start: false when nothing (more) can be done
+      auto enter = [&](Cursor& c) {
+        const Piece& pc = sh.pc[c.n % kPieces];
+        c.cnt = pc.cnt;
+        c.step0 = pc.step0;
+        c.j = 0;
+        c.g = WIDE ? 0 : pc.step0 & 1;
+      };
+      auto group_active = [&](const Cursor& c) {
+        if (!WIDE) return true;
+        const Piece& pc = sh.pc[c.n % kPieces];
+        return c.j >= pc.ga[c.g] && c.j < pc.gb[c.g];
+      };
+      auto advance = [&](Cursor& c) {  // true: the tile is finished
+        if (WIDE) {
+          c.g ^= 1;
+          if (c.g) return false;
+        } else {
+          c.g ^= 1;
+        }
+        ++c.j;
+        return true;
+      };
+      if ((ok = piece_wait(0))) {
+        enter(sc);
+        pv = sc;
+        s_end = pv_end = sc.cnt == 0;
+      }
+      bool s_wait = true;    // the cursor's tile has not been waited for yet
+      bool s_enter = false;  // its piece has not been entered yet
+      while (ok && !pv_end) {
+        if (s_enter && ready(smem_addr(&sh.pc_full[sc.n % kPieces]), (sc.n / kPieces) & 1)) {
+          enter(sc);
+          s_end = sc.cnt == 0;
+          s_enter = false;
+        }
+        // ---- S of the next sub-step, as soon as its group's P has been read ----
+        const bool behind = !s_enter && !s_end && sc.n == pv.n && sc.j == pv.j && sc.g == pv.g;
+        if (!s_end && !s_enter && s_done[sc.g] == pv_done[sc.g]) {
+          const bool must = behind;  // nothing else to do
+          const int64_t load = 2 * (static_cast<int64_t>(sc.step0) + sc.j);
+          const int slot = static_cast<int>(load % NST);
+          const uint32_t kb = smem_addr(&sh.full[slot]), kpar = static_cast<uint32_t>(load / NST) & 1;
+          const uint32_t qb = smem_addr(&sh.qfull), qpar = sc.n & 1;
+          if (!s_wait || must || (ready(kb, kpar) && ready(qb, qpar))) {
+            if (s_wait) {
+              if (!(ok = wait_warp(qb, qpar, p.err, abort_flag) && wait_warp(kb, kpar, p.err, abort_flag))) break;
+              s_wait = false;
+            }
+            const int g = sc.g;
+            const bool act = group_active(sc);
+            if (act && lane == 0) {
+              tc05::fence_after_sync();
+              const uint64_t dq = tc05::smem_desc(smem_addr(smem + (WIDE ? g * C::SLOT : 0)), 16, 1024);
+              const uint64_t dk = tc05::smem_desc(smem_addr(ring + slot * C::SLOT), 16, 1024);
+              const uint32_t ts = tmem + kColS + g * kGroupCols;
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * C::CHUNK + (k & 3) * 32;
+                tc05::mma_ss(ts, dq + (off >> 4), dk + (off >> 4), id_s, k > 0);
+              }
+              tc05::commit(smem_addr(&sh.sfull[g]));
+            }
+            if (act) ++s_done[g];
+            if (advance(sc)) {
+              if (lane == 0) tc05::commit(smem_addr(&sh.empty[slot]));
+              s_wait = true;
+              if (sc.j == sc.cnt) {
+                if (lane == 0) tc05::commit(smem_addr(&sh.qempty));
+                ++sc.n;
+                s_enter = true;
+              }
+            }
+            continue;
+          }
+        }
+        // ---- P.V of the sub-step at the other cursor ----
+        const Piece& pc = sh.pc[pv.n % kPieces];
+        const int g = pv.g;
+        const int64_t load = 2 * (static_cast<int64_t>(pv.step0) + pv.j) + 1;
+        const int slot = static_cast<int>(load % NST);
+        if (s_enter && pv.n == sc.n) continue;  // the record is there: pv has waited for it
+        if (behind) {  // (its S was issued above: the two cursors agree on what is pending)
+          flag_error(p.err, PA_DEVERR_TIMEOUT);
+          ok = false;
+          break;
+        }
+        const bool first_sub = !WIDE || g == 0;
+        if (first_sub) {
+          if (!(ok = wait_warp(smem_addr(&sh.full[slot]), static_cast<uint32_t>(load / NST) & 1, p.err, abort_flag)))
+            break;
+          // V rows outside the item's keys may hold anything (0 * Inf is NaN): zero those that
+          // the product reads, up to the 16-key steps
+          const int k0 = (pc.kt0 + pv.j) * kKT;
+          const int a = max(pc.lo - k0, 0), z = min(pc.hi - k0, kKT);
+          const int na = a & 15, nz = -z & 15;
+          if (na + nz > 0) {
+            uint8_t* v = ring + slot * C::SLOT;
+            for (int e = lane; e < (na + nz) * DCH * 8; e += 32) {
+              const int r = e / (DCH * 8), q = e % (DCH * 8);
+              const int row = r < na ? a - na + r : z + r - na;
+              *reinterpret_cast<uint4*>(v + (q >> 3) * C::CHUNK + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (group_active(pv)) {
+          if (!(ok = wait_warp(smem_addr(&sh.pfull[g]), pv_done[g] & 1, p.err, abort_flag))) break;
+          if (lane == 0) {
+            tc05::fence_after_sync();
+            const int k0 = (pc.kt0 + pv.j) * kKT;
+            const int s0 = max(pc.lo - k0, 0) >> 4, s1 = (min(pc.hi - k0, kKT) + 15) >> 4;
+            const uint64_t dv = tc05::smem_desc(smem_addr(ring + slot * C::SLOT), C::CHUNK, 1024);
+            const uint32_t tp = tmem + kColS + g * kGroupCols, to = tmem + kColO + g * kGroupCols;
+            // the group's first tile of the piece overwrites O
+            const bool fresh = WIDE ? pv.j == pc.ga[g] : pv.j < 2;
+#pragma unroll
+            for (int k = 0; k < kKT / 16; ++k)
+              if (k >= s0 && k < s1) tc05::mma_ts(to, tp + 8 * k, dv + (k * 2048 >> 4), id_pv, !(fresh && k == s0));
+            if (WIDE ? pv.j == pc.gb[g] - 1 : pv.j + 2 >= pv.cnt) tc05::commit(smem_addr(&sh.ofull[g]));
+          }
+          ++pv_done[g];
+        }
+        if (advance(pv)) {
+          if (lane == 0) tc05::commit(smem_addr(&sh.empty[slot]));
+          if (pv.j == pv.cnt) {
+            piece_done(pv.n);
+            ++pv.n;
+            if (!(ok = piece_wait(pv.n))) break;
+            enter(pv);
+            pv_end = pv.cnt == 0;
+          }
+        }
+      }
+      if (!ok) *abort_flag = 1;
+      // every product issued has completed before the memory is freed
+      if (lane == 0) {
+        tc05::commit(smem_addr(&sh.drain_bar));
+        mbar_wait(smem_addr(&sh.drain_bar), 0, p.err);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ============================ softmax ============================
+    setmaxnreg_inc<208>();
+    const int g = warp >> 2, w = warp & 3;
+    const uint32_t lane_addr = static_cast<uint32_t>(32 * w) << 16;
+    const uint32_t ts = tmem + kColS + g * kGroupCols + lane_addr;
+    const uint32_t to = tmem + kColO + g * kGroupCols + lane_addr;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+    const bool plain = p.cap_out == 0.f && !p.slopes && p.scale_log2 > 0.f;
+    const float mul = plain ? p.scale_log2 : 1.f;
+    const int r = WIDE ? 32 * w + lane : lane;  // row of the M tile
+
+    // items whose rows see nothing have no tile: their rows are zero
+    const int items = p.header[0];
+    for (int i0 = 0; s + i0 * p.ctas < items; i0 += kSoftWarps * 32) {
+      const int64_t mine = s + static_cast<int64_t>(i0 + threadIdx.x) * p.ctas;
+      unsigned empty = __ballot_sync(kFull, mine < items && p.tile_sum[mine + 1] == p.tile_sum[mine]);
+      while (empty) {
+        const int i = s + (i0 + 32 * warp + __ffs(empty) - 1) * p.ctas;
+        empty &= empty - 1;
+        const int rows = p.items[i].rows, row0 = p.items[i].row0, q0 = p.items[i].q0;
+        for (int h = 0; h < p.Hkv; ++h)
+          for (int e = lane; e < rows * (D / 8); e += 32) {
+            const int f = row0 + e / (D / 8);
+            *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(q0 + f / p.G) * p.Hq + h * p.G + f % p.G) * D +
+                                      e % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+          }
+      }
+    }
+
+    int done = 0, pieces = 0, merges = 0;  // phases of sfull, ofull and merge_bar
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      if (!(ok = piece_wait(i))) break;
+      const Piece& pc = sh.pc[i % kPieces];
+      const int cnt = pc.cnt;
+      if (cnt == 0) break;
+      const int rows = min(HR, pc.rows - (WIDE ? g * HR : 0));  // of this M tile
+      const int f = pc.row0 + (WIDE ? g * HR : 0) + min(r, max(rows, 1) - 1);
+      Row row{0, 0, 0, 0.f};
+      if (rows > 0) row = row_of(p, pc, f);
+      int ja = 0, jb = cnt, jstep = 1;
+      if (WIDE) {
+        ja = pc.ga[g];
+        jb = pc.gb[g];
+      } else {
+        ja = (pc.step0 & 1) == g ? 0 : 1;
+        jstep = 2;
+      }
+      const bool active = ja < jb;
+      int all_lo = row.lo, all_hi = row.hi;  // keys that every row of the warp sees
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        all_lo = max(all_lo, __shfl_xor_sync(kFull, all_lo, off));
+        all_hi = min(all_hi, __shfl_xor_sync(kFull, all_hi, off));
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = ja; j < jb; j += jstep, ++done) {
+        if (!(ok = wait_warp(smem_addr(&sh.sfull[g]), done & 1, p.err, abort_flag))) break;
+        tc05::fence_after_sync();
+        constexpr int N = WIDE ? kKT : 32;  // this thread's columns
+        const int key0 = (pc.kt0 + j) * kKT + (WIDE ? 0 : 32 * w);
+        if (WIDE && 32 * w >= rows) {  // none of the warp's rows is a row of the item
+          tc05::fence_before_sync();
+          mbar_arrive(smem_addr(&sh.pfull[g]));
+          continue;
+        }
+        uint32_t raw[N / 32][32];
+#pragma unroll
+        for (int c = 0; c < N / 32; ++c) tc05::ld32(ts + (WIDE ? 32 * c : 32 * w), raw[c]);
+        tc05::wait_ld();
+        float x[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = __uint_as_float(raw[e / 32][e % 32]);
+        const bool masked = key0 < all_lo || key0 + N > all_hi;
+        const float mt = modify_scores(x, p, row, key0, plain, masked) * mul;
+        const bool raise = mt > m_ref + kRescaleLog2;
+        // (earlier P.V of the group are complete: S was issued behind them)
+        if (__any_sync(kFull, raise)) {
+          const float alpha = raise ? ex2_approx(m_ref - mt) : 1.f;
+          if (j > ja) {
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t v[32];
+              tc05::ld32(to + c, v);
+              tc05::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tc05::st32(to + c, v);
+            }
+          }
+          l *= alpha;
+          if (raise) m_ref = mt;
+        }
+        const float ref = m_ref == -INFINITY ? 0.f : -m_ref;
+        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+        const float2 mul2 = splat(mul), ref2 = splat(ref);
+#pragma unroll
+        for (int c = 0; c < N; c += 32) {
+          uint32_t v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 y = __ffma2_rn(make_float2(x[c + 2 * e], x[c + 2 * e + 1]), mul2, ref2);
+            y.x = ex2_approx(y.x);
+            y.y = ex2_approx(y.y);
+            if (e & 1) l1 = __fadd2_rn(l1, y); else l0 = __fadd2_rn(l0, y);
+            v[e] = pack_bf16x2(y.x, y.y);
+          }
+          tc05::st16(ts + (WIDE ? c / 2 : 16 * w), v);
+        }
+        if (!WIDE) {  // zero outside this warp's columns
+          uint32_t v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = 0u;
+#pragma unroll
+          for (int c = 1; c < 4; ++c) tc05::st16(ts + 16 * ((w + c) & 3), v);
+        }
+        l += (l0.x + l0.y) + (l1.x + l1.y);
+        tc05::wait_st();
+        tc05::fence_before_sync();
+        mbar_arrive(smem_addr(&sh.pfull[g]));
+      }
+      if (!ok) break;
+
+      // ---- the piece's output, or its partial ----
+      const bool whole = pc.whole;
+      const int64_t base = static_cast<int64_t>(s) * 2 + pc.slot;
+      if (active) {
+        if (!(ok = wait_warp(smem_addr(&sh.ofull[g]), pieces & 1, p.err, abort_flag))) break;
+        ++pieces;
+        tc05::fence_after_sync();
+      }
+      if constexpr (WIDE) {
+        if (rows > 0) {
+          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
+          const int t = f / p.G;
+          __nv_bfloat16* o =
+              out + (static_cast<int64_t>(pc.q0 + t) * p.Hq + pc.kvh * p.G + (f - t * p.G)) * D;
+          const int pr = g * HR + r;  // row of the partial
+          if (!whole && r < rows) reinterpret_cast<float2*>(p.part_ml)[base * p.RT + pr] = make_float2(m_ref, l);
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t v[32];
+            if (active) {
+              tc05::ld32(to + c, v);
+              tc05::wait_ld();
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = 0u;
+            }
+            if (r < rows) {
+              if (whole) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                  auto at = [&](int u) { return __uint_as_float(v[e + u]) * inv; };
+                  *reinterpret_cast<uint4*>(o + c + e) =
+                      make_uint4(pack_bf16x2(at(0), at(1)), pack_bf16x2(at(2), at(3)), pack_bf16x2(at(4), at(5)),
+                                 pack_bf16x2(at(6), at(7)));
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  reinterpret_cast<float4*>(p.part_acc)[(base * (D / 4) + (c + e) / 4) * p.RT + pr] =
+                      make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]),
+                                  __uint_as_float(v[e + 3]));
+              }
+            }
+            __syncwarp();
+          }
+        }
+        tc05::fence_before_sync();  // the reads of O come before the next piece's products
+      } else {
+        // merge the eight parts of each row by log-sum-exp, CC columns of O at a time
+        auto sync = [&] {
+          mbar_arrive(smem_addr(&sh.merge_bar));
+          return wait_warp(smem_addr(&sh.merge_bar), merges++ & 1, p.err, abort_flag);
+        };
+        part_ml[warp * 32 + lane] = make_float2(m_ref, l);
+        if (!(ok = sync())) break;
+        float M = -INFINITY, l_all = 0.f;
+#pragma unroll
+        for (int k = 0; k < kSoftWarps; ++k) M = fmaxf(M, part_ml[k * 32 + lane].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int k = 0; k < kSoftWarps; ++k)
+          l_all += part_ml[k * 32 + lane].y * ex2_approx(part_ml[k * 32 + lane].x - ref);
+        const float e_own = ex2_approx(m_ref - ref);
+        const float inv = l_all > 0.f ? 1.f / l_all : (l_all == 0.f ? 0.f : l_all);  // NaN stays
+        const float k_own = whole ? e_own * inv : e_own;
+        if (!whole && warp == 0 && lane < rows)
+          reinterpret_cast<float2*>(p.part_ml)[base * p.RT + lane] = make_float2(M, l_all);
+        const int CC = min(D, HR <= 4 ? 128 : HR <= 8 ? 64 : HR <= 16 ? 32 : 16);  // HR (CC + 1) <= kMergeFloats
+        const int half = CC / 2;
+        for (int c0 = 0; c0 < D; c0 += CC) {
+          for (int c = c0 & ~31; c < c0 + CC; c += 32) {
+            uint32_t v[32];
+            if (active) {
+              tc05::ld32(to + c, v);
+              tc05::wait_ld();
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = 0u;
+            }
+            if (lane < rows) {
+              float* mine = merge + warp * kMergeFloats + lane * (CC + 1) + (c - c0);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c + e >= c0 && c + e < c0 + CC) mine[e] = __uint_as_float(v[e]) * k_own;
+            }
+            __syncwarp();
+          }
+          if (!(ok = sync())) break;
+          for (int e = threadIdx.x; e < rows * half; e += kSoftWarps * 32) {
+            const int rr = e / half, cc = (e - rr * half) * 2;
+            float a = 0.f, b = 0.f;
+#pragma unroll
+            for (int k = 0; k < kSoftWarps; ++k) {
+              a += merge[k * kMergeFloats + rr * (CC + 1) + cc];
+              b += merge[k * kMergeFloats + rr * (CC + 1) + cc + 1];
+            }
+            const int col = c0 + cc;
+            if (whole) {
+              const int ff = pc.row0 + rr, t = ff / p.G;
+              *reinterpret_cast<uint32_t*>(
+                  out + (static_cast<int64_t>(pc.q0 + t) * p.Hq + pc.kvh * p.G + (ff - t * p.G)) * D + col) =
+                  pack_bf16x2(a, b);
+            } else {
+              *reinterpret_cast<float2*>(p.part_acc + ((base * (D / 4) + col / 4) * p.RT + rr) * 4 + col % 4) =
+                  make_float2(a, b);
+            }
+          }
+          if (!(ok = sync())) break;
+        }
+        if (!ok) break;
+        tc05::fence_before_sync();
+      }
+      piece_done(i);
+    }
+    if (!ok) *abort_flag = 1;
+  }
+
+  // ---- exit: every role is done; free the tensor memory ----
+  __syncwarp();
+  tc05::fence_before_sync();
+  __syncthreads();
+  tc05::fence_after_sync();
+  if (warp == kMmaWarp) tc05::dealloc(tmem, kTmemCols);
+}
+
+template <class C>
+cudaError_t run(const AttnParams& p, cudaStream_t stream) {
+  CUtensorMap tmk, tmv, tmq;
+  const int tokens = (C::WIDE ? p.RT / 2 : p.RT) / p.G;
+  if (!make_pool_map(&tmk, p.k_pool, p.num_blocks, C::BS, p.Hkv, C::D, C::BS) ||
+      !make_pool_map(&tmv, p.v_pool, p.num_blocks, C::BS, p.Hkv, C::D, C::BS) ||
+      !make_q_rows_map(&tmq, p.q, p.T, p.Hq, C::D, p.q_stride, p.G, tokens))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_tc_kernel<C>, tmk, tmv, tmq, p);
+}
+
+template <int D, int BS>
+cudaError_t run_shape(const AttnParams& p, cudaStream_t stream) {
+  return p.RT > 32 ? run<TcAttn<D, BS, true>>(p, stream) : run<TcAttn<D, BS, false>>(p, stream);
+}
+
+}  // namespace
+
+// Rows per item of the tensor-core kernel: one narrow item of whole tokens where every sequence's
+// query tokens fit into 32 rows, else two M tiles.
+int attention_tc_rows(int max_query_len, int G) {
+  const int narrow = G <= 32 ? 32 / G : 0;
+  return max_query_len <= narrow ? max_query_len * G : 2 * (128 / G) * G;
+}
+
+cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t stream) {
+  switch (p.D * 100 + p.block_size) {
+    case 6408: return run_shape<64, 8>(p, stream);
+    case 6416: return run_shape<64, 16>(p, stream);
+    case 6432: return run_shape<64, 32>(p, stream);
+    case 12808: return run_shape<128, 8>(p, stream);
+    case 12816: return run_shape<128, 16>(p, stream);
+    case 12832: return run_shape<128, 32>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pa

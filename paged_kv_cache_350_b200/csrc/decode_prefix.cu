@@ -225,38 +225,6 @@ __device__ __forceinline__ UnitPos locate(const int* P, int R, int Hkv, int g) {
   return u;
 }
 
-// Bounded wait that also gives up when another role has given up (the CTA-wide abort
-// word); on its own expiry it records the timeout and raises the abort word.
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, int32_t* err,
-                                              volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      flag_error(err, PA_DEVERR_TIMEOUT);
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
-
-// The same, decided by lane 0 and shared with the warp.
-__device__ __forceinline__ bool wait_lane0(uint32_t bar, uint32_t parity, int32_t* err,
-                                           volatile int* abort_flag) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = wait_or_abort(bar, parity, err, abort_flag) ? 1 : 0;
-  return __shfl_sync(kFull, ok, 0) != 0;
-}
-
-// The same for a whole warp: every lane waits, and the warp agrees.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* err,
-                                          volatile int* abort_flag) {
-  const bool ok = wait_or_abort(bar, parity, err, abort_flag);
-  return __all_sync(kFull, ok) != 0;
-}
-
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_group_kernel(const __grid_constant__ CUtensorMap tmk,

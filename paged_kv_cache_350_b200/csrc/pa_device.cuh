@@ -107,6 +107,40 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, in
   return __all_sync(0xffffffffu, got) != 0;
 }
 
+// ---- bounded waits of warp-specialised kernels -----------------------------------
+
+// Bounded wait that also gives up when another role has given up (the CTA-wide abort
+// word); on its own expiry it records the timeout and raises the abort word.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, int32_t* err,
+                                              volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      flag_error(err, PA_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+// The same, decided by lane 0 and shared with the warp.
+__device__ __forceinline__ bool wait_lane0(uint32_t bar, uint32_t parity, int32_t* err,
+                                           volatile int* abort_flag) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_or_abort(bar, parity, err, abort_flag) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// The same for a whole warp: every lane waits, and the warp agrees.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* err,
+                                          volatile int* abort_flag) {
+  const bool ok = wait_or_abort(bar, parity, err, abort_flag);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
 // Order this thread's generic-proxy shared-memory writes before later async-proxy
 // (TMA) accesses of the same bytes.
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -194,6 +228,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+// L2 policy for data read again by other CTAs.
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
 

@@ -85,6 +85,10 @@ bool make_pool_map_rows(CUtensorMap* map, const void* pool, int NB, int BS, int 
 // Tensor map over q viewed as [B][Hq][D] (bf16): boxes of 64 columns x G heads of one
 // batch row, 128-byte swizzled.
 bool make_q_map(CUtensorMap* map, const void* q, int B, int Hq, int D, int G);
+// Tensor map over q as T tokens of [Hq][D], q_stride elements apart: boxes of 64 columns x G
+// heads x `tokens` tokens, 128-byte swizzled.
+bool make_q_rows_map(CUtensorMap* map, const void* q, int T, int Hq, int D, int64_t q_stride, int G,
+                     int tokens);
 
 // Launch the bf16 tensor-core decode kernel (+ reduce when max_parts > 1).
 cudaError_t launch_decode_tc(const DecodeParams& p, cudaStream_t stream);
@@ -143,6 +147,7 @@ struct AttnParams {
   int32_t* err;
   // the plan (in the workspace): rows per item, keys per tile, CTAs of the main kernel
   int RT, KT, ctas, max_items;
+  int HR;                       // rows of a softmax group of the tensor-core kernel (RT, or RT / 2)
   int32_t* header;              // [2]: items, tiles (of one KV head)
   int32_t* seq_items;           // [B] items before the sequence
   AttnItem* items;              // [max_items]
@@ -155,6 +160,8 @@ struct AttnParams {
 };
 cudaError_t launch_attention_plan(const AttnParams& p, cudaStream_t stream);
 cudaError_t launch_attention_generic(const AttnParams& p, pa_dtype dtype, cudaStream_t stream);
+cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t stream);
+int attention_tc_rows(int max_query_len, int G);
 cudaError_t launch_attention_join(const AttnParams& p, pa_dtype dtype, cudaStream_t stream);
 int attention_generic_ctas_per_sm(int RT, int D);
 

@@ -207,6 +207,7 @@ def test_single_tokens(dtype, Hq, Hkv, D, bs):
 
 MODS = {
     "cap": dict(softcap=5.0, spread=4.0),
+    "cap_small": dict(softcap=50.0, spread=4.0),
     "cap_wide": dict(softcap=50.0, spread=60.0),
     "bias": dict(bias=True),
     "window": dict(window=37),
