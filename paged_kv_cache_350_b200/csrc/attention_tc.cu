@@ -46,7 +46,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10, kQWarp = 11;
 constexpr int kPieces = 4;      // records in flight
 constexpr int kMaxSlots = 10;
 constexpr int kMergeFloats = 32 * 17;  // rows x (columns + 1) of a merge step, one part
-constexpr float kRescaleLog2 = 8.f;
+constexpr float kRescaleLog2 = 8.f, kOverflowLog2 = 64.f;
 constexpr uint32_t kColS = 0, kColO = 256, kGroupCols = 128, kTmemCols = 512;
 // released by the MMA warp, the two load warps and each softmax warp
 constexpr int kPieceUsers = 3 + kSoftWarps;
@@ -118,63 +118,98 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, const Piece& pc, int 
 
 // Turn N raw scores (keys key0 .. of one row) into log2-domain scores in place and return their
 // maximum.  The plain case keeps raw scores, so that the scale and the subtraction of the maximum
-// become one operation.
+// become one operation.  Elements are taken 8 at a time, step by step, so that the steps of one
+// element do not wait for each other.
 template <int N>
 __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& p, const Row& r, int key0,
                                                bool plain, bool masked) {
+  constexpr int E = 8;
   const int a = r.lo - key0, b = r.hi - key0;
   if (p.cap_out > 0.f) {
     if (masked) {  // what lies in masked columns must not choose the branch below
 #pragma unroll
       for (int j = 0; j < N; ++j) x[j] = j >= a && j < b ? x[j] : 0.f;
     }
-    float ax = 0.f;
+    float ax[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < N; j += 2) ax = fmaxf(ax, fmaxf(fabsf(x[j]), fabsf(x[j + 1])));
+    for (int j = 0; j < N; j += 8)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ax[e] = fmaxf(ax[e], fmaxf(fabsf(x[j + 2 * e]), fabsf(x[j + 2 * e + 1])));
     // (a NaN fails the comparison only if it is all there is; both ways carry it through)
-    if (__all_sync(kFull, ax * fabsf(p.cap_in) <= 1.f)) {
+    const float top = fmaxf(fmaxf(ax[0], ax[1]), fmaxf(ax[2], ax[3]));
+    if (__all_sync(kFull, top * fabsf(p.cap_in) <= 1.f)) {
       // tanh(t) / t as a polynomial in t^2 (iterated reweighted least squares on |t| <= 1, where
       // |t P(t^2) - tanh t| < 2.4e-7): on the FMA pipe alone, the exponentials need the other
       const float2 ci = splat(p.cap_in), co = splat(p.cap_out);
 #pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        const float2 t = __fmul2_rn(make_float2(x[j], x[j + 1]), ci);
-        const float2 u = __fmul2_rn(t, t);
-        float2 y = __ffma2_rn(u, splat(-0.0028394642286f), splat(0.01611417718f));
-        y = __ffma2_rn(y, u, splat(-0.0509728603065f));
-        y = __ffma2_rn(y, u, splat(0.132535248995f));
-        y = __ffma2_rn(y, u, splat(-0.333240032196f));
-        y = __ffma2_rn(y, u, splat(0.999996840954f));
-        y = __fmul2_rn(y, __fmul2_rn(t, co));
-        x[j] = y.x;
-        x[j + 1] = y.y;
+      for (int j = 0; j < N; j += E) {
+        float2 t[E / 2], u[E / 2], y[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) t[e] = __fmul2_rn(make_float2(x[j + 2 * e], x[j + 2 * e + 1]), ci);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) u[e] = __fmul2_rn(t[e], t[e]);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(u[e], splat(-0.0028394642286f), splat(0.01611417718f));
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], splat(-0.0509728603065f));
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], splat(0.132535248995f));
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], splat(-0.333240032196f));
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) t[e] = __fmul2_rn(t[e], co);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], splat(0.999996840954f));
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          y[e] = __fmul2_rn(y[e], t[e]);
+          x[j + 2 * e] = y[e].x;
+          x[j + 2 * e + 1] = y[e].y;
+        }
       }
     } else {
       // tanh t = 1 - 2 / (1 + e^2t)
       const float c2 = p.cap_in * (2.f * kLog2e), m2 = -2.f * p.cap_out;
 #pragma unroll
-      for (int j = 0; j < N; ++j) x[j] = fmaf(m2, rcp_approx(1.f + ex2_approx(x[j] * c2)), p.cap_out);
+      for (int j = 0; j < N; j += E) {
+        float u[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) u[e] = ex2_approx(x[j + e] * c2);
+#pragma unroll
+        for (int e = 0; e < E; ++e) u[e] = rcp_approx(1.f + u[e]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[j + e] = fmaf(m2, u[e], p.cap_out);
+      }
     }
   } else if (!plain) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] *= p.scale_log2;
+    for (int j = 0; j < N; j += 2) {
+      const float2 y = __fmul2_rn(make_float2(x[j], x[j + 1]), splat(p.scale_log2));
+      x[j] = y.x;
+      x[j + 1] = y.y;
+    }
   }
   if (p.slopes) {
     const float d0 = static_cast<float>(r.pos - key0);
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = fmaf(-r.slope, fabsf(d0 - static_cast<float>(j)), x[j]);
+    for (int j = 0; j < N; j += E) {
+      float d[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) d[e] = d0 - static_cast<float>(j + e);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[j + e] = fmaf(-r.slope, fabsf(d[e]), x[j + e]);
+    }
   }
   if (masked) {
 #pragma unroll
     for (int j = 0; j < N; ++j) x[j] = j >= a && j < b ? x[j] : -INFINITY;
   }
-  float m0 = -INFINITY, m1 = -INFINITY;
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int j = 0; j < N; j += 4) {
-    m0 = fmaxf(m0, fmaxf(x[j], x[j + 1]));
-    m1 = fmaxf(m1, fmaxf(x[j + 2], x[j + 3]));
-  }
-  return fmaxf(m0, m1);
+  for (int j = 0; j < N; j += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(x[j + 2 * e], x[j + 2 * e + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 template <int N>
@@ -242,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc05::fence_before_sync();
   __syncthreads();
   tc05::fence_after_sync();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __reduce_max_sync(kFull, sh.tmem);
   volatile int* abort_flag = &sh.abort_flag;
   // nothing above reads global memory; the plan is written by the kernel before
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -326,7 +361,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int BPT = kKT / BS;  // blocks per tile, at most 16
       const uint64_t policy = WIDE ? l2_policy_evict_normal() : l2_policy_evict_first();
       bool ok = true;
-      int64_t n = 0;  // loads issued
+      int slot = 0;
+      uint32_t phase = 0, used = 0;  // of the next load; slots in use (bits) once round
+      auto next_slot = [&] {
+        used |= 1u << slot;
+        if (++slot == NST) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
       for (int i = 0; ok; ++i) {
         if (!(ok = piece_wait(i))) break;
         const Piece& pc = sh.pc[i % kPieces];
@@ -342,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto id_at = [&](int j) { return live_at(j) ? __ldg(tab + (kt0 + j) * BPT + lane) : 0; };
         int next = id_at(0);
-        for (int j = 0; j < cnt; ++j) {
+        for (int j = 0; j < cnt && ok; ++j) {
           int phys = next;
           const bool live = live_at(j);
           next = id_at(j + 1);
@@ -352,10 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t bytes = __popc(__ballot_sync(kFull, live)) * BS * D * 2;
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++n) {
-            const int slot = static_cast<int>(n % NST);
-            if (n >= NST &&
-                !(ok = wait_warp(smem_addr(&sh.empty[slot]), static_cast<uint32_t>(n / NST - 1) & 1, p.err, abort_flag)))
+          for (int kv = 0; kv < 2; ++kv) {
+            if ((used >> slot & 1) &&
+                !(ok = wait_warp(smem_addr(&sh.empty[slot]), phase ^ 1, p.err, abort_flag)))
               break;
             const uint32_t bar = smem_addr(&sh.full[slot]);
             if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
@@ -367,13 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_4d(dst + c * C::CHUNK, kv ? &tmv : &tmk, c * 64, kvh, 0, phys, bar, policy);
             }
             __syncwarp();
+            next_slot();
           }
-          if (!ok) break;
         }
       }
-      if (!ok)  // loads issued but perhaps never waited for
-        for (int64_t k = n > NST ? n - NST : 0; k < n; ++k)
-          mbar_wait(smem_addr(&sh.full[k % NST]), static_cast<uint32_t>(k / NST) & 1, nullptr);
+      if (!ok)  // loads issued but perhaps never waited for: the last of each slot
+        for (int k = 0; k < NST; ++k)
+          if (used >> k & 1) mbar_wait(smem_addr(&sh.full[k]), k < slot ? phase : phase ^ 1, nullptr);
     } else if (warp == kQWarp) {
       // ============================ Q tiles ============================
       const uint64_t policy = l2_policy_evict_normal();
@@ -406,42 +448,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_s = tc05::instr_desc_bf16(128, kKT, 0);
       constexpr uint32_t id_pv = tc05::instr_desc_bf16(128, D, 1);
       // A cursor over the sub-steps: tile by tile, and for the wide shape group 0 then group 1.
+      // All it needs lies in registers, ring slots are counted rather than divided: this loop is
+      // the latency between a group's P and its next S.
       struct Cursor {
-        int n = 0, j = 0, g = 0;  // piece, tile, group
-        int cnt = 0, step0 = 0;   // of that piece
+        int n = 0, j = 0, g = 0, cnt = 0;  // piece, tile, group; tiles of the piece
+        int slot = 0;                      // the tile's ring slot
+        uint32_t phase = 0;
+        int a0 = 0, b0 = 0, a1 = 0, b1 = 0;  // the groups' tiles (wide)
+        int lo = 0, hi = 0;                  // the item's keys from the piece's first tile on
       };
       Cursor sc, pv;
+      pv.slot = 1;
       bool s_end = false, pv_end = false, ok = true;
-      int s_done[2] = {0, 0}, pv_done[2] = {0, 0};  // sub-steps issued per group
-      auto ready = [&](uint32_t bar, uint32_t parity) {  // lane 0's view, for the whole warp
-        return __shfl_sync(kFull, static_cast<int>(mbar_test_wait(bar, parity)), 0) != 0;
+      uint32_t pend = 0;    // bit g: S of group g is issued, its P.V is not
+      uint32_t ppar = 0;    // bit g: parity of the group's P
+      auto ready = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(kFull, mbar_test_wait(bar, parity)) != 0;
       };
-      // the piece of a cursor at its start: false when nothing (more) can be done
+      // (a reduction over the warp tells the compiler that the value is the same in all lanes)
+      auto uni = [](int v) { return __reduce_max_sync(kFull, v); };
       auto enter = [&](Cursor& c) {
         const Piece& pc = sh.pc[c.n % kPieces];
-        c.cnt = pc.cnt;
-        c.step0 = pc.step0;
+        c.cnt = uni(pc.cnt);
         c.j = 0;
-        c.g = WIDE ? 0 : pc.step0 & 1;
+        const int k0 = uni(pc.kt0) * kKT;
+        c.lo = uni(pc.lo) - k0;
+        c.hi = uni(pc.hi) - k0;
+        if (WIDE) {
+          c.g = 0;
+          c.a0 = uni(pc.ga[0]);
+          c.b0 = uni(pc.gb[0]);
+          c.a1 = uni(pc.ga[1]);
+          c.b1 = uni(pc.gb[1]);
+        } else {
+          c.g = uni(pc.step0) & 1;
+        }
       };
       auto group_active = [&](const Cursor& c) {
-        if (!WIDE) return true;
-        const Piece& pc = sh.pc[c.n % kPieces];
-        return c.j >= pc.ga[c.g] && c.j < pc.gb[c.g];
+        return !WIDE || (c.g ? c.j >= c.a1 && c.j < c.b1 : c.j >= c.a0 && c.j < c.b0);
       };
       auto advance = [&](Cursor& c) {  // true: the tile is finished
-        if (WIDE) {
-          c.g ^= 1;
-          if (c.g) return false;
-        } else {
-          c.g ^= 1;
-        }
+        c.g ^= 1;
+        if (WIDE && c.g) return false;
         ++c.j;
+        c.slot += 2;
+        if (c.slot >= NST) {
+          c.slot -= NST;
+          c.phase ^= 1;
+        }
         return true;
       };
       if ((ok = piece_wait(0))) {
         enter(sc);
-        pv = sc;
+        enter(pv);
         s_end = pv_end = sc.cnt == 0;
       }
       bool s_wait = true;    // the cursor's tile has not been waited for yet
@@ -453,38 +512,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           s_enter = false;
         }
         // ---- S of the next sub-step, as soon as its group's P has been read ----
-        const bool behind = !s_enter && !s_end && sc.n == pv.n && sc.j == pv.j && sc.g == pv.g;
-        if (!s_end && !s_enter && s_done[sc.g] == pv_done[sc.g]) {
-          const bool must = behind;  // nothing else to do
-          const int64_t load = 2 * (static_cast<int64_t>(sc.step0) + sc.j);
-          const int slot = static_cast<int>(load % NST);
-          const uint32_t kb = smem_addr(&sh.full[slot]), kpar = static_cast<uint32_t>(load / NST) & 1;
-          const uint32_t qb = smem_addr(&sh.qfull), qpar = sc.n & 1;
-          if (!s_wait || must || (ready(kb, kpar) && ready(qb, qpar))) {
+        const bool must = !s_enter && !s_end && sc.n == pv.n && sc.j == pv.j && sc.g == pv.g;  // nothing is pending
+        if (!s_end && !s_enter && !(pend >> sc.g & 1)) {
+          const uint32_t kb = smem_addr(&sh.full[sc.slot]), qb = smem_addr(&sh.qfull);
+          if (!s_wait || must || (ready(kb, sc.phase) && (sc.j > 0 || ready(qb, sc.n & 1)))) {
             if (s_wait) {
-              if (!(ok = wait_warp(qb, qpar, p.err, abort_flag) && wait_warp(kb, kpar, p.err, abort_flag))) break;
+              if (!(ok = (sc.j > 0 || wait_warp(qb, sc.n & 1, p.err, abort_flag)) &&
+                         wait_warp(kb, sc.phase, p.err, abort_flag)))
+                break;
               s_wait = false;
             }
             const int g = sc.g;
-            const bool act = group_active(sc);
-            if (act && lane == 0) {
+            if (group_active(sc)) {
               tc05::fence_after_sync();
-              const uint64_t dq = tc05::smem_desc(smem_addr(smem + (WIDE ? g * C::SLOT : 0)), 16, 1024);
-              const uint64_t dk = tc05::smem_desc(smem_addr(ring + slot * C::SLOT), 16, 1024);
+              const uint64_t dq = tc05::smem_desc(smem_addr(smem) + (WIDE ? g * C::SLOT : 0), 16, 1024);
+              const uint64_t dk = tc05::smem_desc(smem_addr(ring) + sc.slot * C::SLOT, 16, 1024);
               const uint32_t ts = tmem + kColS + g * kGroupCols;
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = (k >> 2) * C::CHUNK + (k & 3) * 32;
-                tc05::mma_ss(ts, dq + (off >> 4), dk + (off >> 4), id_s, k > 0);
+                tc05::mma_ss_warp(ts, dq + (off >> 4), dk + (off >> 4), id_s, k > 0);
               }
-              tc05::commit(smem_addr(&sh.sfull[g]));
+              tc05::commit_warp(smem_addr(&sh.sfull[g]));
+              pend |= 1u << g;
             }
-            if (act) ++s_done[g];
+            const uint32_t eb = smem_addr(&sh.empty[sc.slot]);
             if (advance(sc)) {
-              if (lane == 0) tc05::commit(smem_addr(&sh.empty[slot]));
+              tc05::commit_warp(eb);
               s_wait = true;
               if (sc.j == sc.cnt) {
-                if (lane == 0) tc05::commit(smem_addr(&sh.qempty));
+                tc05::commit_warp(smem_addr(&sh.qempty));
                 ++sc.n;
                 s_enter = true;
               }
@@ -493,27 +550,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // ---- P.V of the sub-step at the other cursor ----
-        const Piece& pc = sh.pc[pv.n % kPieces];
-        const int g = pv.g;
-        const int64_t load = 2 * (static_cast<int64_t>(pv.step0) + pv.j) + 1;
-        const int slot = static_cast<int>(load % NST);
         if (s_enter && pv.n == sc.n) continue;  // the record is there: pv has waited for it
-        if (behind) {  // (its S was issued above: the two cursors agree on what is pending)
+        if (must) {  // (its S was issued above: the two cursors agree on what is pending)
           flag_error(p.err, PA_DEVERR_TIMEOUT);
           ok = false;
           break;
         }
-        const bool first_sub = !WIDE || g == 0;
-        if (first_sub) {
-          if (!(ok = wait_warp(smem_addr(&sh.full[slot]), static_cast<uint32_t>(load / NST) & 1, p.err, abort_flag)))
-            break;
+        const int g = pv.g;
+        // the item's keys within the tile
+        const int a = max(pv.lo - pv.j * kKT, 0), z = min(pv.hi - pv.j * kKT, kKT);
+        if (!WIDE || g == 0) {
+          if (!(ok = wait_warp(smem_addr(&sh.full[pv.slot]), pv.phase, p.err, abort_flag))) break;
           // V rows outside the item's keys may hold anything (0 * Inf is NaN): zero those that
           // the product reads, up to the 16-key steps
-          const int k0 = (pc.kt0 + pv.j) * kKT;
-          const int a = max(pc.lo - k0, 0), z = min(pc.hi - k0, kKT);
           const int na = a & 15, nz = -z & 15;
           if (na + nz > 0) {
-            uint8_t* v = ring + slot * C::SLOT;
+            uint8_t* v = ring + pv.slot * C::SLOT;
             for (int e = lane; e < (na + nz) * DCH * 8; e += 32) {
               const int r = e / (DCH * 8), q = e % (DCH * 8);
               const int row = r < na ? a - na + r : z + r - na;
@@ -524,24 +576,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (group_active(pv)) {
-          if (!(ok = wait_warp(smem_addr(&sh.pfull[g]), pv_done[g] & 1, p.err, abort_flag))) break;
-          if (lane == 0) {
-            tc05::fence_after_sync();
-            const int k0 = (pc.kt0 + pv.j) * kKT;
-            const int s0 = max(pc.lo - k0, 0) >> 4, s1 = (min(pc.hi - k0, kKT) + 15) >> 4;
-            const uint64_t dv = tc05::smem_desc(smem_addr(ring + slot * C::SLOT), C::CHUNK, 1024);
-            const uint32_t tp = tmem + kColS + g * kGroupCols, to = tmem + kColO + g * kGroupCols;
-            // the group's first tile of the piece overwrites O
-            const bool fresh = WIDE ? pv.j == pc.ga[g] : pv.j < 2;
+          if (!(ok = wait_warp(smem_addr(&sh.pfull[g]), ppar >> g & 1, p.err, abort_flag))) break;
+          ppar ^= 1u << g;
+          pend &= ~(1u << g);
+          tc05::fence_after_sync();
+          const uint64_t dv = tc05::smem_desc(smem_addr(ring) + pv.slot * C::SLOT, C::CHUNK, 1024);
+          const uint32_t tp = tmem + kColS + g * kGroupCols, to = tmem + kColO + g * kGroupCols;
+          // the group's first tile of the piece overwrites O
+          const bool fresh = WIDE ? pv.j == (g ? pv.a1 : pv.a0) : pv.j < 2;
+          const int s0 = a >> 4, s1 = (z + 15) >> 4;
+          if (s0 == 0 && s1 == kKT / 16) {
 #pragma unroll
             for (int k = 0; k < kKT / 16; ++k)
-              if (k >= s0 && k < s1) tc05::mma_ts(to, tp + 8 * k, dv + (k * 2048 >> 4), id_pv, !(fresh && k == s0));
-            if (WIDE ? pv.j == pc.gb[g] - 1 : pv.j + 2 >= pv.cnt) tc05::commit(smem_addr(&sh.ofull[g]));
+              tc05::mma_ts_warp(to, tp + 8 * k, dv + (k * 2048 >> 4), id_pv, k > 0 || !fresh);
+          } else {
+#pragma unroll 1
+            for (int k = s0; k < s1; ++k)
+              tc05::mma_ts_warp(to, tp + 8 * k, dv + (k * 2048 >> 4), id_pv, k > s0 || !fresh);
           }
-          ++pv_done[g];
+          if (WIDE ? pv.j == (g ? pv.b1 : pv.b0) - 1 : pv.j + 2 >= pv.cnt) tc05::commit_warp(smem_addr(&sh.ofull[g]));
         }
+        const uint32_t eb = smem_addr(&sh.empty[pv.slot]);
         if (advance(pv)) {
-          if (lane == 0) tc05::commit(smem_addr(&sh.empty[slot]));
+          tc05::commit_warp(eb);
           if (pv.j == pv.cnt) {
             piece_done(pv.n);
             ++pv.n;
@@ -553,11 +610,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) *abort_flag = 1;
       // every product issued has completed before the memory is freed
-      if (lane == 0) {
-        tc05::commit(smem_addr(&sh.drain_bar));
-        mbar_wait(smem_addr(&sh.drain_bar), 0, p.err);
-      }
       __syncwarp();
+      tc05::commit_warp(smem_addr(&sh.drain_bar));
+      mbar_wait(smem_addr(&sh.drain_bar), 0, p.err);
     }
   } else {
     // ============================ softmax ============================
@@ -615,59 +670,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         all_lo = max(all_lo, __shfl_xor_sync(kFull, all_lo, off));
         all_hi = min(all_hi, __shfl_xor_sync(kFull, all_hi, off));
       }
-      float m_ref = -INFINITY, l = 0.f;
+      // reference maximum, sum, and the maximum seen (the reference may lag by kOverflowLog2)
+      float m_ref = -INFINITY, l = 0.f, m_next = -INFINITY;
       for (int j = ja; j < jb; j += jstep, ++done) {
         if (!(ok = wait_warp(smem_addr(&sh.sfull[g]), done & 1, p.err, abort_flag))) break;
         tc05::fence_after_sync();
-        constexpr int N = WIDE ? kKT : 32;  // this thread's columns
-        const int key0 = (pc.kt0 + j) * kKT + (WIDE ? 0 : 32 * w);
         if (WIDE && 32 * w >= rows) {  // none of the warp's rows is a row of the item
           tc05::fence_before_sync();
           mbar_arrive(smem_addr(&sh.pfull[g]));
           continue;
         }
-        uint32_t raw[N / 32][32];
+        // The wide shape takes a tile's 128 columns in two halves, so that the scores and what
+        // their modification needs stay in registers.  The reference maximum is that of the first
+        // half and the tiles before; the second half moves it only where its weights might
+        // overflow (the first half's P would have to be rescaled, and is), else the next tile does.
+        constexpr int N = WIDE ? 64 : 32, NH = WIDE ? 2 : 1;
+        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+#pragma unroll 1  // (one copy of the code: instruction fetches bound two)
+        for (int h = 0; h < NH; ++h) {
+          const int col = WIDE ? N * h : 32 * w;  // first column
+          const int key0 = (pc.kt0 + j) * kKT + col;
+          uint32_t raw[N / 32][32];
 #pragma unroll
-        for (int c = 0; c < N / 32; ++c) tc05::ld32(ts + (WIDE ? 32 * c : 32 * w), raw[c]);
-        tc05::wait_ld();
-        float x[N];
+          for (int c = 0; c < N / 32; ++c) tc05::ld32(ts + col + 32 * c, raw[c]);
+          tc05::wait_ld();
+          float x[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = __uint_as_float(raw[e / 32][e % 32]);
-        const bool masked = key0 < all_lo || key0 + N > all_hi;
-        const float mt = modify_scores(x, p, row, key0, plain, masked) * mul;
-        const bool raise = mt > m_ref + kRescaleLog2;
-        // (earlier P.V of the group are complete: S was issued behind them)
-        if (__any_sync(kFull, raise)) {
-          const float alpha = raise ? ex2_approx(m_ref - mt) : 1.f;
-          if (j > ja) {
+          for (int e = 0; e < N; ++e) x[e] = __uint_as_float(raw[e / 32][e % 32]);
+          const bool masked = key0 < all_lo || key0 + N > all_hi;
+          const float mt = fmaxf(m_next, modify_scores(x, p, row, key0, plain, masked) * mul);
+          const bool raise = mt > m_ref + (h == 0 ? kRescaleLog2 : kOverflowLog2);
+          // (earlier P.V of the group are complete: S was issued behind them)
+          if (__any_sync(kFull, raise)) {
+            const float alpha = raise ? ex2_approx(m_ref - mt) : 1.f;
+            if (j > ja) {
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
+              for (int c = 0; c < D; c += 32) {
+                uint32_t v[32];
+                tc05::ld32(to + c, v);
+                tc05::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                tc05::st32(to + c, v);
+              }
+            }
+            if (h == 1) {  // the first half's P, which is in tensor memory already
+              tc05::wait_st();
               uint32_t v[32];
-              tc05::ld32(to + c, v);
+              tc05::ld32(ts, v);
               tc05::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-              tc05::st32(to + c, v);
+              for (int e = 0; e < 32; ++e) v[e] = pack_bf16x2(bf16_lo(v[e]) * alpha, bf16_hi(v[e]) * alpha);
+              tc05::st32(ts, v);
+              l0 = __fmul2_rn(l0, splat(alpha));
+              l1 = __fmul2_rn(l1, splat(alpha));
             }
+            l *= alpha;
+            if (raise) m_ref = mt;
           }
-          l *= alpha;
-          if (raise) m_ref = mt;
-        }
-        const float ref = m_ref == -INFINITY ? 0.f : -m_ref;
-        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-        const float2 mul2 = splat(mul), ref2 = splat(ref);
+          m_next = mt;
+          const float2 mul2 = splat(mul), ref2 = splat(m_ref == -INFINITY ? 0.f : -m_ref);
 #pragma unroll
-        for (int c = 0; c < N; c += 32) {
-          uint32_t v[16];
+          for (int c = 0; c < N; c += 32) {
+            uint32_t v[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 y = __ffma2_rn(make_float2(x[c + 2 * e], x[c + 2 * e + 1]), mul2, ref2);
-            y.x = ex2_approx(y.x);
-            y.y = ex2_approx(y.y);
-            if (e & 1) l1 = __fadd2_rn(l1, y); else l0 = __fadd2_rn(l0, y);
-            v[e] = pack_bf16x2(y.x, y.y);
+            for (int e = 0; e < 16; ++e) {
+              float2 y = __ffma2_rn(make_float2(x[c + 2 * e], x[c + 2 * e + 1]), mul2, ref2);
+              y.x = ex2_approx(y.x);
+              y.y = ex2_approx(y.y);
+              if (e & 1) l1 = __fadd2_rn(l1, y); else l0 = __fadd2_rn(l0, y);
+              v[e] = pack_bf16x2(y.x, y.y);
+            }
+            tc05::st16(ts + (WIDE ? (col + c) / 2 : 16 * w), v);
           }
-          tc05::st16(ts + (WIDE ? c / 2 : 16 * w), v);
         }
         if (!WIDE) {  // zero outside this warp's columns
           uint32_t v[16];

@@ -110,15 +110,19 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, in
 // ---- bounded waits of warp-specialised kernels -----------------------------------
 
 // Bounded wait that also gives up when another role has given up (the CTA-wide abort
-// word); on its own expiry it records the timeout and raises the abort word.
+// word); on its own expiry it records the timeout and raises the abort word.  A try waits
+// for a while in hardware; the clock is read only every 64th, as reading it costs more.
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, int32_t* err,
                                               volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
     if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 63) != 63) continue;
     if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > kWaitLimitNs) {
       flag_error(err, PA_DEVERR_TIMEOUT);
       *abort_flag = 1;
       return false;
