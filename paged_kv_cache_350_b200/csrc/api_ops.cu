@@ -34,18 +34,30 @@ struct AttnShape {
   int RT, HR, KT, ctas, max_items;
 };
 
-// The tensor-core kernel takes bf16, blocks of whole swizzle atoms (8 rows) and groups of at
-// most the 128 rows of its M tile.
-bool attention_on_tc(int G, int block_size, pa_dtype dtype) {
-  return dtype == PA_BF16 && block_size >= 8 && G <= 128;
+// Which kernel a call takes.  The tensor-core ones take bf16 and blocks of whole swizzle atoms (8
+// rows): the tokens kernel a few rows per sequence, bound by the cache's bytes; the other groups
+// of at most the 128 rows of its M tile.
+enum AttnKernel { kGeneric, kTensor, kTokens };
+
+AttnKernel attention_kernel(int B, int max_query_len, int G, int block_size, pa_dtype dtype) {
+  if (dtype != PA_BF16 || block_size < 8) return kGeneric;
+  if (pa::attention_tokens_eligible(max_query_len, G, B)) return kTokens;
+  return G <= 128 ? kTensor : kGeneric;
 }
 
-AttnShape attention_shape(int T, int B, int max_query_len, int G, int D, bool tc, int sms) {
+AttnShape attention_shape(int T, int B, int max_query_len, int G, int D, AttnKernel kernel, int sms) {
   AttnShape s;
-  if (tc) {
+  if (kernel == kTokens) {
+    s.KT = 16;
+    s.RT = s.HR = max_query_len * G;
+    s.ctas = pa::attention_tokens_ranges(sms);
+    s.max_items = 0;
+    return s;
+  }
+  if (kernel == kTensor) {
     s.KT = 128;
-    s.RT = pa::attention_tc_rows(max_query_len, G);
-    s.HR = s.RT > 32 ? s.RT / 2 : s.RT;
+    s.RT = pa::attention_tc_rows(G);
+    s.HR = s.RT / 2;
     s.ctas = sms;
   } else {
     s.KT = 64;
@@ -195,9 +207,10 @@ size_t pa_attention_workspace_size(int T, int B, int max_query_len, int Hq, int 
   if (T == 0 || B == 0) return 0;
   const int sms = sm_count() > 0 ? sm_count() : kSmBound;
   size_t n = 0;  // enough for either type
-  for (int tc = attention_on_tc(Hq / Hkv, block_size, PA_BF16); tc >= 0; --tc)
-    n = std::max(n, attention_carve(attention_shape(T, B, std::max(max_query_len, 1), Hq / Hkv, D, tc != 0, sms), B, D,
-                                    nullptr, nullptr));
+  const int most = std::max(max_query_len, 1), G = Hq / Hkv;
+  for (const pa_dtype dtype : {PA_F32, PA_BF16})
+    n = std::max(n, attention_carve(attention_shape(T, B, most, G, D, attention_kernel(B, most, G, block_size, dtype), sms),
+                                    B, D, nullptr, nullptr));
   return n;
 }
 
@@ -231,10 +244,11 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
   const int sms = sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
   const int G = Hq / Hkv;
-  const bool tc = attention_on_tc(G, block_size, dtype);
-  const AttnShape sh = attention_shape(T, B, max_query_len, G, D, tc, sms);
-  // tile counts of one KV head are summed in 32 bits
-  if (static_cast<int64_t>(sh.max_items) * (max_seq / sh.KT + 2) >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+  const AttnKernel kernel = attention_kernel(B, max_query_len, G, block_size, dtype);
+  const AttnShape sh = attention_shape(T, B, max_query_len, G, D, kernel, sms);
+  // tile counts are summed in 32 bits: of one KV head, or of all in the tokens kernel
+  const int64_t rows = kernel == kTokens ? static_cast<int64_t>(B) * Hkv : sh.max_items;
+  if (rows * (max_seq / sh.KT + 2) >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
   pa::AttnParams p{};
   if (workspace_bytes < attention_carve(sh, B, D, static_cast<char*>(workspace), &p)) return PA_ERR_INVALID_ARG;
   const double log2e = 1.4426950408889634;
@@ -265,9 +279,15 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
   p.num_blocks = num_blocks;
   p.err = dev_err_flag;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = pa::launch_attention_plan(p, s);
-  if (e == cudaSuccess) e = tc ? pa::launch_attention_tc(p, s) : pa::launch_attention_generic(p, dtype, s);
-  if (e == cudaSuccess) e = pa::launch_attention_join(p, dtype, s);
+  cudaError_t e;
+  if (kernel == kTokens) {
+    e = pa::launch_attention_tokens(p, s);
+  } else {
+    e = pa::launch_attention_plan(p, s);
+    if (e == cudaSuccess)
+      e = kernel == kTensor ? pa::launch_attention_tc(p, s) : pa::launch_attention_generic(p, dtype, s);
+    if (e == cudaSuccess) e = pa::launch_attention_join(p, dtype, s);
+  }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -64,16 +64,6 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
   return r;
 }
 
-// Query tokens of sequence b: [q0, q0 + n); none where the span is malformed or longer than
-// the caller said.
-__device__ __forceinline__ int query_span(const AttnParams& p, int b, bool flag, int& q0) {
-  const int s0 = __ldg(p.query_starts + b), s1 = __ldg(p.query_starts + b + 1);
-  const bool bad = s0 < 0 || s1 < s0 || s1 > p.T || s1 - s0 > p.max_query_len;
-  if (bad && flag) flag_error(p.err, PA_DEVERR_BAD_SEQ_LEN);
-  q0 = s0;
-  return bad ? 0 : s1 - s0;
-}
-
 // One CTA.  Sequences' item counts are scanned, then each item's interval and tile count,
 // then the tile counts; last, where each CTA of the main kernel begins.
 __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const AttnParams p) {
@@ -84,7 +74,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
     int n = 0, q0;
-    if (b < p.B) n = (static_cast<int64_t>(query_span(p, b, true, q0)) * p.G + p.RT - 1) / p.RT;
+    if (b < p.B) n = (static_cast<int64_t>(attn_query_span(p, b, true, q0)) * p.G + p.RT - 1) / p.RT;
     int total;
     const int at = block_scan(n, sums, total);
     if (b < p.B) p.seq_items[b] = items + at;
@@ -108,7 +98,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
       }
       AttnItem it;
       it.b = a;
-      const int n = query_span(p, a, false, it.q0);
+      const int n = attn_query_span(p, a, false, it.q0);
       const int nrows = n * p.G;
       it.row0 = (i - p.seq_items[a]) * p.RT;
       it.rows = min(p.RT, nrows - it.row0);

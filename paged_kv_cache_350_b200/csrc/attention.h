@@ -35,6 +35,16 @@ __device__ __forceinline__ int attn_len(const AttnParams& p, int b, bool flag) {
   return L;
 }
 
+// Query tokens of sequence b: [q0, q0 + n); none where the span is malformed or longer than
+// the caller said.
+__device__ __forceinline__ int attn_query_span(const AttnParams& p, int b, bool flag, int& q0) {
+  const int s0 = __ldg(p.query_starts + b), s1 = __ldg(p.query_starts + b + 1);
+  const bool bad = s0 < 0 || s1 < s0 || s1 > p.T || s1 - s0 > p.max_query_len;
+  if (bad && flag) flag_error(p.err, PA_DEVERR_BAD_SEQ_LEN);
+  q0 = s0;
+  return bad ? 0 : s1 - s0;
+}
+
 // Keys visible to the query token at position pos of a sequence of L tokens: [lo, hi) with
 //   key j visible iff j < L, (j <= pos or j < prefix), j > pos - window (if any), j >= first.
 // A position below 0 (more query tokens than cached ones) sees nothing.

@@ -2,16 +2,9 @@
 // (sm_100a, bf16).  The formula, the masks and the work plan are attention.cu's; a CTA of one
 // wave walks its equal contiguous range of (item, KV head, tile of 128 keys).
 //
-// Two shapes of the same kernel:
-//   wide    an item is two M tiles of whole tokens, HR = floor(128 / G) * G rows each.  Softmax
-//           group g serves M tile g; both read the same K and V tiles, so a tile of 128 keys is
-//           loaded once for up to 256 rows.  Group g skips the tiles that none of its rows sees.
-//   narrow  at most 32 rows (single tokens, a few speculative ones).  Q lies four times in
-//           the M tile, at rows 0, 32, 64 and 96, and softmax warp w of a group takes its columns
-//           32w .. 32w + 31 of a tile: four warps share the tile's exponentials where one
-//           would do them all, and a lane's P is zero outside its warp's columns, so that its O is
-//           the part of those columns.  Groups take alternate tiles.  The eight parts of a row
-//           (2 groups x 4 warps) are merged once per piece.
+// An item is two M tiles of whole tokens, HR = floor(128 / G) * G rows each.  Softmax group g
+// serves M tile g; both read the same K and V tiles, so a tile of 128 keys is loaded once for up to
+// 256 rows.  Group g skips the tiles that none of its rows sees.
 //
 // Warps: 0-7 softmax (group g = warps 4g .. 4g + 3, a thread per row), 8 MMA, 9 K/V loads, 10
 // schedule, 11 Q loads.  The schedule warp writes records of the CTA's pieces (a piece is the part
@@ -45,26 +38,22 @@ constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10, kQWarp = 11;
 constexpr int kPieces = 4;      // records in flight
 constexpr int kMaxSlots = 10;
-constexpr int kMergeFloats = 32 * 17;  // rows x (columns + 1) of a merge step, one part
 constexpr float kRescaleLog2 = 8.f, kOverflowLog2 = 64.f;
 constexpr uint32_t kColS = 0, kColO = 256, kGroupCols = 128, kTmemCols = 512;
 // released by the MMA warp, the two load warps and each softmax warp
 constexpr int kPieceUsers = 3 + kSoftWarps;
 
-template <int D_, int BS_, bool WIDE_>
+template <int D_, int BS_>
 struct TcAttn {
   static constexpr int D = D_, BS = BS_;
-  static constexpr bool WIDE = WIDE_;
-  static constexpr int MT = WIDE ? 2 : 1;             // M tiles of an item
+  static constexpr int MT = 2;                        // M tiles of an item
   static constexpr int DCH = D / 64;
   static constexpr int CHUNK = kKT * 128;             // one 64-column chunk of 128 rows
   static constexpr int SLOT = DCH * CHUNK;            // a K or V tile; an M tile of Q
-  // the narrow shape's merge: (max, sum) of each part, and kSoftWarps * kMergeFloats of O
-  static constexpr int MERGE = WIDE ? 0 : kSoftWarps * (32 * 8 + kMergeFloats * 4);
   static constexpr int BUDGET = 227 * 1024 - 1024 - 1536;  // alignment, static shared memory
-  static constexpr int FIT = (BUDGET - MT * SLOT - MERGE) / SLOT;
+  static constexpr int FIT = (BUDGET - MT * SLOT) / SLOT;
   static constexpr int NST = FIT < kMaxSlots ? FIT : kMaxSlots;
-  static constexpr int SMEM = 1024 + MT * SLOT + NST * SLOT + MERGE;
+  static constexpr int SMEM = 1024 + MT * SLOT + NST * SLOT;
   static_assert(NST >= 5, "K and V of two tiles and one more");
   static_assert(SMEM > 114 * 1024, "one CTA per SM: it holds all of the SM's tensor memory");
 };
@@ -76,7 +65,7 @@ struct Piece {
   int step0;           // tiles of the CTA's range before the piece
   int kvh;
   int b, q0, row0, rows, pos0, L, lo, hi;
-  int ga[2], gb[2];    // group g's tiles (wide)
+  int ga[2], gb[2];    // group g's tiles
   int whole, slot;     // the whole unit; else the slot of its partial
 };
 
@@ -85,19 +74,13 @@ struct Shared {
   uint64_t qfull, qempty;
   uint64_t sfull[2], pfull[2], ofull[2];
   uint64_t pc_full[kPieces], pc_empty[kPieces];
-  uint64_t merge_bar, drain_bar;
+  uint64_t drain_bar;
   Piece pc[kPieces];
   uint32_t tmem;
   volatile int abort_flag;
 };
 
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
-
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // What a row of a piece sees and how its scores are biased.
 struct Row {
@@ -226,17 +209,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                         const __grid_constant__ CUtensorMap tmq, const AttnParams p) {
   constexpr int D = C::D, BS = C::BS, DCH = C::DCH, NST = C::NST;
-  constexpr bool WIDE = C::WIDE;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem + C::MT * C::SLOT;
-  float2* part_ml = reinterpret_cast<float2*>(ring + NST * C::SLOT);  // [kSoftWarps][32]
-  float* merge = reinterpret_cast<float*>(part_ml + kSoftWarps * 32);
   __shared__ __align__(16) Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = blockIdx.x;
-  const int HR = WIDE ? p.RT / 2 : p.RT;  // rows of an M tile
+  const int HR = p.HR;  // rows of an M tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -254,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&sh.pc_full[i]), 1);
       mbar_init(smem_addr(&sh.pc_empty[i]), kPieceUsers);
     }
-    mbar_init(smem_addr(&sh.merge_bar), kSoftWarps * 32);
     mbar_init(smem_addr(&sh.drain_bar), 1);
     sh.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -264,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // rows of the Q tiles that no load covers: finite scores for them (their P is never used)
   for (int e = threadIdx.x; e < C::MT * DCH * 128 * 8; e += kThreads) {
     const int row = (e >> 3) & 127;
-    if ((WIDE ? row : row & 31) >= HR) *reinterpret_cast<uint4*>(smem + e * 16) = make_uint4(0, 0, 0, 0);
+    if (row >= HR) *reinterpret_cast<uint4*>(smem + e * 16) = make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
   if (threadIdx.x == kLoadWarp * 32) {
@@ -359,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kLoadWarp) {
       // ============================ K and V tiles ============================
       constexpr int BPT = kKT / BS;  // blocks per tile, at most 16
-      const uint64_t policy = WIDE ? l2_policy_evict_normal() : l2_policy_evict_first();
+      const uint64_t policy = l2_policy_evict_normal();
       bool ok = true;
       int slot = 0;
       uint32_t phase = 0, used = 0;  // of the next load; slots in use (bits) once round
@@ -432,13 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i > 0 && !(ok = wait_warp(smem_addr(&sh.qempty), (i - 1) & 1, p.err, abort_flag))) break;
         if (lane == 0) {
           const uint32_t bar = smem_addr(&sh.qfull), q = smem_addr(smem);
-          const int tiles = WIDE ? (rows > HR ? 2 : 1) : 4;
+          const int tiles = rows > HR ? 2 : 1;
           mbar_arrive_expect_tx(bar, box * DCH * tiles);
           for (int m = 0; m < tiles; ++m)
 #pragma unroll
             for (int c = 0; c < DCH; ++c)
-              tma_load_3d(q + (WIDE ? m * C::SLOT : m * 4096) + c * C::CHUNK, &tmq, c * 64, kvh * p.G,
-                          tok + (WIDE ? m * ht : 0), bar, policy);
+              tma_load_3d(q + m * C::SLOT + c * C::CHUNK, &tmq, c * 64, kvh * p.G,
+                          tok + m * ht, bar, policy);
         }
         __syncwarp();
       }
@@ -447,14 +426,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ============================ products ============================
       constexpr uint32_t id_s = tc05::instr_desc_bf16(128, kKT, 0);
       constexpr uint32_t id_pv = tc05::instr_desc_bf16(128, D, 1);
-      // A cursor over the sub-steps: tile by tile, and for the wide shape group 0 then group 1.
+      // A cursor over the sub-steps: tile by tile, group 0 then group 1.
       // All it needs lies in registers, ring slots are counted rather than divided: this loop is
       // the latency between a group's P and its next S.
       struct Cursor {
         int n = 0, j = 0, g = 0, cnt = 0;  // piece, tile, group; tiles of the piece
         int slot = 0;                      // the tile's ring slot
         uint32_t phase = 0;
-        int a0 = 0, b0 = 0, a1 = 0, b1 = 0;  // the groups' tiles (wide)
+        int a0 = 0, b0 = 0, a1 = 0, b1 = 0;  // the groups' tiles
         int lo = 0, hi = 0;                  // the item's keys from the piece's first tile on
       };
       Cursor sc, pv;
@@ -474,22 +453,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int k0 = uni(pc.kt0) * kKT;
         c.lo = uni(pc.lo) - k0;
         c.hi = uni(pc.hi) - k0;
-        if (WIDE) {
-          c.g = 0;
-          c.a0 = uni(pc.ga[0]);
-          c.b0 = uni(pc.gb[0]);
-          c.a1 = uni(pc.ga[1]);
-          c.b1 = uni(pc.gb[1]);
-        } else {
-          c.g = uni(pc.step0) & 1;
-        }
+        c.g = 0;
+        c.a0 = uni(pc.ga[0]);
+        c.b0 = uni(pc.gb[0]);
+        c.a1 = uni(pc.ga[1]);
+        c.b1 = uni(pc.gb[1]);
       };
       auto group_active = [&](const Cursor& c) {
-        return !WIDE || (c.g ? c.j >= c.a1 && c.j < c.b1 : c.j >= c.a0 && c.j < c.b0);
+        return c.g ? c.j >= c.a1 && c.j < c.b1 : c.j >= c.a0 && c.j < c.b0;
       };
       auto advance = [&](Cursor& c) {  // true: the tile is finished
         c.g ^= 1;
-        if (WIDE && c.g) return false;
+        if (c.g) return false;
         ++c.j;
         c.slot += 2;
         if (c.slot >= NST) {
@@ -525,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int g = sc.g;
             if (group_active(sc)) {
               tc05::fence_after_sync();
-              const uint64_t dq = tc05::smem_desc(smem_addr(smem) + (WIDE ? g * C::SLOT : 0), 16, 1024);
+              const uint64_t dq = tc05::smem_desc(smem_addr(smem) + g * C::SLOT, 16, 1024);
               const uint64_t dk = tc05::smem_desc(smem_addr(ring) + sc.slot * C::SLOT, 16, 1024);
               const uint32_t ts = tmem + kColS + g * kGroupCols;
 #pragma unroll
@@ -559,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g = pv.g;
         // the item's keys within the tile
         const int a = max(pv.lo - pv.j * kKT, 0), z = min(pv.hi - pv.j * kKT, kKT);
-        if (!WIDE || g == 0) {
+        if (g == 0) {
           if (!(ok = wait_warp(smem_addr(&sh.full[pv.slot]), pv.phase, p.err, abort_flag))) break;
           // V rows outside the item's keys may hold anything (0 * Inf is NaN): zero those that
           // the product reads, up to the 16-key steps
@@ -583,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t dv = tc05::smem_desc(smem_addr(ring) + pv.slot * C::SLOT, C::CHUNK, 1024);
           const uint32_t tp = tmem + kColS + g * kGroupCols, to = tmem + kColO + g * kGroupCols;
           // the group's first tile of the piece overwrites O
-          const bool fresh = WIDE ? pv.j == (g ? pv.a1 : pv.a0) : pv.j < 2;
+          const bool fresh = pv.j == (g ? pv.a1 : pv.a0);
           const int s0 = a >> 4, s1 = (z + 15) >> 4;
           if (s0 == 0 && s1 == kKT / 16) {
 #pragma unroll
@@ -594,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = s0; k < s1; ++k)
               tc05::mma_ts_warp(to, tp + 8 * k, dv + (k * 2048 >> 4), id_pv, k > s0 || !fresh);
           }
-          if (WIDE ? pv.j == (g ? pv.b1 : pv.b0) - 1 : pv.j + 2 >= pv.cnt) tc05::commit_warp(smem_addr(&sh.ofull[g]));
+          if (pv.j == (g ? pv.b1 : pv.b0) - 1) tc05::commit_warp(smem_addr(&sh.ofull[g]));
         }
         const uint32_t eb = smem_addr(&sh.empty[pv.slot]);
         if (advance(pv)) {
@@ -624,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
     const bool plain = p.cap_out == 0.f && !p.slopes && p.scale_log2 > 0.f;
     const float mul = plain ? p.scale_log2 : 1.f;
-    const int r = WIDE ? 32 * w + lane : lane;  // row of the M tile
+    const int r = 32 * w + lane;  // row of the M tile
 
     // items whose rows see nothing have no tile: their rows are zero
     const int items = p.header[0];
@@ -644,25 +619,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
-    int done = 0, pieces = 0, merges = 0;  // phases of sfull, ofull and merge_bar
+    int done = 0, pieces = 0;  // phases of sfull and ofull
     bool ok = true;
     for (int i = 0; ok; ++i) {
       if (!(ok = piece_wait(i))) break;
       const Piece& pc = sh.pc[i % kPieces];
       const int cnt = pc.cnt;
       if (cnt == 0) break;
-      const int rows = min(HR, pc.rows - (WIDE ? g * HR : 0));  // of this M tile
-      const int f = pc.row0 + (WIDE ? g * HR : 0) + min(r, max(rows, 1) - 1);
+      const int rows = min(HR, pc.rows - g * HR);  // of this M tile
+      const int f = pc.row0 + g * HR + min(r, max(rows, 1) - 1);
       Row row{0, 0, 0, 0.f};
       if (rows > 0) row = row_of(p, pc, f);
-      int ja = 0, jb = cnt, jstep = 1;
-      if (WIDE) {
-        ja = pc.ga[g];
-        jb = pc.gb[g];
-      } else {
-        ja = (pc.step0 & 1) == g ? 0 : 1;
-        jstep = 2;
-      }
+      const int ja = pc.ga[g], jb = pc.gb[g];
       const bool active = ja < jb;
       int all_lo = row.lo, all_hi = row.hi;  // keys that every row of the warp sees
 #pragma unroll
@@ -672,23 +640,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // reference maximum, sum, and the maximum seen (the reference may lag by kOverflowLog2)
       float m_ref = -INFINITY, l = 0.f, m_next = -INFINITY;
-      for (int j = ja; j < jb; j += jstep, ++done) {
+      for (int j = ja; j < jb; ++j, ++done) {
         if (!(ok = wait_warp(smem_addr(&sh.sfull[g]), done & 1, p.err, abort_flag))) break;
         tc05::fence_after_sync();
-        if (WIDE && 32 * w >= rows) {  // none of the warp's rows is a row of the item
+        if (32 * w >= rows) {  // none of the warp's rows is a row of the item
           tc05::fence_before_sync();
           mbar_arrive(smem_addr(&sh.pfull[g]));
           continue;
         }
-        // The wide shape takes a tile's 128 columns in two halves, so that the scores and what
+        // A tile's 128 columns are taken in two halves, so that the scores and what
         // their modification needs stay in registers.  The reference maximum is that of the first
         // half and the tiles before; the second half moves it only where its weights might
         // overflow (the first half's P would have to be rescaled, and is), else the next tile does.
-        constexpr int N = WIDE ? 64 : 32, NH = WIDE ? 2 : 1;
+        constexpr int N = 64;
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll 1  // (one copy of the code: instruction fetches bound two)
-        for (int h = 0; h < NH; ++h) {
-          const int col = WIDE ? N * h : 32 * w;  // first column
+        for (int h = 0; h < 2; ++h) {
+          const int col = N * h;  // first column
           const int key0 = (pc.kt0 + j) * kKT + col;
           uint32_t raw[N / 32][32];
 #pragma unroll
@@ -741,15 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (e & 1) l1 = __fadd2_rn(l1, y); else l0 = __fadd2_rn(l0, y);
               v[e] = pack_bf16x2(y.x, y.y);
             }
-            tc05::st16(ts + (WIDE ? (col + c) / 2 : 16 * w), v);
+            tc05::st16(ts + (col + c) / 2, v);
           }
-        }
-        if (!WIDE) {  // zero outside this warp's columns
-          uint32_t v[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = 0u;
-#pragma unroll
-          for (int c = 1; c < 4; ++c) tc05::st16(ts + 16 * ((w + c) & 3), v);
         }
         l += (l0.x + l0.y) + (l1.x + l1.y);
         tc05::wait_st();
@@ -766,110 +727,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++pieces;
         tc05::fence_after_sync();
       }
-      if constexpr (WIDE) {
-        if (rows > 0) {
-          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
-          const int t = f / p.G;
-          __nv_bfloat16* o =
-              out + (static_cast<int64_t>(pc.q0 + t) * p.Hq + pc.kvh * p.G + (f - t * p.G)) * D;
-          const int pr = g * HR + r;  // row of the partial
-          if (!whole && r < rows) reinterpret_cast<float2*>(p.part_ml)[base * p.RT + pr] = make_float2(m_ref, l);
+      if (rows > 0) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays
+        const int t = f / p.G;
+        __nv_bfloat16* o =
+            out + (static_cast<int64_t>(pc.q0 + t) * p.Hq + pc.kvh * p.G + (f - t * p.G)) * D;
+        const int pr = g * HR + r;  // row of the partial
+        if (!whole && r < rows) reinterpret_cast<float2*>(p.part_ml)[base * p.RT + pr] = make_float2(m_ref, l);
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t v[32];
-            if (active) {
-              tc05::ld32(to + c, v);
-              tc05::wait_ld();
-            } else {
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          if (active) {
+            tc05::ld32(to + c, v);
+            tc05::wait_ld();
+          } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = 0u;
-            }
-            if (r < rows) {
-              if (whole) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  auto at = [&](int u) { return __uint_as_float(v[e + u]) * inv; };
-                  *reinterpret_cast<uint4*>(o + c + e) =
-                      make_uint4(pack_bf16x2(at(0), at(1)), pack_bf16x2(at(2), at(3)), pack_bf16x2(at(4), at(5)),
-                                 pack_bf16x2(at(6), at(7)));
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  reinterpret_cast<float4*>(p.part_acc)[(base * (D / 4) + (c + e) / 4) * p.RT + pr] =
-                      make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]),
-                                  __uint_as_float(v[e + 3]));
-              }
-            }
-            __syncwarp();
+            for (int e = 0; e < 32; ++e) v[e] = 0u;
           }
-        }
-        tc05::fence_before_sync();  // the reads of O come before the next piece's products
-      } else {
-        // merge the eight parts of each row by log-sum-exp, CC columns of O at a time
-        auto sync = [&] {
-          mbar_arrive(smem_addr(&sh.merge_bar));
-          return wait_warp(smem_addr(&sh.merge_bar), merges++ & 1, p.err, abort_flag);
-        };
-        part_ml[warp * 32 + lane] = make_float2(m_ref, l);
-        if (!(ok = sync())) break;
-        float M = -INFINITY, l_all = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSoftWarps; ++k) M = fmaxf(M, part_ml[k * 32 + lane].x);
-        const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-        for (int k = 0; k < kSoftWarps; ++k)
-          l_all += part_ml[k * 32 + lane].y * ex2_approx(part_ml[k * 32 + lane].x - ref);
-        const float e_own = ex2_approx(m_ref - ref);
-        const float inv = l_all > 0.f ? 1.f / l_all : (l_all == 0.f ? 0.f : l_all);  // NaN stays
-        const float k_own = whole ? e_own * inv : e_own;
-        if (!whole && warp == 0 && lane < rows)
-          reinterpret_cast<float2*>(p.part_ml)[base * p.RT + lane] = make_float2(M, l_all);
-        const int CC = min(D, HR <= 4 ? 128 : HR <= 8 ? 64 : HR <= 16 ? 32 : 16);  // HR (CC + 1) <= kMergeFloats
-        const int half = CC / 2;
-        for (int c0 = 0; c0 < D; c0 += CC) {
-          for (int c = c0 & ~31; c < c0 + CC; c += 32) {
-            uint32_t v[32];
-            if (active) {
-              tc05::ld32(to + c, v);
-              tc05::wait_ld();
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = 0u;
-            }
-            if (lane < rows) {
-              float* mine = merge + warp * kMergeFloats + lane * (CC + 1) + (c - c0);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c + e >= c0 && c + e < c0 + CC) mine[e] = __uint_as_float(v[e]) * k_own;
-            }
-            __syncwarp();
-          }
-          if (!(ok = sync())) break;
-          for (int e = threadIdx.x; e < rows * half; e += kSoftWarps * 32) {
-            const int rr = e / half, cc = (e - rr * half) * 2;
-            float a = 0.f, b = 0.f;
-#pragma unroll
-            for (int k = 0; k < kSoftWarps; ++k) {
-              a += merge[k * kMergeFloats + rr * (CC + 1) + cc];
-              b += merge[k * kMergeFloats + rr * (CC + 1) + cc + 1];
-            }
-            const int col = c0 + cc;
+          if (r < rows) {
             if (whole) {
-              const int ff = pc.row0 + rr, t = ff / p.G;
-              *reinterpret_cast<uint32_t*>(
-                  out + (static_cast<int64_t>(pc.q0 + t) * p.Hq + pc.kvh * p.G + (ff - t * p.G)) * D + col) =
-                  pack_bf16x2(a, b);
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                auto at = [&](int u) { return __uint_as_float(v[e + u]) * inv; };
+                *reinterpret_cast<uint4*>(o + c + e) =
+                    make_uint4(pack_bf16x2(at(0), at(1)), pack_bf16x2(at(2), at(3)), pack_bf16x2(at(4), at(5)),
+                               pack_bf16x2(at(6), at(7)));
+              }
             } else {
-              *reinterpret_cast<float2*>(p.part_acc + ((base * (D / 4) + col / 4) * p.RT + rr) * 4 + col % 4) =
-                  make_float2(a, b);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                reinterpret_cast<float4*>(p.part_acc)[(base * (D / 4) + (c + e) / 4) * p.RT + pr] =
+                    make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]),
+                                __uint_as_float(v[e + 3]));
             }
           }
-          if (!(ok = sync())) break;
+          __syncwarp();
         }
-        if (!ok) break;
-        tc05::fence_before_sync();
       }
+      tc05::fence_before_sync();  // the reads of O come before the next piece's products
       piece_done(i);
     }
     if (!ok) *abort_flag = 1;
@@ -886,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <class C>
 cudaError_t run(const AttnParams& p, cudaStream_t stream) {
   CUtensorMap tmk, tmv, tmq;
-  const int tokens = (C::WIDE ? p.RT / 2 : p.RT) / p.G;
+  const int tokens = p.HR / p.G;
   if (!make_pool_map(&tmk, p.k_pool, p.num_blocks, C::BS, p.Hkv, C::D, C::BS) ||
       !make_pool_map(&tmv, p.v_pool, p.num_blocks, C::BS, p.Hkv, C::D, C::BS) ||
       !make_q_rows_map(&tmq, p.q, p.T, p.Hq, C::D, p.q_stride, p.G, tokens))
@@ -906,28 +801,19 @@ cudaError_t run(const AttnParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, attention_tc_kernel<C>, tmk, tmv, tmq, p);
 }
 
-template <int D, int BS>
-cudaError_t run_shape(const AttnParams& p, cudaStream_t stream) {
-  return p.RT > 32 ? run<TcAttn<D, BS, true>>(p, stream) : run<TcAttn<D, BS, false>>(p, stream);
-}
-
 }  // namespace
 
-// Rows per item of the tensor-core kernel: one narrow item of whole tokens where every sequence's
-// query tokens fit into 32 rows, else two M tiles.
-int attention_tc_rows(int max_query_len, int G) {
-  const int narrow = G <= 32 ? 32 / G : 0;
-  return max_query_len <= narrow ? max_query_len * G : 2 * (128 / G) * G;
-}
+// Rows per item: two M tiles of whole tokens.
+int attention_tc_rows(int G) { return 2 * (128 / G) * G; }
 
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t stream) {
   switch (p.D * 100 + p.block_size) {
-    case 6408: return run_shape<64, 8>(p, stream);
-    case 6416: return run_shape<64, 16>(p, stream);
-    case 6432: return run_shape<64, 32>(p, stream);
-    case 12808: return run_shape<128, 8>(p, stream);
-    case 12816: return run_shape<128, 16>(p, stream);
-    case 12832: return run_shape<128, 32>(p, stream);
+    case 6408: return run<TcAttn<64, 8>>(p, stream);
+    case 6416: return run<TcAttn<64, 16>>(p, stream);
+    case 6432: return run<TcAttn<64, 32>>(p, stream);
+    case 12808: return run<TcAttn<128, 8>>(p, stream);
+    case 12816: return run<TcAttn<128, 16>>(p, stream);
+    case 12832: return run<TcAttn<128, 32>>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }

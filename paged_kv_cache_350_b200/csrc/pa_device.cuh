@@ -207,6 +207,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// 1 / x by the SFU's approximation (relative error about 2^-23).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 3-D tiled TMA load into shared memory, completing on the mbarrier at `bar`.
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c0,
                                             int c1, int c2, int c3, int c4, uint32_t bar,

@@ -126,7 +126,7 @@ struct RopeParams {
 };
 cudaError_t launch_rope(const RopeParams& p, pa_dtype dtype, cudaStream_t stream);
 
-// Attention of ragged query tokens (attention.cu, attention_tc.cu).
+// Attention of ragged query tokens (attention.cu, attention_tc.cu, attention_tokens.cu).
 struct AttnItem;
 struct AttnStart;
 struct AttnParams {
@@ -161,7 +161,10 @@ struct AttnParams {
 cudaError_t launch_attention_plan(const AttnParams& p, cudaStream_t stream);
 cudaError_t launch_attention_generic(const AttnParams& p, pa_dtype dtype, cudaStream_t stream);
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t stream);
-int attention_tc_rows(int max_query_len, int G);
+int attention_tc_rows(int G);
+cudaError_t launch_attention_tokens(const AttnParams& p, cudaStream_t stream);  // its join included
+bool attention_tokens_eligible(int max_query_len, int G, int B);
+int attention_tokens_ranges(int sms);
 cudaError_t launch_attention_join(const AttnParams& p, pa_dtype dtype, cudaStream_t stream);
 int attention_generic_ctas_per_sm(int RT, int D);
 

@@ -43,6 +43,18 @@ __device__ __forceinline__ uint32_t sw128(int row, int c16) {
   return static_cast<uint32_t>(row * 128 + ((c16 ^ (row & 7)) << 4));
 }
 
+// What the tile math makes of a raw score: the log2-domain score of key `key` of the tile for the
+// lane's row 0 or 1 (tile_t: rows 2 tig, 2 tig + 1; tile: rows g, g + 8), -inf where masked.
+// kEmptyRows: a tile may hold no key at all for a row.
+struct ScaledScore {
+  static constexpr bool kEmptyRows = false;
+  float sl2;
+  int valid;
+  __device__ __forceinline__ float operator()(float s, int key, int) const {
+    return key < valid ? s * sl2 : -INFINITY;
+  }
+};
+
 // Online-softmax state and output accumulator of one warp for one (sequence, KV head).
 // Lane (g = lane/4, tig = lane%4) owns rows g (and g+8 with ROWS16) and output columns
 // 8j + 2tig, 8j + 2tig + 1 of every n-tile j.
@@ -165,6 +177,7 @@ struct WarpAcc {
 
   // One online-softmax row update for scores x0..x3 (tokens 2tig, 2tig+1, 8+2tig, 9+2tig).
   // A masked row takes no part in this tile: its state is kept and its P is zero.
+  template <bool EMPTY = false>
   __device__ __forceinline__ static float row_update(float x0, float x1, float x2, float x3,
                                                      float& m, float& l, uint32_t& hi0,
                                                      uint32_t& lo0, uint32_t& hi2,
@@ -177,9 +190,12 @@ struct WarpAcc {
       hi0 = lo0 = hi2 = lo2 = 0u;
       return 1.f;
     }
-    const float m_new = fmaxf(m, mx);
+    float m_new = fmaxf(m, mx);
+    if constexpr (EMPTY) {  // no key yet: every weight is 0, the maximum stays
+      if (m_new == -INFINITY) m_new = 0.f;
+    }
     const float alpha = exp2f(m - m_new);
-    m = m_new;
+    m = EMPTY ? fmaxf(m, mx) : m_new;
     const float e0 = exp2f(x0 - m_new), e1 = exp2f(x1 - m_new);
     const float e2 = exp2f(x2 - m_new), e3 = exp2f(x3 - m_new);
     split_bf16x2(e0, e1, hi0, lo0);
@@ -195,8 +211,15 @@ struct WarpAcc {
   __device__ __forceinline__ void tile(uint32_t kbase, int valid, float sl2, int lane,
                                        int row_lo = 0, int row_hi = 16) {
     static_assert(!ROWMASK || C::ROWS16, "row masks are kept for 16-row tiles only");
+    tile_scores<ROWMASK>(kbase, valid, ScaledScore{sl2, valid}, lane, row_lo, row_hi);
+  }
+
+  // The same with the scores as `score` makes them.
+  template <bool ROWMASK = false, class Score>
+  __device__ __forceinline__ void tile_scores(uint32_t kbase, int valid, const Score& score, int lane,
+                                              int row_lo = 0, int row_hi = 16) {
     if constexpr (!C::ROWS16) {
-      tile_t(kbase, valid, sl2, lane);
+      tile_t(kbase, valid, score, lane);
       return;
     }
     const uint32_t vbase = kbase + C::TILE_BYTES;
@@ -222,23 +245,21 @@ struct WarpAcc {
         mma_bf16_16816(s1[0], s1[1], s1[2], s1[3], a0, a1, a2, a3, b10, b11, s1[0], s1[1], s1[2],
                        s1[3]);
       }
-      const int lim = valid - r0;
-      const bool v0 = 2 * tig < lim, v1 = 2 * tig + 1 < lim;
-      const bool v2 = 8 + 2 * tig < lim, v3 = 9 + 2 * tig < lim;
+      const int k0 = r0 + 2 * tig;
       uint32_t pa0, pa1 = 0u, pa2, pa3 = 0u;   // P hi parts (A fragment registers)
       uint32_t pr0, pr1 = 0u, pr2, pr3 = 0u;   // P lo parts
       const int gr = lane >> 2;
       const bool mask_lo = ROWMASK && (gr < row_lo || gr >= row_hi);
       const bool mask_hi = ROWMASK && (gr + 8 < row_lo || gr + 8 >= row_hi);
       const float alpha_lo =
-          row_update(v0 ? s0[0] * sl2 : -INFINITY, v1 ? s0[1] * sl2 : -INFINITY,
-                     v2 ? s1[0] * sl2 : -INFINITY, v3 ? s1[1] * sl2 : -INFINITY, m_lo, l_lo,
-                     pa0, pr0, pa2, pr2, mask_lo);
+          row_update<Score::kEmptyRows>(score(s0[0], k0, 0), score(s0[1], k0 + 1, 0),
+                                        score(s1[0], k0 + 8, 0), score(s1[1], k0 + 9, 0), m_lo,
+                                        l_lo, pa0, pr0, pa2, pr2, mask_lo);
       float alpha_hi = 1.f;
       if constexpr (C::ROWS16)
-        alpha_hi = row_update(v0 ? s0[2] * sl2 : -INFINITY, v1 ? s0[3] * sl2 : -INFINITY,
-                              v2 ? s1[2] * sl2 : -INFINITY, v3 ? s1[3] * sl2 : -INFINITY, m_hi,
-                              l_hi, pa1, pr1, pa3, pr3, mask_hi);
+        alpha_hi = row_update<Score::kEmptyRows>(score(s0[2], k0, 1), score(s0[3], k0 + 1, 1),
+                                                 score(s1[2], k0 + 8, 1), score(s1[3], k0 + 9, 1),
+                                                 m_hi, l_hi, pa1, pr1, pa3, pr3, mask_hi);
 #pragma unroll
       for (int j = 0; j < C::NT; ++j) {
         o_lo[j][0] *= alpha_lo;
@@ -288,7 +309,8 @@ struct WarpAcc {
   // 8 lanes of a column by shuffles, sums per lane until reduce_l), and movmatrix
   // transposes P back into A-operand layout (heads as rows) for O += P.V.  P.V then runs
   // as in tile(), with the lo part of P in the A rows 8-15 and its products in o_hi.
-  __device__ __forceinline__ void tile_t(uint32_t kbase, int valid, float sl2, int lane) {
+  template <class Score>
+  __device__ __forceinline__ void tile_t(uint32_t kbase, int valid, const Score& score, int lane) {
     constexpr unsigned kFull = 0xffffffffu;
     const uint32_t vbase = kbase + C::TILE_BYTES;
     const int g = lane >> 2;
@@ -312,21 +334,25 @@ struct WarpAcc {
         q_frag(k, lane, q0, q1, q2, q3);
         mma_bf16_16816(c0, c1, c2, c3, a0, a1, a2, a3, q0, q2, c0, c1, c2, c3);
       }
-      const bool va = r0 + g < valid, vb = r0 + g + 8 < valid;
-      const float x0 = va ? c0 * sl2 : -INFINITY;  // token g,   head 2tig
-      const float x1 = va ? c1 * sl2 : -INFINITY;  // token g,   head 2tig+1
-      const float x2 = vb ? c2 * sl2 : -INFINITY;  // token g+8, head 2tig
-      const float x3 = vb ? c3 * sl2 : -INFINITY;  // token g+8, head 2tig+1
+      const float x0 = score(c0, r0 + g, 0);      // token g,   head 2tig
+      const float x1 = score(c1, r0 + g, 1);      // token g,   head 2tig+1
+      const float x2 = score(c2, r0 + g + 8, 0);  // token g+8, head 2tig
+      const float x3 = score(c3, r0 + g + 8, 1);  // token g+8, head 2tig+1
       float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, off));
         mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, off));
       }
-      const float mn0 = fmaxf(mh[0], mx0), mn1 = fmaxf(mh[1], mx1);  // token r0 is valid
+      float mn0 = fmaxf(mh[0], mx0), mn1 = fmaxf(mh[1], mx1);
+      const float top0 = mn0, top1 = mn1;
+      if constexpr (Score::kEmptyRows) {  // no key yet: every weight is 0 (else token r0 is valid)
+        if (mn0 == -INFINITY) mn0 = 0.f;
+        if (mn1 == -INFINITY) mn1 = 0.f;
+      }
       const float al0 = exp2f(mh[0] - mn0), al1 = exp2f(mh[1] - mn1);
-      mh[0] = mn0;
-      mh[1] = mn1;
+      mh[0] = top0;
+      mh[1] = top1;
       const float e0 = exp2f(x0 - mn0), e1 = exp2f(x1 - mn1);
       const float e2 = exp2f(x2 - mn0), e3 = exp2f(x3 - mn1);
       lh[0] = lh[0] * al0 + (e0 + e2);
@@ -397,20 +423,26 @@ struct WarpAcc {
   }
 };
 
-// Zero the V rows [valid, TILE_T) of a staged tile (their slots may hold anything), then
-// order those generic-proxy writes before later TMA writes to the same stage.
+// Zero the V rows [from, to) of a staged tile (their slots may hold anything), then order
+// those generic-proxy writes before later TMA writes to the same stage.
 template <class C>
-__device__ __forceinline__ void zero_tail_rows(uint8_t* stage_ptr, int valid, int lane) {
+__device__ __forceinline__ void zero_rows(uint8_t* stage_ptr, int from, int to, int lane) {
   uint8_t* vt = stage_ptr + C::TILE_BYTES;
-  const int nchunks = (C::TILE_T - valid) * C::DCH * 8;
+  const int nchunks = (to - from) * C::DCH * 8;
   for (int i = lane; i < nchunks; i += 32) {
-    const int r = valid + i / (C::DCH * 8);
+    const int r = from + i / (C::DCH * 8);
     const int rem = i % (C::DCH * 8);
     *reinterpret_cast<uint4*>(vt + (rem >> 3) * C::CHUNK_BYTES + r * 128 + (rem & 7) * 16) =
         make_uint4(0u, 0u, 0u, 0u);
   }
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// The rows from `valid` on.
+template <class C>
+__device__ __forceinline__ void zero_tail_rows(uint8_t* stage_ptr, int valid, int lane) {
+  zero_rows<C>(stage_ptr, valid, C::TILE_T, lane);
 }
 
 }  // namespace pa
