@@ -7,7 +7,7 @@
 // 256 rows.  Group g skips the tiles that none of its rows sees.
 //
 // Warps: 0-7 softmax (group g = warps 4g .. 4g + 3, a thread per row), 8 MMA, 9 K/V loads, 10
-// schedule, 11 Q loads.  The schedule warp writes records of the CTA's pieces (a piece is the part
+// schedule and Q loads.  The schedule warp writes records of the CTA's pieces (a piece is the part
 // of a unit in the range) into a small ring that all others follow.  K and V tiles share a ring
 // of slots in load order (K0 V0 K1 V1 ..), one TMA box per block and 64-column chunk.
 //
@@ -35,17 +35,22 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kKT = 128;        // keys per tile
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10, kQWarp = 11;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;  // (11 only rounds up the warpgroup)
+// Registers of a softmax thread and of another one: together what 384 threads are launched with.
+constexpr int kSoftRegs = 208, kOtherRegs = 88;
 constexpr int kPieces = 4;      // records in flight
 constexpr int kMaxSlots = 10;
-constexpr float kRescaleLog2 = 8.f, kOverflowLog2 = 64.f;
+constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kColS = 0, kColO = 256, kGroupCols = 128, kTmemCols = 512;
-// released by the MMA warp, the two load warps and each softmax warp
-constexpr int kPieceUsers = 3 + kSoftWarps;
+// released by the MMA warp, the K/V load warp and each softmax warp
+constexpr int kPieceUsers = 2 + kSoftWarps;
 
-template <int D_, int BS_>
+// CAP, BIAS: what is done to the scores, fixed at compile time so that the loop of a call is short
+// straight code (instruction fetches bound the kernel that decided at run time).
+template <int D_, bool CAP_, bool BIAS_>
 struct TcAttn {
-  static constexpr int D = D_, BS = BS_;
+  static constexpr int D = D_;
+  static constexpr bool CAP = CAP_, BIAS = BIAS_;
   static constexpr int MT = 2;                        // M tiles of an item
   static constexpr int DCH = D / 64;
   static constexpr int CHUNK = kKT * 128;             // one 64-column chunk of 128 rows
@@ -72,7 +77,7 @@ struct Piece {
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t qfull, qempty;
-  uint64_t sfull[2], pfull[2], ofull[2];
+  uint64_t sfull[2], pfull[2][2], ofull[2];  // per group; P in two halves
   uint64_t pc_full[kPieces], pc_empty[kPieces];
   uint64_t drain_bar;
   Piece pc[kPieces];
@@ -99,16 +104,20 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, const Piece& pc, int 
   return r;
 }
 
-// Turn N raw scores (keys key0 .. of one row) into log2-domain scores in place and return their
+// Turn the N raw scores of a row (keys key0 ..) into log2-domain scores in place and return their
 // maximum.  The plain case keeps raw scores, so that the scale and the subtraction of the maximum
-// become one operation.  Elements are taken 8 at a time, step by step, so that the steps of one
-// element do not wait for each other.
-template <int N>
+// become one operation.  `ahead`: some of the keys may lie behind the row's position and count.
+//
+// One operation per element costs a warp 128 cycles a tile, two warps share a sub-partition and the
+// products of a pair of tiles take 2048: operations are counted here.  So are instructions: once
+// the loop of all roles is larger than the 32 KB that instructions are kept in, each takes three
+// times as long.  Two-element forms take as long as two scalar ones, but half the instructions.
+template <bool CAP, bool BIAS, int N>
 __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& p, const Row& r, int key0,
-                                               bool plain, bool masked) {
-  constexpr int E = 8;
+                                               bool masked, bool ahead) {
+  constexpr int E = 8;  // elements taken step by step, so that the steps of one do not wait
   const int a = r.lo - key0, b = r.hi - key0;
-  if (p.cap_out > 0.f) {
+  if constexpr (CAP) {
     if (masked) {  // what lies in masked columns must not choose the branch below
 #pragma unroll
       for (int j = 0; j < N; ++j) x[j] = j >= a && j < b ? x[j] : 0.f;
@@ -120,10 +129,15 @@ __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& 
       for (int e = 0; e < 4; ++e) ax[e] = fmaxf(ax[e], fmaxf(fabsf(x[j + 2 * e]), fabsf(x[j + 2 * e + 1])));
     // (a NaN fails the comparison only if it is all there is; both ways carry it through)
     const float top = fmaxf(fmaxf(ax[0], ax[1]), fmaxf(ax[2], ax[3]));
-    if (__all_sync(kFull, top * fabsf(p.cap_in) <= 1.f)) {
-      // tanh(t) / t as a polynomial in t^2 (iterated reweighted least squares on |t| <= 1, where
-      // |t P(t^2) - tanh t| < 2.4e-7): on the FMA pipe alone, the exponentials need the other
-      const float2 ci = splat(p.cap_in), co = splat(p.cap_out);
+    if (__all_sync(kFull, top * fabsf(p.cap_in) <= 0.85f)) {
+      // tanh(t) / t as a polynomial in t^2 (iterated reweighted least squares on |t| <= 0.85, where
+      // |t P(t^2) - tanh t| < 6.9e-7 in 32 bits): on the FMA pipe alone, the exponentials need the
+      // other
+      const float2 ci = splat(p.cap_in);
+      const float co = p.cap_out;
+      const float2 c4 = splat(0.01063788216561079f * co), c3 = splat(-0.04714450612664223f * co),
+                   c2 = splat(0.13136771321296692f * co), c1 = splat(-0.3330950140953064f * co),
+                   c0 = splat(0.9999918341636658f * co);
 #pragma unroll
       for (int j = 0; j < N; j += E) {
         float2 t[E / 2], u[E / 2], y[E / 2];
@@ -132,17 +146,13 @@ __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& 
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) u[e] = __fmul2_rn(t[e], t[e]);
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(u[e], splat(-0.0028394642286f), splat(0.01611417718f));
+        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(u[e], c4, c3);
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], splat(-0.0509728603065f));
+        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c2);
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], splat(0.132535248995f));
+        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c1);
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], splat(-0.333240032196f));
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) t[e] = __fmul2_rn(t[e], co);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], splat(0.999996840954f));
+        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c0);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
           y[e] = __fmul2_rn(y[e], t[e]);
@@ -164,23 +174,25 @@ __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& 
         for (int e = 0; e < E; ++e) x[j + e] = fmaf(m2, u[e], p.cap_out);
       }
     }
-  } else if (!plain) {
-#pragma unroll
-    for (int j = 0; j < N; j += 2) {
-      const float2 y = __fmul2_rn(make_float2(x[j], x[j + 1]), splat(p.scale_log2));
-      x[j] = y.x;
-      x[j + 1] = y.y;
-    }
   }
-  if (p.slopes) {
+  if constexpr (BIAS) {
     const float d0 = static_cast<float>(r.pos - key0);
+    if (ahead) {
 #pragma unroll
-    for (int j = 0; j < N; j += E) {
-      float d[E];
+      for (int j = 0; j < N; ++j) {
+        const float y = CAP ? x[j] : x[j] * p.scale_log2;
+        x[j] = fmaf(-r.slope, fabsf(d0 - static_cast<float>(j)), y);
+      }
+    } else {  // |pos - key| = d0 - j
+      const float c0 = -r.slope * d0;
 #pragma unroll
-      for (int e = 0; e < E; ++e) d[e] = d0 - static_cast<float>(j + e);
+      for (int j = 0; j < N; j += E) {
+        float d[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[j + e] = fmaf(-r.slope, fabsf(d[e]), x[j + e]);
+        for (int e = 0; e < E; ++e) d[e] = fmaf(r.slope, static_cast<float>(j + e), c0);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[j + e] = CAP ? x[j + e] + d[e] : fmaf(x[j + e], p.scale_log2, d[e]);
+      }
     }
   }
   if (masked) {
@@ -208,7 +220,8 @@ template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                         const __grid_constant__ CUtensorMap tmq, const AttnParams p) {
-  constexpr int D = C::D, BS = C::BS, DCH = C::DCH, NST = C::NST;
+  constexpr int D = C::D, DCH = C::DCH, NST = C::NST;
+  const int BS = p.block_size;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -227,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_addr(&sh.qempty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.sfull[i]), 1);
-      mbar_init(smem_addr(&sh.pfull[i]), 128);
+      mbar_init(smem_addr(&sh.pfull[i][0]), 128);
+      mbar_init(smem_addr(&sh.pfull[i][1]), 128);
       mbar_init(smem_addr(&sh.ofull[i]), 1);
     }
     for (int i = 0; i < kPieces; ++i) {
@@ -269,15 +283,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(smem_addr(&sh.pc_empty[n % kPieces]));
   };
 
+  static_assert(256 * kSoftRegs + 128 * kOtherRegs <= kThreads * 168, "the launch's registers");
   if (warp >= kSoftWarps) {
-    setmaxnreg_dec<88>();
+    setmaxnreg_dec<kOtherRegs>();
     if (warp == kPlanWarp) {
-      // ============================ schedule ============================
+      // ============================ schedule, Q tiles ============================
       if (lane == 0) {
+        const uint64_t policy = l2_policy_evict_normal();
+        const int ht = HR / p.G;  // tokens of an M tile
+        const uint32_t box = static_cast<uint32_t>(HR) * 128;
+        bool ok = true;
         const int64_t per =
             (static_cast<int64_t>(p.header[1]) * p.Hkv + p.ctas - 1) / p.ctas;
         const AttnStart st = p.starts[s];
         int left = st.count, item = st.item, kvh = st.kvh, tile = st.tile, step = 0, n = 0;
+        int loaded = 0;  // Q loads issued
         int4 cut = make_int4(-1, 0, 0, 0);
         AttnItem it{};
         int sum = 0, nt = 0;
@@ -289,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (left > 0) load_item();
         for (;; ++n) {
           const int slot = n % kPieces;
-          if (n >= kPieces && !wait_or_abort(smem_addr(&sh.pc_empty[slot]), (n / kPieces - 1) & 1, p.err, abort_flag))
+          if (n >= kPieces &&
+              !(ok = wait_or_abort(smem_addr(&sh.pc_empty[slot]), (n / kPieces - 1) & 1, p.err, abort_flag)))
             break;
           Piece* pc = &sh.pc[slot];
           if (left <= 0) {
@@ -324,6 +345,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t ubeg = static_cast<int64_t>(sum) * p.Hkv + static_cast<int64_t>(kvh) * nt;
             cut = make_int4(item, kvh, n == 0 ? 0 : 1, static_cast<int>((ubeg + nt - 1) / per) - s + 1);
           }
+          // its Q, once the products of the piece before have read theirs
+          if (n > 0 && !(ok = wait_or_abort(smem_addr(&sh.qempty), (n - 1) & 1, p.err, abort_flag))) break;
+          const uint32_t bar = smem_addr(&sh.qfull), q = smem_addr(smem);
+          const int tiles = it.rows > HR ? 2 : 1, tok = it.q0 + it.row0 / p.G;
+          mbar_arrive_expect_tx(bar, box * DCH * tiles);
+          for (int m = 0; m < tiles; ++m)
+#pragma unroll
+            for (int c = 0; c < DCH; ++c)
+              tma_load_3d(q + m * C::SLOT + c * C::CHUNK, &tmq, c * 64, kvh * p.G, tok + m * ht, bar, policy);
+          ++loaded;
           left -= cnt;
           step += cnt;
           tile = 0;
@@ -334,10 +365,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         reinterpret_cast<int4*>(p.cuts)[s] = cut;
+        if (!ok && loaded > 0) mbar_wait(smem_addr(&sh.qfull), (loaded - 1) & 1, nullptr);
       }
     } else if (warp == kLoadWarp) {
       // ============================ K and V tiles ============================
-      constexpr int BPT = kKT / BS;  // blocks per tile, at most 16
+      const int BPT = kKT / BS;  // blocks per tile, at most 16
       const uint64_t policy = l2_policy_evict_normal();
       bool ok = true;
       int slot = 0;
@@ -395,152 +427,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok)  // loads issued but perhaps never waited for: the last of each slot
         for (int k = 0; k < NST; ++k)
           if (used >> k & 1) mbar_wait(smem_addr(&sh.full[k]), k < slot ? phase : phase ^ 1, nullptr);
-    } else if (warp == kQWarp) {
-      // ============================ Q tiles ============================
-      const uint64_t policy = l2_policy_evict_normal();
-      const int ht = HR / p.G;  // tokens of an M tile
-      const uint32_t box = static_cast<uint32_t>(HR) * 128;
-      bool ok = true;
-      int i = 0;
-      for (;; ++i) {
-        if (!(ok = piece_wait(i))) break;
-        const Piece& pc = sh.pc[i % kPieces];
-        if (pc.cnt == 0) break;
-        const int rows = pc.rows, kvh = pc.kvh, tok = pc.q0 + pc.row0 / p.G;
-        piece_done(i);
-        if (i > 0 && !(ok = wait_warp(smem_addr(&sh.qempty), (i - 1) & 1, p.err, abort_flag))) break;
-        if (lane == 0) {
-          const uint32_t bar = smem_addr(&sh.qfull), q = smem_addr(smem);
-          const int tiles = rows > HR ? 2 : 1;
-          mbar_arrive_expect_tx(bar, box * DCH * tiles);
-          for (int m = 0; m < tiles; ++m)
-#pragma unroll
-            for (int c = 0; c < DCH; ++c)
-              tma_load_3d(q + m * C::SLOT + c * C::CHUNK, &tmq, c * 64, kvh * p.G,
-                          tok + m * ht, bar, policy);
-        }
-        __syncwarp();
-      }
-      if (!ok && i > 0) mbar_wait(smem_addr(&sh.qfull), (i - 1) & 1, nullptr);
-    } else {
+    } else if (warp == kMmaWarp) {
       // ============================ products ============================
       constexpr uint32_t id_s = tc05::instr_desc_bf16(128, kKT, 0);
       constexpr uint32_t id_pv = tc05::instr_desc_bf16(128, D, 1);
-      // A cursor over the sub-steps: tile by tile, group 0 then group 1.
-      // All it needs lies in registers, ring slots are counted rather than divided: this loop is
-      // the latency between a group's P and its next S.
-      struct Cursor {
-        int n = 0, j = 0, g = 0, cnt = 0;  // piece, tile, group; tiles of the piece
-        int slot = 0;                      // the tile's ring slot
-        uint32_t phase = 0;
-        int a0 = 0, b0 = 0, a1 = 0, b1 = 0;  // the groups' tiles
-        int lo = 0, hi = 0;                  // the item's keys from the piece's first tile on
-      };
-      Cursor sc, pv;
-      pv.slot = 1;
-      bool s_end = false, pv_end = false, ok = true;
-      uint32_t pend = 0;    // bit g: S of group g is issued, its P.V is not
-      uint32_t ppar = 0;    // bit g: parity of the group's P
-      auto ready = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(kFull, mbar_test_wait(bar, parity)) != 0;
-      };
-      // (a reduction over the warp tells the compiler that the value is the same in all lanes)
+      // This loop is the latency between a group's P and its next S, so it is kept short: what it
+      // needs of a piece lies in (uniform) registers and ring slots are counted.
+      // (a reduction over the warp tells the compiler that a value is the same in all lanes)
       auto uni = [](int v) { return __reduce_max_sync(kFull, v); };
-      auto enter = [&](Cursor& c) {
-        const Piece& pc = sh.pc[c.n % kPieces];
-        c.cnt = uni(pc.cnt);
-        c.j = 0;
-        const int k0 = uni(pc.kt0) * kKT;
-        c.lo = uni(pc.lo) - k0;
-        c.hi = uni(pc.hi) - k0;
-        c.g = 0;
-        c.a0 = uni(pc.ga[0]);
-        c.b0 = uni(pc.gb[0]);
-        c.a1 = uni(pc.ga[1]);
-        c.b1 = uni(pc.gb[1]);
-      };
-      auto group_active = [&](const Cursor& c) {
-        return c.g ? c.j >= c.a1 && c.j < c.b1 : c.j >= c.a0 && c.j < c.b0;
-      };
-      auto advance = [&](Cursor& c) {  // true: the tile is finished
-        c.g ^= 1;
-        if (c.g) return false;
-        ++c.j;
-        c.slot += 2;
-        if (c.slot >= NST) {
-          c.slot -= NST;
-          c.phase ^= 1;
+      const uint32_t q_base = smem_addr(smem), ring_base = smem_addr(ring);
+      const uint32_t full0 = smem_addr(&sh.full[0]), empty0 = smem_addr(&sh.empty[0]);
+      bool ok = true;
+      int kslot = 0, vslot = 1;
+      uint32_t kphase = 0, vphase = 0;
+      uint32_t ppar = 0;  // bit g: parity of the group's P
+      auto next_slot = [](int& slot, uint32_t& phase) {
+        slot += 2;
+        if (slot >= NST) {
+          slot -= NST;
+          phase ^= 1;
         }
-        return true;
       };
-      if ((ok = piece_wait(0))) {
-        enter(sc);
-        enter(pv);
-        s_end = pv_end = sc.cnt == 0;
-      }
-      bool s_wait = true;    // the cursor's tile has not been waited for yet
-      bool s_enter = false;  // its piece has not been entered yet
-      while (ok && !pv_end) {
-        if (s_enter && ready(smem_addr(&sh.pc_full[sc.n % kPieces]), (sc.n / kPieces) & 1)) {
-          enter(sc);
-          s_end = sc.cnt == 0;
-          s_enter = false;
-        }
-        // ---- S of the next sub-step, as soon as its group's P has been read ----
-        const bool must = !s_enter && !s_end && sc.n == pv.n && sc.j == pv.j && sc.g == pv.g;  // nothing is pending
-        if (!s_end && !s_enter && !(pend >> sc.g & 1)) {
-          const uint32_t kb = smem_addr(&sh.full[sc.slot]), qb = smem_addr(&sh.qfull);
-          if (!s_wait || must || (ready(kb, sc.phase) && (sc.j > 0 || ready(qb, sc.n & 1)))) {
-            if (s_wait) {
-              if (!(ok = (sc.j > 0 || wait_warp(qb, sc.n & 1, p.err, abort_flag)) &&
-                         wait_warp(kb, sc.phase, p.err, abort_flag)))
-                break;
-              s_wait = false;
-            }
-            const int g = sc.g;
-            if (group_active(sc)) {
-              tc05::fence_after_sync();
-              const uint64_t dq = tc05::smem_desc(smem_addr(smem) + g * C::SLOT, 16, 1024);
-              const uint64_t dk = tc05::smem_desc(smem_addr(ring) + sc.slot * C::SLOT, 16, 1024);
-              const uint32_t ts = tmem + kColS + g * kGroupCols;
+      auto issue_s = [&](int g) {
+        const uint64_t dq = tc05::smem_desc(q_base + g * C::SLOT, 16, 1024);
+        const uint64_t dk = tc05::smem_desc(ring_base + kslot * C::SLOT, 16, 1024);
+        const uint32_t ts = tmem + kColS + g * kGroupCols;
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * C::CHUNK + (k & 3) * 32;
-                tc05::mma_ss_warp(ts, dq + (off >> 4), dk + (off >> 4), id_s, k > 0);
-              }
-              tc05::commit_warp(smem_addr(&sh.sfull[g]));
-              pend |= 1u << g;
-            }
-            const uint32_t eb = smem_addr(&sh.empty[sc.slot]);
-            if (advance(sc)) {
-              tc05::commit_warp(eb);
-              s_wait = true;
-              if (sc.j == sc.cnt) {
-                tc05::commit_warp(smem_addr(&sh.qempty));
-                ++sc.n;
-                s_enter = true;
-              }
-            }
-            continue;
-          }
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * C::CHUNK + (k & 3) * 32;
+          tc05::mma_ss_warp(ts, dq + (off >> 4), dk + (off >> 4), id_s, k > 0);
         }
-        // ---- P.V of the sub-step at the other cursor ----
-        if (s_enter && pv.n == sc.n) continue;  // the record is there: pv has waited for it
-        if (must) {  // (its S was issued above: the two cursors agree on what is pending)
-          flag_error(p.err, PA_DEVERR_TIMEOUT);
-          ok = false;
+        tc05::commit_warp(smem_addr(&sh.sfull[g]));
+      };
+      for (int n = 0; ok; ++n) {
+        if (!(ok = piece_wait(n))) break;
+        const Piece& pc = sh.pc[n % kPieces];
+        const int cnt = uni(pc.cnt);
+        if (cnt == 0) break;
+        const int k00 = uni(pc.kt0) * kKT, lo = uni(pc.lo) - k00, hi = uni(pc.hi) - k00;
+        const int a0 = uni(pc.ga[0]), b0 = uni(pc.gb[0]), a1 = uni(pc.ga[1]), b1 = uni(pc.gb[1]);
+        piece_done(n);
+        // S of the first tile
+        if (!(ok = wait_warp(smem_addr(&sh.qfull), n & 1, p.err, abort_flag) &&
+                   wait_warp(full0 + 8 * kslot, kphase, p.err, abort_flag)))
           break;
-        }
-        const int g = pv.g;
-        // the item's keys within the tile
-        const int a = max(pv.lo - pv.j * kKT, 0), z = min(pv.hi - pv.j * kKT, kKT);
-        if (g == 0) {
-          if (!(ok = wait_warp(smem_addr(&sh.full[pv.slot]), pv.phase, p.err, abort_flag))) break;
-          // V rows outside the item's keys may hold anything (0 * Inf is NaN): zero those that
-          // the product reads, up to the 16-key steps
-          const int na = a & 15, nz = -z & 15;
-          if (na + nz > 0) {
-            uint8_t* v = ring + pv.slot * C::SLOT;
+        tc05::fence_after_sync();
+        if (a0 == 0 && b0 > 0) issue_s(0);
+        if (a1 == 0 && b1 > 0) issue_s(1);
+        tc05::commit_warp(empty0 + 8 * kslot);
+        if (cnt == 1) tc05::commit_warp(smem_addr(&sh.qempty));
+        next_slot(kslot, kphase);
+        for (int j = 0; j < cnt; ++j) {
+          const bool more = j + 1 < cnt;
+          if (!(ok = wait_warp(full0 + 8 * vslot, vphase, p.err, abort_flag))) break;
+          const int a = max(lo - j * kKT, 0), z = min(hi - j * kKT, kKT);  // the item's keys within the tile
+          if (a > 0 || z < kKT) {
+            // V rows outside them may hold anything (0 * Inf is NaN): zero those that the product
+            // reads, up to the 16-key steps
+            const int na = a & 15, nz = -z & 15;
+            uint8_t* v = ring + vslot * C::SLOT;
             for (int e = lane; e < (na + nz) * DCH * 8; e += 32) {
               const int r = e / (DCH * 8), q = e % (DCH * 8);
               const int row = r < na ? a - na + r : z + r - na;
@@ -549,37 +494,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
-        }
-        if (group_active(pv)) {
-          if (!(ok = wait_warp(smem_addr(&sh.pfull[g]), ppar >> g & 1, p.err, abort_flag))) break;
-          ppar ^= 1u << g;
-          pend &= ~(1u << g);
-          tc05::fence_after_sync();
-          const uint64_t dv = tc05::smem_desc(smem_addr(ring) + pv.slot * C::SLOT, C::CHUNK, 1024);
-          const uint32_t tp = tmem + kColS + g * kGroupCols, to = tmem + kColO + g * kGroupCols;
-          // the group's first tile of the piece overwrites O
-          const bool fresh = pv.j == (g ? pv.a1 : pv.a0);
+          const uint64_t dv = tc05::smem_desc(ring_base + vslot * C::SLOT, C::CHUNK, 1024);
           const int s0 = a >> 4, s1 = (z + 15) >> 4;
-          if (s0 == 0 && s1 == kKT / 16) {
-#pragma unroll
-            for (int k = 0; k < kKT / 16; ++k)
-              tc05::mma_ts_warp(to, tp + 8 * k, dv + (k * 2048 >> 4), id_pv, k > 0 || !fresh);
-          } else {
+          bool k_there = false;
 #pragma unroll 1
-            for (int k = s0; k < s1; ++k)
-              tc05::mma_ts_warp(to, tp + 8 * k, dv + (k * 2048 >> 4), id_pv, k > s0 || !fresh);
+          for (int g = 0; g < 2; ++g) {
+            const int ga = g ? a1 : a0, gb = g ? b1 : b0;
+            if (j >= ga && j < gb) {
+              const uint32_t tp = tmem + kColS + g * kGroupCols, to = tmem + kColO + g * kGroupCols;
+              // the group's first tile of the piece overwrites O
+              uint32_t acc = j != ga;
+#pragma unroll 1
+              for (int h = 0; h < 2 && ok; ++h) {  // P comes in two halves
+                if (!(ok = wait_warp(smem_addr(&sh.pfull[g][h]), ppar >> g & 1, p.err, abort_flag))) break;
+                tc05::fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int kk = 4 * h + k;
+                  if (kk >= s0 && kk < s1) {
+                    tc05::mma_ts_warp(to, tp + 8 * kk, dv + (kk * 2048 >> 4), id_pv, acc);
+                    acc = 1;
+                  }
+                }
+              }
+              if (!ok) break;
+              ppar ^= 1u << g;
+              if (j == gb - 1) tc05::commit_warp(smem_addr(&sh.ofull[g]));
+            }
+            if (more && j + 1 >= ga && j + 1 < gb) {
+              if (!k_there && !(ok = wait_warp(full0 + 8 * kslot, kphase, p.err, abort_flag))) break;
+              k_there = true;
+              issue_s(g);
+            }
           }
-          if (pv.j == (g ? pv.b1 : pv.b0) - 1) tc05::commit_warp(smem_addr(&sh.ofull[g]));
-        }
-        const uint32_t eb = smem_addr(&sh.empty[pv.slot]);
-        if (advance(pv)) {
-          tc05::commit_warp(eb);
-          if (pv.j == pv.cnt) {
-            piece_done(pv.n);
-            ++pv.n;
-            if (!(ok = piece_wait(pv.n))) break;
-            enter(pv);
-            pv_end = pv.cnt == 0;
+          if (!ok) break;
+          tc05::commit_warp(empty0 + 8 * vslot);
+          next_slot(vslot, vphase);
+          if (more) {
+            if (!k_there && !(ok = wait_warp(full0 + 8 * kslot, kphase, p.err, abort_flag))) break;
+            tc05::commit_warp(empty0 + 8 * kslot);
+            if (j + 2 == cnt) tc05::commit_warp(smem_addr(&sh.qempty));
+            next_slot(kslot, kphase);
           }
         }
       }
@@ -591,14 +546,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ============================ softmax ============================
-    setmaxnreg_inc<208>();
+    setmaxnreg_inc<kSoftRegs>();
     const int g = warp >> 2, w = warp & 3;
     const uint32_t lane_addr = static_cast<uint32_t>(32 * w) << 16;
     const uint32_t ts = tmem + kColS + g * kGroupCols + lane_addr;
     const uint32_t to = tmem + kColO + g * kGroupCols + lane_addr;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-    const bool plain = p.cap_out == 0.f && !p.slopes && p.scale_log2 > 0.f;
-    const float mul = plain ? p.scale_log2 : 1.f;
+    constexpr bool PLAIN = !C::CAP && !C::BIAS;  // (with a positive scale: it commutes with the maximum)
+    const float mul = PLAIN ? p.scale_log2 : 1.f;
     const int r = 32 * w + lane;  // row of the M tile
 
     // items whose rows see nothing have no tile: their rows are zero
@@ -632,90 +587,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rows > 0) row = row_of(p, pc, f);
       const int ja = pc.ga[g], jb = pc.gb[g];
       const bool active = ja < jb;
-      int all_lo = row.lo, all_hi = row.hi;  // keys that every row of the warp sees
+      // keys that every row of the warp sees, and its first position
+      int all_lo = row.lo, all_hi = row.hi, all_pos = row.pos;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) {
         all_lo = max(all_lo, __shfl_xor_sync(kFull, all_lo, off));
         all_hi = min(all_hi, __shfl_xor_sync(kFull, all_hi, off));
+        all_pos = min(all_pos, __shfl_xor_sync(kFull, all_pos, off));
       }
-      // reference maximum, sum, and the maximum seen (the reference may lag by kOverflowLog2)
-      float m_ref = -INFINITY, l = 0.f, m_next = -INFINITY;
+      float m_ref = -INFINITY, l = 0.f;
       for (int j = ja; j < jb; ++j, ++done) {
         if (!(ok = wait_warp(smem_addr(&sh.sfull[g]), done & 1, p.err, abort_flag))) break;
         tc05::fence_after_sync();
         if (32 * w >= rows) {  // none of the warp's rows is a row of the item
           tc05::fence_before_sync();
-          mbar_arrive(smem_addr(&sh.pfull[g]));
+          mbar_arrive(smem_addr(&sh.pfull[g][0]));
+          mbar_arrive(smem_addr(&sh.pfull[g][1]));
           continue;
         }
-        // A tile's 128 columns are taken in two halves, so that the scores and what
-        // their modification needs stay in registers.  The reference maximum is that of the first
-        // half and the tiles before; the second half moves it only where its weights might
-        // overflow (the first half's P would have to be rescaled, and is), else the next tile does.
-        constexpr int N = 64;
-        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-#pragma unroll 1  // (one copy of the code: instruction fetches bound two)
-        for (int h = 0; h < 2; ++h) {
-          const int col = N * h;  // first column
-          const int key0 = (pc.kt0 + j) * kKT + col;
-          uint32_t raw[N / 32][32];
+        const int key0 = (pc.kt0 + j) * kKT;
+        uint32_t raw[4][32];
 #pragma unroll
-          for (int c = 0; c < N / 32; ++c) tc05::ld32(ts + col + 32 * c, raw[c]);
-          tc05::wait_ld();
-          float x[N];
+        for (int c = 0; c < 4; ++c) tc05::ld32(ts + 32 * c, raw[c]);
+        tc05::wait_ld();
 #pragma unroll
-          for (int e = 0; e < N; ++e) x[e] = __uint_as_float(raw[e / 32][e % 32]);
-          const bool masked = key0 < all_lo || key0 + N > all_hi;
-          const float mt = fmaxf(m_next, modify_scores(x, p, row, key0, plain, masked) * mul);
-          const bool raise = mt > m_ref + (h == 0 ? kRescaleLog2 : kOverflowLog2);
-          // (earlier P.V of the group are complete: S was issued behind them)
-          if (__any_sync(kFull, raise)) {
-            const float alpha = raise ? ex2_approx(m_ref - mt) : 1.f;
-            if (j > ja) {
+        for (int c = 0; c < 4; ++c) tc05::landed(raw[c]);
+        float x[kKT];
 #pragma unroll
-              for (int c = 0; c < D; c += 32) {
-                uint32_t v[32];
-                tc05::ld32(to + c, v);
-                tc05::wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-                tc05::st32(to + c, v);
-              }
-            }
-            if (h == 1) {  // the first half's P, which is in tensor memory already
-              tc05::wait_st();
-              uint32_t v[32];
-              tc05::ld32(ts, v);
+        for (int e = 0; e < kKT; ++e) x[e] = __uint_as_float(raw[e / 32][e % 32]);
+        const bool masked = key0 < all_lo || key0 + kKT > all_hi;
+        const float mt = modify_scores<C::CAP, C::BIAS>(x, p, row, key0, masked,
+                                                        p.prefix_lens && key0 + kKT - 1 > all_pos) * mul;
+        const bool raise = mt > m_ref + kRescaleLog2;
+        // (earlier P.V of the group are complete: S was issued behind them)
+        if (__any_sync(kFull, raise)) {
+          const float alpha = raise ? ex2_approx(m_ref - mt) : 1.f;
+          if (j > ja) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t v[16];
+              tc05::ld16(to + c, v);
               tc05::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = pack_bf16x2(bf16_lo(v[e]) * alpha, bf16_hi(v[e]) * alpha);
-              tc05::st32(ts, v);
-              l0 = __fmul2_rn(l0, splat(alpha));
-              l1 = __fmul2_rn(l1, splat(alpha));
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tc05::st16(to + c, v);
             }
-            l *= alpha;
-            if (raise) m_ref = mt;
           }
-          m_next = mt;
-          const float2 mul2 = splat(mul), ref2 = splat(m_ref == -INFINITY ? 0.f : -m_ref);
+          l *= alpha;
+          if (raise) m_ref = mt;
+        }
+        const float2 mul2 = splat(mul), ref2 = splat(m_ref == -INFINITY ? 0.f : -m_ref);
+        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+        // P in two halves, so that the product of the first runs while the second is computed
 #pragma unroll
-          for (int c = 0; c < N; c += 32) {
-            uint32_t v[16];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 y = __ffma2_rn(make_float2(x[c + 2 * e], x[c + 2 * e + 1]), mul2, ref2);
-              y.x = ex2_approx(y.x);
-              y.y = ex2_approx(y.y);
-              if (e & 1) l1 = __fadd2_rn(l1, y); else l0 = __fadd2_rn(l0, y);
-              v[e] = pack_bf16x2(y.x, y.y);
-            }
-            tc05::st16(ts + (col + c) / 2, v);
+          for (int e = 0; e < 32; ++e) {
+            float2 y = make_float2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]);
+            y = PLAIN ? __ffma2_rn(y, mul2, ref2) : __fadd2_rn(y, ref2);
+            y.x = ex2_approx(y.x);
+            y.y = ex2_approx(y.y);
+            if (e & 1) l1 = __fadd2_rn(l1, y); else l0 = __fadd2_rn(l0, y);
+            v[e] = pack_bf16x2(y.x, y.y);
           }
+          tc05::st32(ts + 32 * h, v);
+          tc05::wait_st();
+          tc05::fence_before_sync();
+          mbar_arrive(smem_addr(&sh.pfull[g][h]));
         }
         l += (l0.x + l0.y) + (l1.x + l1.y);
-        tc05::wait_st();
-        tc05::fence_before_sync();
-        mbar_arrive(smem_addr(&sh.pfull[g]));
       }
       if (!ok) break;
 
@@ -782,8 +723,8 @@ template <class C>
 cudaError_t run(const AttnParams& p, cudaStream_t stream) {
   CUtensorMap tmk, tmv, tmq;
   const int tokens = p.HR / p.G;
-  if (!make_pool_map(&tmk, p.k_pool, p.num_blocks, C::BS, p.Hkv, C::D, C::BS) ||
-      !make_pool_map(&tmv, p.v_pool, p.num_blocks, C::BS, p.Hkv, C::D, C::BS) ||
+  if (!make_pool_map(&tmk, p.k_pool, p.num_blocks, p.block_size, p.Hkv, C::D, p.block_size) ||
+      !make_pool_map(&tmv, p.v_pool, p.num_blocks, p.block_size, p.Hkv, C::D, p.block_size) ||
       !make_q_rows_map(&tmq, p.q, p.T, p.Hq, C::D, p.q_stride, p.G, tokens))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -806,16 +747,15 @@ cudaError_t run(const AttnParams& p, cudaStream_t stream) {
 // Rows per item: two M tiles of whole tokens.
 int attention_tc_rows(int G) { return 2 * (128 / G) * G; }
 
+template <int D>
+static cudaError_t run_modified(const AttnParams& p, cudaStream_t stream) {
+  const bool cap = p.cap_out > 0.f, bias = p.slopes != nullptr || (!cap && !(p.scale_log2 > 0.f));
+  if (cap) return bias ? run<TcAttn<D, true, true>>(p, stream) : run<TcAttn<D, true, false>>(p, stream);
+  return bias ? run<TcAttn<D, false, true>>(p, stream) : run<TcAttn<D, false, false>>(p, stream);
+}
+
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t stream) {
-  switch (p.D * 100 + p.block_size) {
-    case 6408: return run<TcAttn<64, 8>>(p, stream);
-    case 6416: return run<TcAttn<64, 16>>(p, stream);
-    case 6432: return run<TcAttn<64, 32>>(p, stream);
-    case 12808: return run<TcAttn<128, 8>>(p, stream);
-    case 12816: return run<TcAttn<128, 16>>(p, stream);
-    case 12832: return run<TcAttn<128, 32>>(p, stream);
-    default: return cudaErrorInvalidValue;
-  }
+  return p.D == 64 ? run_modified<64>(p, stream) : run_modified<128>(p, stream);
 }
 
 }  // namespace pa
