@@ -104,76 +104,95 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, const Piece& pc, int 
   return r;
 }
 
-// Turn the N raw scores of a row (keys key0 ..) into log2-domain scores in place and return their
-// maximum.  The plain case keeps raw scores, so that the scale and the subtraction of the maximum
-// become one operation.  `ahead`: some of the keys may lie behind the row's position and count.
-//
 // One operation per element costs a warp 128 cycles a tile, two warps share a sub-partition and the
 // products of a pair of tiles take 2048: operations are counted here.  So are instructions: once
 // the loop of all roles is larger than the 32 KB that instructions are kept in, each takes three
 // times as long.  Two-element forms take as long as two scalar ones, but half the instructions.
+
+// Whether the polynomial below holds for raw scores of up to `top` in any lane of the warp.
+__device__ __forceinline__ bool cap_is_small(const AttnParams& p, float top) {
+  return __all_sync(kFull, top * fabsf(p.cap_in) <= 0.85f);  // (NaN: no)
+}
+
+// cap * tanh(scale * x / cap) log2(e) of N raw scores, in place.
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&x)[N], const AttnParams& p, bool small) {
+  constexpr int E = 8;  // elements taken step by step, so that the steps of one do not wait
+  if (small) {
+    // tanh(t) / t as a polynomial in t^2 (iterated reweighted least squares on |t| <= 0.85, where
+    // |t P(t^2) - tanh t| < 6.9e-7 in 32 bits): on the FMA pipe alone, the exponentials need the
+    // other
+    const float2 ci = splat(p.cap_in);
+    const float co = p.cap_out;
+    const float2 c4 = splat(0.01063788216561079f * co), c3 = splat(-0.04714450612664223f * co),
+                 c2 = splat(0.13136771321296692f * co), c1 = splat(-0.3330950140953064f * co),
+                 c0 = splat(0.9999918341636658f * co);
+#pragma unroll
+    for (int j = 0; j < N; j += E) {
+      float2 t[E / 2], u[E / 2], y[E / 2];
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) t[e] = __fmul2_rn(make_float2(x[j + 2 * e], x[j + 2 * e + 1]), ci);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) u[e] = __fmul2_rn(t[e], t[e]);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(u[e], c4, c3);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c2);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c1);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c0);
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        y[e] = __fmul2_rn(y[e], t[e]);
+        x[j + 2 * e] = y[e].x;
+        x[j + 2 * e + 1] = y[e].y;
+      }
+    }
+  } else {
+    // tanh t = 1 - 2 / (1 + e^2t)
+    const float c2 = p.cap_in * (2.f * kLog2e), m2 = -2.f * p.cap_out;
+#pragma unroll
+    for (int j = 0; j < N; j += E) {
+      float u[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) u[e] = ex2_approx(x[j + e] * c2);
+#pragma unroll
+      for (int e = 0; e < E; ++e) u[e] = rcp_approx(1.f + u[e]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[j + e] = fmaf(m2, u[e], p.cap_out);
+    }
+  }
+}
+
+// Maximum of op(x) where op is max (SIGN 1) or of -x (SIGN -1); NaN are passed over.
+template <int SIGN, int N>
+__device__ __forceinline__ float extreme(const float (&x)[N]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 0; j < N; j += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(SIGN * x[j + 2 * e], SIGN * x[j + 2 * e + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Elements of columns outside [a, b) become `v`.
+template <int N>
+__device__ __forceinline__ void mask_scores(float (&x)[N], int a, int b, float v) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) x[j] = j >= a && j < b ? x[j] : v;
+}
+
+// Turn the N raw scores of a row (keys key0 ..) into log2-domain scores in place and return their
+// maximum.  The plain case keeps raw scores, so that the scale and the subtraction of the maximum
+// become one operation.  `ahead`: some of the keys may lie behind the row's position and count.
 template <bool CAP, bool BIAS, int N>
 __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& p, const Row& r, int key0,
                                                bool masked, bool ahead) {
-  constexpr int E = 8;  // elements taken step by step, so that the steps of one do not wait
-  const int a = r.lo - key0, b = r.hi - key0;
+  constexpr int E = 8;
   if constexpr (CAP) {
-    if (masked) {  // what lies in masked columns must not choose the branch below
-#pragma unroll
-      for (int j = 0; j < N; ++j) x[j] = j >= a && j < b ? x[j] : 0.f;
-    }
-    float ax[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < N; j += 8)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ax[e] = fmaxf(ax[e], fmaxf(fabsf(x[j + 2 * e]), fabsf(x[j + 2 * e + 1])));
-    // (a NaN fails the comparison only if it is all there is; both ways carry it through)
-    const float top = fmaxf(fmaxf(ax[0], ax[1]), fmaxf(ax[2], ax[3]));
-    if (__all_sync(kFull, top * fabsf(p.cap_in) <= 0.85f)) {
-      // tanh(t) / t as a polynomial in t^2 (iterated reweighted least squares on |t| <= 0.85, where
-      // |t P(t^2) - tanh t| < 6.9e-7 in 32 bits): on the FMA pipe alone, the exponentials need the
-      // other
-      const float2 ci = splat(p.cap_in);
-      const float co = p.cap_out;
-      const float2 c4 = splat(0.01063788216561079f * co), c3 = splat(-0.04714450612664223f * co),
-                   c2 = splat(0.13136771321296692f * co), c1 = splat(-0.3330950140953064f * co),
-                   c0 = splat(0.9999918341636658f * co);
-#pragma unroll
-      for (int j = 0; j < N; j += E) {
-        float2 t[E / 2], u[E / 2], y[E / 2];
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) t[e] = __fmul2_rn(make_float2(x[j + 2 * e], x[j + 2 * e + 1]), ci);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) u[e] = __fmul2_rn(t[e], t[e]);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(u[e], c4, c3);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c2);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c1);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c0);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          y[e] = __fmul2_rn(y[e], t[e]);
-          x[j + 2 * e] = y[e].x;
-          x[j + 2 * e + 1] = y[e].y;
-        }
-      }
-    } else {
-      // tanh t = 1 - 2 / (1 + e^2t)
-      const float c2 = p.cap_in * (2.f * kLog2e), m2 = -2.f * p.cap_out;
-#pragma unroll
-      for (int j = 0; j < N; j += E) {
-        float u[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) u[e] = ex2_approx(x[j + e] * c2);
-#pragma unroll
-        for (int e = 0; e < E; ++e) u[e] = rcp_approx(1.f + u[e]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[j + e] = fmaf(m2, u[e], p.cap_out);
-      }
-    }
+    if (masked) mask_scores(x, r.lo - key0, r.hi - key0, 0.f);  // what lies there must not choose the formula
+    cap_scores(x, p, cap_is_small(p, fmaxf(extreme<1>(x), extreme<-1>(x))));
   }
   if constexpr (BIAS) {
     const float d0 = static_cast<float>(r.pos - key0);
@@ -191,20 +210,17 @@ __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& 
 #pragma unroll
         for (int e = 0; e < E; ++e) d[e] = fmaf(r.slope, static_cast<float>(j + e), c0);
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[j + e] = CAP ? x[j + e] + d[e] : fmaf(x[j + e], p.scale_log2, d[e]);
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = make_float2(x[j + e], x[j + e + 1]), w = make_float2(d[e], d[e + 1]);
+          const float2 y = CAP ? __fadd2_rn(v, w) : __ffma2_rn(v, splat(p.scale_log2), w);
+          x[j + e] = y.x;
+          x[j + e + 1] = y.y;
+        }
       }
     }
   }
-  if (masked) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = j >= a && j < b ? x[j] : -INFINITY;
-  }
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int j = 0; j < N; j += 8)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(x[j + 2 * e], x[j + 2 * e + 1]));
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  if (masked) mask_scores(x, r.lo - key0, r.hi - key0, -INFINITY);
+  return extreme<1>(x);
 }
 
 template <int N>
@@ -552,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + kColS + g * kGroupCols + lane_addr;
     const uint32_t to = tmem + kColO + g * kGroupCols + lane_addr;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+    constexpr bool CAP_ONLY = C::CAP && !C::BIAS;
     constexpr bool PLAIN = !C::CAP && !C::BIAS;  // (with a positive scale: it commutes with the maximum)
     const float mul = PLAIN ? p.scale_log2 : 1.f;
     const int r = 32 * w + lane;  // row of the M tile
@@ -616,8 +633,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < kKT; ++e) x[e] = __uint_as_float(raw[e / 32][e % 32]);
         const bool masked = key0 < all_lo || key0 + kKT > all_hi;
-        const float mt = modify_scores<C::CAP, C::BIAS>(x, p, row, key0, masked,
-                                                        p.prefix_lens && key0 + kKT - 1 > all_pos) * mul;
+        float mt;
+        bool small = false;
+        if constexpr (CAP_ONLY) {
+          // the cap is monotone: the extremes of the raw scores give the maximum and the formula,
+          // and the scores are capped half by half below (short code, few registers)
+          if (masked) mask_scores(x, row.lo - key0, row.hi - key0, __int_as_float(0x7fffffff));
+          const float mx = extreme<1>(x), mn = -extreme<-1>(x);
+          small = cap_is_small(p, fmaxf(fabsf(mx), fabsf(mn)));
+          float top[1] = {p.cap_in >= 0.f ? mx : mn};
+          const bool none = mx == -INFINITY && mn == INFINITY;
+          top[0] = fmaf(-2.f * p.cap_out, rcp_approx(1.f + ex2_approx(top[0] * p.cap_in * (2.f * kLog2e))), p.cap_out);
+          mt = none ? -INFINITY : top[0];
+        } else {
+          mt = modify_scores<C::CAP, C::BIAS>(x, p, row, key0, masked, p.prefix_lens && key0 + kKT - 1 > all_pos) * mul;
+        }
         const bool raise = mt > m_ref + kRescaleLog2;
         // (earlier P.V of the group are complete: S was issued behind them)
         if (__any_sync(kFull, raise)) {
@@ -639,12 +669,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 mul2 = splat(mul), ref2 = splat(m_ref == -INFINITY ? 0.f : -m_ref);
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
         // P in two halves, so that the product of the first runs while the second is computed
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        auto weights = [&](const float* y64, int h) {
           uint32_t v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            float2 y = make_float2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1]);
+            float2 y = make_float2(y64[2 * e], y64[2 * e + 1]);
             y = PLAIN ? __ffma2_rn(y, mul2, ref2) : __fadd2_rn(y, ref2);
             y.x = ex2_approx(y.x);
             y.y = ex2_approx(y.y);
@@ -655,6 +684,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc05::wait_st();
           tc05::fence_before_sync();
           mbar_arrive(smem_addr(&sh.pfull[g][h]));
+        };
+        if constexpr (CAP_ONLY) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t again[2][32];
+            tc05::ld32(ts + 64 * h, again[0]);
+            tc05::ld32(ts + 64 * h + 32, again[1]);
+            tc05::wait_ld();
+            tc05::landed(again[0]);
+            tc05::landed(again[1]);
+            float y[64];
+#pragma unroll
+            for (int e = 0; e < 64; ++e) y[e] = __uint_as_float(again[e / 32][e % 32]);
+            cap_scores(y, p, small);
+            if (masked) mask_scores(y, row.lo - key0 - 64 * h, row.hi - key0 - 64 * h, -INFINITY);
+            weights(y, h);
+          }
+        } else {
+          weights(x, 0);
+          weights(x + 64, 1);
         }
         l += (l0.x + l0.y) + (l1.x + l1.y);
       }
