@@ -31,7 +31,7 @@ int sm_count() {
 // The plan of a pa_attention call on `sms` multiprocessors: rows per item (and per softmax
 // group), keys per tile, CTAs.
 struct AttnShape {
-  int RT, HR, KT, ctas, max_items;
+  int RT, HR, KT, ctas, max_items, extra;
 };
 
 // Which kernel a call takes.  The tensor-core ones take bf16 and blocks of whole swizzle atoms (8
@@ -46,7 +46,7 @@ AttnKernel attention_kernel(int B, int max_query_len, int G, int block_size, pa_
 }
 
 AttnShape attention_shape(int T, int B, int max_query_len, int G, int D, AttnKernel kernel, int sms) {
-  AttnShape s;
+  AttnShape s{};
   if (kernel == kTokens) {
     s.KT = 16;
     s.RT = s.HR = max_query_len * G;
@@ -59,6 +59,7 @@ AttnShape attention_shape(int T, int B, int max_query_len, int G, int D, AttnKer
     s.RT = pa::attention_tc_rows(G);
     s.HR = s.RT / 2;
     s.ctas = sms;
+    s.extra = pa::attention_tc_extra();
   } else {
     s.KT = 64;
     s.RT = s.HR = static_cast<int64_t>(max_query_len) * G <= 16 ? 16 : 64;
@@ -85,6 +86,7 @@ size_t attention_carve(const AttnShape& s, int B, int D, char* ws, pa::AttnParam
   if (p) {
     p->RT = s.RT;
     p->HR = s.HR;
+    p->extra = s.extra;
     p->KT = s.KT;
     p->ctas = s.ctas;
     p->max_items = s.max_items;
@@ -248,7 +250,7 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
   const AttnShape sh = attention_shape(T, B, max_query_len, G, D, kernel, sms);
   // tile counts are summed in 32 bits: of one KV head, or of all in the tokens kernel
   const int64_t rows = kernel == kTokens ? static_cast<int64_t>(B) * Hkv : sh.max_items;
-  if (rows * (max_seq / sh.KT + 2) >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+  if (rows * (max_seq / sh.KT + 2 + sh.extra) >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
   pa::AttnParams p{};
   if (workspace_bytes < attention_carve(sh, B, D, static_cast<char*>(workspace), &p)) return PA_ERR_INVALID_ARG;
   const double log2e = 1.4426950408889634;

@@ -12,8 +12,10 @@
 // with one KV head it is a unit of nt = tiles of KT keys that its rows may see.  All units lie
 // end to end (item, then KV head, then tile) and every CTA of one wave takes an equal contiguous
 // range, whatever mixture of lengths and masks the batch is: a long axis with few rows is split
-// and a short one is not by the same rule.  A unit cut by a range's end leaves partials (max,
-// sum, unnormalised output; base 2) that attention_join_kernel merges by log-sum-exp.
+// and a short one is not by the same rule.  Before its tiles a unit counts `extra` more, which
+// stand for its loads of Q and its output, so that ranges of many short units are not the last
+// to end.  A unit cut by a range's end leaves partials (max, sum, unnormalised output; base 2)
+// that attention_join_kernel merges by log-sum-exp.
 //
 // CUDA-core kernel: fp32 inputs (no TF32), bf16 with blocks of 4 tokens.  A CTA holds a tile
 // of RT rows of Q, and K and V tiles of 64 keys as fp32 in shared memory; a thread computes MR x 4
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
       }
       if (it.hi == 0) it.lo = 0;
       p.items[i] = it;
-      nt = it.hi > 0 ? (it.hi - 1) / p.KT - it.lo / p.KT + 1 : 0;
+      nt = it.hi > 0 ? (it.hi - 1) / p.KT - it.lo / p.KT + 1 + p.extra : 0;
     }
     int total;
     const int at = block_scan(nt, sums, total);
@@ -246,12 +248,19 @@ __global__ void __launch_bounds__(kGenThreads) attention_generic_kernel(const At
   bool first_piece = true;
   while (left > 0) {
     const AttnItem it = p.items[item];
-    const int nt = p.tile_sum[item + 1] - p.tile_sum[item];
-    if (nt == 0) {
+    const int slots = p.tile_sum[item + 1] - p.tile_sum[item];
+    if (slots == 0) {
       ++item;
       continue;
     }
-    const int cnt = min(left, nt - tile);
+    UnitPart u = unit_part(p, slots, tile, left);
+    left -= u.slots;
+    if (u.cnt == 0) {  // the range ends before the unit's first tile
+      tile = 0;
+      continue;
+    }
+    const int nt = u.nt, cnt = u.cnt;
+    tile = u.tile;
     const int pre = p.prefix_lens ? __ldg(p.prefix_lens + it.b) : 0;
     __syncthreads();  // the last piece's reads of Q are done
     for (int e = tid; e < RT * (D / 4); e += kGenThreads) {
@@ -410,10 +419,9 @@ __global__ void __launch_bounds__(kGenThreads) attention_generic_kernel(const At
       own_item = item;
       own_kvh = kvh;
       own_slot = slot;
-      const int64_t ubeg = static_cast<int64_t>(p.tile_sum[item]) * p.Hkv + static_cast<int64_t>(kvh) * nt;
-      own_n = static_cast<int>((ubeg + nt - 1) / per) - s + 1;
+      const int64_t ubeg = static_cast<int64_t>(p.tile_sum[item]) * p.Hkv + static_cast<int64_t>(kvh) * slots;
+      own_n = static_cast<int>((ubeg + slots - 1) / per) - s + 1;
     }
-    left -= cnt;
     first_piece = false;
     tile = 0;
     if (++kvh == p.Hkv) {

@@ -20,10 +20,26 @@ struct AttnItem {
   int glo[2], ghi[2];  // the same of its rows [0, HR) and [HR, 2 HR)
 };
 
-// The first piece of one CTA's range.
+// Where a CTA's range begins: the slot (extra ones, then tiles) of a unit, and the range's slots.
 struct AttnStart {
-  int item, kvh, tile, count;  // count: tiles of the whole range
+  int item, kvh, tile, count;
 };
+
+// The part of a unit of `slots` slots that a range with `left` slots to go takes from slot
+// `slot` on: its slots, and its tiles [tile, tile + cnt) of nt.  A range that begins among the
+// unit's extra slots begins with its first tile; one that ends there takes none.
+struct UnitPart {
+  int slots, nt, tile, cnt;
+};
+
+__device__ __forceinline__ UnitPart unit_part(const AttnParams& p, int slots, int slot, int left) {
+  UnitPart u;
+  u.slots = min(left, slots - slot);
+  u.nt = slots - p.extra;
+  u.tile = max(slot - p.extra, 0);
+  u.cnt = max(slot + u.slots - p.extra - u.tile, 0);
+  return u;
+}
 
 __device__ __forceinline__ int attn_len(const AttnParams& p, int b, bool flag) {
   const int L = __ldg(p.seq_lens + b);

@@ -67,7 +67,6 @@ struct TcAttn {
 struct Piece {
   int cnt;             // 0: no more pieces
   int kt0;
-  int step0;           // tiles of the CTA's range before the piece
   int kvh;
   int b, q0, row0, rows, pos0, L, lo, hi;
   int ga[2], gb[2];    // group g's tiles
@@ -77,7 +76,7 @@ struct Piece {
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t qfull, qempty;
-  uint64_t sfull[2], pfull[2][2], ofull[2];  // per group; P in two halves
+  uint64_t sfull[2], pfull[2], ofull[2];  // per group
   uint64_t pc_full[kPieces], pc_empty[kPieces];
   uint64_t drain_bar;
   Piece pc[kPieces];
@@ -94,13 +93,26 @@ struct Row {
   float slope;     // times log2 e
 };
 
-__device__ __forceinline__ Row row_of(const AttnParams& p, const Piece& pc, int f) {
-  Row r;
+// What a row reads from global memory, loaded while the piece before ends.
+struct RowLoads {
+  int prefix, first;
+  float slope;
+};
+
+__device__ __forceinline__ RowLoads load_row(const AttnParams& p, const Piece& pc, int f) {
   const int t = f / p.G;
-  r.pos = pc.pos0 + t;
-  const int pre = p.prefix_lens ? __ldg(p.prefix_lens + pc.b) : 0;
-  attn_visible(p, r.pos, pc.L, pre, p.first_keys ? __ldg(p.first_keys + pc.q0 + t) : 0, r.lo, r.hi);
-  r.slope = p.slopes ? __ldg(p.slopes + pc.kvh * p.G + (f - t * p.G)) * kLog2e : 0.f;
+  RowLoads r;
+  r.prefix = p.prefix_lens ? __ldg(p.prefix_lens + pc.b) : 0;
+  r.first = p.first_keys ? __ldg(p.first_keys + pc.q0 + t) : 0;
+  r.slope = p.slopes ? __ldg(p.slopes + pc.kvh * p.G + (f - t * p.G)) : 0.f;
+  return r;
+}
+
+__device__ __forceinline__ Row row_of(const AttnParams& p, const Piece& pc, int f, const RowLoads& in) {
+  Row r;
+  r.pos = pc.pos0 + f / p.G;
+  attn_visible(p, r.pos, pc.L, in.prefix, in.first, r.lo, r.hi);
+  r.slope = in.slope * kLog2e;
   return r;
 }
 
@@ -256,8 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_addr(&sh.qempty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.sfull[i]), 1);
-      mbar_init(smem_addr(&sh.pfull[i][0]), 128);
-      mbar_init(smem_addr(&sh.pfull[i][1]), 128);
+      mbar_init(smem_addr(&sh.pfull[i]), 128);
       mbar_init(smem_addr(&sh.ofull[i]), 1);
     }
     for (int i = 0; i < kPieces; ++i) {
@@ -312,14 +323,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t per =
             (static_cast<int64_t>(p.header[1]) * p.Hkv + p.ctas - 1) / p.ctas;
         const AttnStart st = p.starts[s];
-        int left = st.count, item = st.item, kvh = st.kvh, tile = st.tile, step = 0, n = 0;
+        int left = st.count, item = st.item, kvh = st.kvh, at = st.tile, n = 0;
         int loaded = 0;  // Q loads issued
         int4 cut = make_int4(-1, 0, 0, 0);
         AttnItem it{};
-        int sum = 0, nt = 0;
+        int sum = 0, slots = 0;
         auto load_item = [&] {  // the item at or after `item` that has tiles
           sum = p.tile_sum[item];
-          while ((nt = p.tile_sum[item + 1] - sum) == 0) ++item;
+          while ((slots = p.tile_sum[item + 1] - sum) == 0) ++item;
           it = p.items[item];
         };
         if (left > 0) load_item();
@@ -328,17 +339,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n >= kPieces &&
               !(ok = wait_or_abort(smem_addr(&sh.pc_empty[slot]), (n / kPieces - 1) & 1, p.err, abort_flag)))
             break;
+          UnitPart u{0, 0, 0, 0};
+          if (left > 0) u = unit_part(p, slots, at, left);
+          left -= u.slots;
+          if (u.cnt == 0) left = -1;  // (the range ends before the unit's first tile)
+          at = 0;
           Piece* pc = &sh.pc[slot];
-          if (left <= 0) {
+          if (left < 0) {
             pc->cnt = 0;
             mbar_arrive(smem_addr(&sh.pc_full[slot]));
             break;
           }
-          const int cnt = min(left, nt - tile);
-          const int first = it.lo / kKT + tile;
+          const int cnt = u.cnt;
+          const int first = it.lo / kKT + u.tile;
           pc->cnt = cnt;
           pc->kt0 = first;
-          pc->step0 = step;
           pc->kvh = kvh;
           pc->b = it.b;
           pc->q0 = it.q0;
@@ -354,12 +369,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             pc->ga[g] = it.ghi[g] > 0 ? max(a, 0) : 0;
             pc->gb[g] = it.ghi[g] > 0 ? min(z, cnt) : 0;
           }
-          pc->whole = tile == 0 && cnt == nt;
+          pc->whole = cnt == u.nt;
           pc->slot = n == 0 ? 0 : 1;
           mbar_arrive(smem_addr(&sh.pc_full[slot]));
-          if (tile == 0 && cnt != nt) {  // the unit begins here and goes on in the next CTAs
-            const int64_t ubeg = static_cast<int64_t>(sum) * p.Hkv + static_cast<int64_t>(kvh) * nt;
-            cut = make_int4(item, kvh, n == 0 ? 0 : 1, static_cast<int>((ubeg + nt - 1) / per) - s + 1);
+          if (u.tile == 0 && cnt != u.nt) {  // the unit begins here and goes on in the next CTAs
+            const int64_t ubeg = static_cast<int64_t>(sum) * p.Hkv + static_cast<int64_t>(kvh) * slots;
+            cut = make_int4(item, kvh, n == 0 ? 0 : 1, static_cast<int>((ubeg + slots - 1) / per) - s + 1);
           }
           // its Q, once the products of the piece before have read theirs
           if (n > 0 && !(ok = wait_or_abort(smem_addr(&sh.qempty), (n - 1) & 1, p.err, abort_flag))) break;
@@ -371,9 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < DCH; ++c)
               tma_load_3d(q + m * C::SLOT + c * C::CHUNK, &tmq, c * 64, kvh * p.G, tok + m * ht, bar, policy);
           ++loaded;
-          left -= cnt;
-          step += cnt;
-          tile = 0;
           if (++kvh == p.Hkv) {
             kvh = 0;
             ++item;
@@ -520,20 +532,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t tp = tmem + kColS + g * kGroupCols, to = tmem + kColO + g * kGroupCols;
               // the group's first tile of the piece overwrites O
               uint32_t acc = j != ga;
-#pragma unroll 1
-              for (int h = 0; h < 2 && ok; ++h) {  // P comes in two halves
-                if (!(ok = wait_warp(smem_addr(&sh.pfull[g][h]), ppar >> g & 1, p.err, abort_flag))) break;
-                tc05::fence_after_sync();
+              if (!(ok = wait_warp(smem_addr(&sh.pfull[g]), ppar >> g & 1, p.err, abort_flag))) break;
+              tc05::fence_after_sync();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int kk = 4 * h + k;
-                  if (kk >= s0 && kk < s1) {
-                    tc05::mma_ts_warp(to, tp + 8 * kk, dv + (kk * 2048 >> 4), id_pv, acc);
-                    acc = 1;
-                  }
+              for (int k = 0; k < kKT / 16; ++k) {
+                if (k >= s0 && k < s1) {
+                  tc05::mma_ts_warp(to, tp + 8 * k, dv + (k * 2048 >> 4), id_pv, acc);
+                  acc = 1;
                 }
               }
-              if (!ok) break;
               ppar ^= 1u << g;
               if (j == gb - 1) tc05::commit_warp(smem_addr(&sh.ofull[g]));
             }
@@ -571,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool CAP_ONLY = C::CAP && !C::BIAS;
     constexpr bool PLAIN = !C::CAP && !C::BIAS;  // (with a positive scale: it commutes with the maximum)
     const float mul = PLAIN ? p.scale_log2 : 1.f;
+    const bool wide_out = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
     const int r = 32 * w + lane;  // row of the M tile
 
     // items whose rows see nothing have no tile: their rows are zero
@@ -592,16 +600,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     int done = 0, pieces = 0;  // phases of sfull and ofull
-    bool ok = true;
+    // rows of this group in a piece's M tile, and this thread's row of the sequence
+    auto rows_of = [&](const Piece& pc) { return min(HR, pc.rows - g * HR); };
+    auto mine = [&](const Piece& pc) { return pc.row0 + g * HR + min(r, max(rows_of(pc), 1) - 1); };
+    RowLoads next{0, 0, 0.f};
+    bool ok = piece_wait(0);
+    if (ok && sh.pc[0].cnt != 0 && rows_of(sh.pc[0]) > 0) next = load_row(p, sh.pc[0], mine(sh.pc[0]));
     for (int i = 0; ok; ++i) {
-      if (!(ok = piece_wait(i))) break;
-      const Piece& pc = sh.pc[i % kPieces];
+      const Piece& pc = sh.pc[i % kPieces];  // (waited for)
       const int cnt = pc.cnt;
       if (cnt == 0) break;
-      const int rows = min(HR, pc.rows - g * HR);  // of this M tile
-      const int f = pc.row0 + g * HR + min(r, max(rows, 1) - 1);
+      const int rows = rows_of(pc), f = mine(pc);
       Row row{0, 0, 0, 0.f};
-      if (rows > 0) row = row_of(p, pc, f);
+      if (rows > 0) row = row_of(p, pc, f, next);
       const int ja = pc.ga[g], jb = pc.gb[g];
       const bool active = ja < jb;
       // keys that every row of the warp sees, and its first position
@@ -618,8 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc05::fence_after_sync();
         if (32 * w >= rows) {  // none of the warp's rows is a row of the item
           tc05::fence_before_sync();
-          mbar_arrive(smem_addr(&sh.pfull[g][0]));
-          mbar_arrive(smem_addr(&sh.pfull[g][1]));
+          mbar_arrive(smem_addr(&sh.pfull[g]));
           continue;
         }
         const int key0 = (pc.kt0 + j) * kKT;
@@ -668,7 +678,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float2 mul2 = splat(mul), ref2 = splat(m_ref == -INFINITY ? 0.f : -m_ref);
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-        // P in two halves, so that the product of the first runs while the second is computed
         auto weights = [&](const float* y64, int h) {
           uint32_t v[32];
 #pragma unroll
@@ -681,9 +690,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[e] = pack_bf16x2(y.x, y.y);
           }
           tc05::st32(ts + 32 * h, v);
-          tc05::wait_st();
-          tc05::fence_before_sync();
-          mbar_arrive(smem_addr(&sh.pfull[g][h]));
         };
         if constexpr (CAP_ONLY) {
 #pragma unroll 1
@@ -705,11 +711,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           weights(x, 0);
           weights(x + 64, 1);
         }
+        // (P as a whole: where its halves were signalled one by one, the products waited for the
+        // second half of one group while the other group's P lay ready: 790 us against 700)
+        tc05::wait_st();
+        tc05::fence_before_sync();
+        mbar_arrive(smem_addr(&sh.pfull[g]));
         l += (l0.x + l0.y) + (l1.x + l1.y);
       }
       if (!ok) break;
 
       // ---- the piece's output, or its partial ----
+      if (!(ok = piece_wait(i + 1))) break;
+      {
+        const Piece& np = sh.pc[(i + 1) % kPieces];
+        if (np.cnt != 0 && rows_of(np) > 0) next = load_row(p, np, mine(np));
+      }
       const bool whole = pc.whole;
       const int64_t base = static_cast<int64_t>(s) * 2 + pc.slot;
       if (active) {
@@ -737,11 +753,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (r < rows) {
             if (whole) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                auto at = [&](int u) { return __uint_as_float(v[e + u]) * inv; };
-                *reinterpret_cast<uint4*>(o + c + e) =
-                    make_uint4(pack_bf16x2(at(0), at(1)), pack_bf16x2(at(2), at(3)), pack_bf16x2(at(4), at(5)),
-                               pack_bf16x2(at(6), at(7)));
+              for (int e = 0; e < 32; e += 16) {
+                uint32_t u[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  u[k] = pack_bf16x2(__uint_as_float(v[e + 2 * k]) * inv, __uint_as_float(v[e + 2 * k + 1]) * inv);
+                if (wide_out) {  // whole 32-byte sectors: every lane writes a line of its own
+                  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + c + e), "r"(u[0]),
+                               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                               : "memory");
+                } else {
+                  *reinterpret_cast<uint4*>(o + c + e) = make_uint4(u[0], u[1], u[2], u[3]);
+                  *reinterpret_cast<uint4*>(o + c + e + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+                }
               }
             } else {
 #pragma unroll
@@ -792,6 +816,9 @@ cudaError_t run(const AttnParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// What a unit costs beside its tiles, in tiles.
+int attention_tc_extra() { return 1; }
 
 // Rows per item: two M tiles of whole tokens.
 int attention_tc_rows(int G) { return 2 * (128 / G) * G; }

@@ -147,11 +147,12 @@ struct AttnParams {
   int32_t* err;
   // the plan (in the workspace): rows per item, keys per tile, CTAs of the main kernel
   int RT, KT, ctas, max_items;
+  int extra;                    // what a unit costs beside its tiles, in tiles
   int HR;                       // rows of a softmax group of the tensor-core kernel (RT, or RT / 2)
-  int32_t* header;              // [2]: items, tiles (of one KV head)
+  int32_t* header;              // [2]: items, slots (tiles and extra ones, of one KV head)
   int32_t* seq_items;           // [B] items before the sequence
   AttnItem* items;              // [max_items]
-  int32_t* tile_sum;            // [max_items + 1] tiles before the item
+  int32_t* tile_sum;            // [max_items + 1] slots before the item
   AttnStart* starts;            // [ctas]
   int32_t* cuts;                // [ctas][4]: item, KV head, slot, pieces of the cut unit that
                                 // begins in the CTA (item -1: none)
@@ -162,6 +163,7 @@ cudaError_t launch_attention_plan(const AttnParams& p, cudaStream_t stream);
 cudaError_t launch_attention_generic(const AttnParams& p, pa_dtype dtype, cudaStream_t stream);
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t stream);
 int attention_tc_rows(int G);
+int attention_tc_extra();
 cudaError_t launch_attention_tokens(const AttnParams& p, cudaStream_t stream);  // its join included
 bool attention_tokens_eligible(int max_query_len, int G, int B);
 int attention_tokens_ranges(int sms);
