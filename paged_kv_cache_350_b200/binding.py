@@ -222,7 +222,8 @@ def _ptr(t):
 def _stream(stream):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle itself: making a Stream object of it takes 3 us
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -245,12 +246,17 @@ def _on_device(*ts, err_flag=None):
     raw device pointers and launches there, so a host tensor would be read by a kernel.
     err_flag, when given, is an int32 device tensor of at least one element."""
     import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    dev = None
     for t in (*ts, err_flag):
         if t is None:
             continue
-        _need(t.is_cuda, "tensors must be CUDA tensors (the library takes device pointers)")
-        _need(t.device.index == dev, f"tensors must be on the current device (cuda:{dev})")
+        at = t.get_device()
+        if at < 0:
+            raise ValueError("tensors must be CUDA tensors (the library takes device pointers)")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if at != dev:
+            raise ValueError(f"tensors must be on the current device (cuda:{dev})")
     _need(err_flag is None or (err_flag.dtype == torch.int32 and err_flag.numel() >= 1),
           "err_flag must be an int32 tensor of at least one element")
 
@@ -489,15 +495,28 @@ def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=PA_ROPE_SCALE_NONE, fa
     return out, f.value
 
 
+# The calls of a step take a few microseconds on the GPU, so their checks are written to take as
+# little on the host: attributes are read once, messages are built on failure only.
+
 def _token_rows(t, name):
     """Elements between the tokens of [T, H, D] rows whose heads lie side by side."""
-    _need(t.dim() == 3, f"{name} must be [T, heads, D]")
-    T, H, D = t.shape
-    _need((t.stride(2) == 1 or D == 1) and (t.stride(1) == D or H == 1),
-          f"{name}: the heads of a token must be contiguous")
-    # (the stride of a single token is arbitrary)
-    _need(T <= 1 or t.stride(0) >= H * D, f"{name}: tokens must not overlap")
-    return t.stride(0) if T > 1 else H * D
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [T, heads, D]")
+    T, H, D = shape
+    if not ((stride[2] == 1 or D == 1) and (stride[1] == D or H == 1)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if T <= 1:  # (the stride of a single token is arbitrary)
+        return H * D
+    if stride[0] < H * D:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return stride[0]
+
+
+def _contiguous(names, *ts):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{names} must be contiguous")
 
 
 def pa_rope_and_cache(q_out, q, k, v, k_pool, v_pool, positions, slot_mapping, inv_freq,
@@ -505,25 +524,32 @@ def pa_rope_and_cache(q_out, q, k, v, k_pool, v_pool, positions, slot_mapping, i
     """Rotate q [T,Hq,D] into q_out and k [T,Hkv,D] into its slots, v unchanged into its own
     (see include/pa.h); the rotated part of a head is 2 * inv_freq.numel() elements."""
     import torch
-    _need(k_pool.dim() == 4 and v_pool.shape == k_pool.shape, "pools must be [NB, bs, Hkv, D]")
-    NB, bs, Hkv, D = k_pool.shape
-    strides = [_token_rows(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
-    T, Hq = q.shape[:2]
-    _need(q.shape[2] == D and k.shape == (T, Hkv, D) and v.shape == k.shape, "q/k/v shape mismatch")
-    _need(q_out.shape == q.shape, "q_out must have q's shape")
-    _need(positions.dtype == torch.int32 and positions.numel() == T, "positions int32 [T]")
-    _need(slot_mapping.dtype == torch.int64 and slot_mapping.numel() == T, "slot_mapping int64 [T]")
-    _need(inv_freq.dtype == torch.float64 and inv_freq.dim() == 1, "inv_freq float64 [rotary_dim / 2]")
-    _need(q.dtype == k.dtype == v.dtype == q_out.dtype == k_pool.dtype == v_pool.dtype,
-          "q, k, v, q_out and pools share a dtype")
-    for t in (q_out, k_pool, v_pool, positions, slot_mapping, inv_freq):
-        _need(t.is_contiguous(), "q_out, pools and index tensors must be contiguous")
+    pool, dt = k_pool.shape, q.dtype
+    if len(pool) != 4 or v_pool.shape != pool:
+        raise ValueError("pools must be [NB, bs, Hkv, D]")
+    NB, bs, Hkv, D = pool
+    qs, ks, vs = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
+    T, Hq, Dq = q.shape
+    if Dq != D or tuple(k.shape) != (T, Hkv, D) or v.shape != k.shape:
+        raise ValueError("q/k/v shape mismatch")
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    if positions.dtype != torch.int32 or positions.numel() != T:
+        raise ValueError("positions int32 [T]")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+        raise ValueError("slot_mapping int64 [T]")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise ValueError("inv_freq float64 [rotary_dim / 2]")
+    if not (dt == k.dtype == v.dtype == q_out.dtype == k_pool.dtype == v_pool.dtype):
+        raise ValueError("q, k, v, q_out and pools share a dtype")
+    _contiguous("q_out, pools and index tensors", q_out, k_pool, v_pool, positions, slot_mapping, inv_freq)
     _on_device(q_out, q, k, v, k_pool, v_pool, positions, slot_mapping, inv_freq, err_flag=err_flag)
-    st = lib.pa_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool),
-                               _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq), T, Hq, Hkv, D,
-                               bs, NB, *strides, 2 * inv_freq.numel(), layout, float(attn_factor),
-                               _dtype_of(q), _ptr(err_flag), _stream(stream))
-    _check(st, "pa_rope_and_cache")
+    st = lib.pa_rope_and_cache(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pool.data_ptr(),
+                               v_pool.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(),
+                               inv_freq.data_ptr(), T, Hq, Hkv, D, bs, NB, qs, ks, vs, 2 * inv_freq.numel(),
+                               layout, float(attn_factor), _dtype_of(q), _ptr(err_flag), _stream(stream))
+    if st:
+        _check(st, "pa_rope_and_cache")
 
 
 def pa_attention_workspace_size(T, B, max_query_len, Hq, Hkv, D, block_size, max_blocks):
@@ -540,32 +566,47 @@ def pa_attention(out, q, k_pool, v_pool, block_tables, seq_lens, query_starts, m
     include/pa.h): sequence b's tokens are rows query_starts[b] .. query_starts[b + 1] - 1."""
     import torch
     stride = _token_rows(q, "q")
-    _need(out.shape == q.shape, "out must have q's shape")
-    _need(k_pool.dim() == 4 and v_pool.shape == k_pool.shape, "pools must be [NB, bs, Hkv, D]")
-    _need(block_tables.dim() == 2 and block_tables.dtype == torch.int32, "block_tables int32 [B, MB]")
-    T, Hq, D = q.shape
-    NB, bs, Hkv, D2 = k_pool.shape
-    B = block_tables.shape[0]
-    _need(D2 == D, "head dim mismatch")
-    _need(seq_lens.dtype == torch.int32 and seq_lens.numel() == B, "seq_lens int32 [B]")
-    _need(query_starts.dtype == torch.int32 and query_starts.numel() == B + 1, "query_starts int32 [B + 1]")
-    for t, n, dt, name in ((alibi_slopes, Hq, torch.float32, "alibi_slopes float32 [Hq]"),
-                           (prefix_lens, B, torch.int32, "prefix_lens int32 [B]"),
-                           (first_keys, T, torch.int32, "first_keys int32 [T]")):
-        _need(t is None or (t.dtype == dt and t.numel() == n and t.is_contiguous()), name)
-    for t in (out, k_pool, v_pool, block_tables, seq_lens, query_starts):
-        _need(t.is_contiguous(), "out, pools and index tensors must be contiguous")
-    _need(q.dtype == out.dtype == k_pool.dtype == v_pool.dtype, "q, out and pools share a dtype")
+    shape, pool, i32 = q.shape, k_pool.shape, torch.int32
+    if out.shape != shape:
+        raise ValueError("out must have q's shape")
+    if len(pool) != 4 or v_pool.shape != pool:
+        raise ValueError("pools must be [NB, bs, Hkv, D]")
+    if block_tables.dim() != 2 or block_tables.dtype != i32:
+        raise ValueError("block_tables int32 [B, MB]")
+    T, Hq, D = shape
+    NB, bs, Hkv, D2 = pool
+    B, MB = block_tables.shape
+    if D2 != D:
+        raise ValueError("head dim mismatch")
+    if seq_lens.dtype != i32 or seq_lens.numel() != B:
+        raise ValueError("seq_lens int32 [B]")
+    if query_starts.dtype != i32 or query_starts.numel() != B + 1:
+        raise ValueError("query_starts int32 [B + 1]")
+    mods = None
+    if softcap or window or alibi_slopes is not None or prefix_lens is not None or first_keys is not None:
+        for t, n, dt, name in ((alibi_slopes, Hq, torch.float32, "alibi_slopes float32 [Hq]"),
+                               (prefix_lens, B, i32, "prefix_lens int32 [B]"),
+                               (first_keys, T, i32, "first_keys int32 [T]")):
+            if t is not None and (t.dtype != dt or t.numel() != n):
+                raise ValueError(name)
+        mods = ctypes.byref(pa_attention_mods(float(softcap), int(window),
+                                              None if alibi_slopes is None else alibi_slopes.data_ptr(),
+                                              None if prefix_lens is None else prefix_lens.data_ptr(),
+                                              None if first_keys is None else first_keys.data_ptr()))
+    dt = q.dtype
+    if not (dt == out.dtype == k_pool.dtype == v_pool.dtype):
+        raise ValueError("q, out and pools share a dtype")
+    _contiguous("out, pools and index tensors", out, k_pool, v_pool, block_tables, seq_lens, query_starts,
+                alibi_slopes, prefix_lens, first_keys, workspace)
     _on_device(out, q, k_pool, v_pool, block_tables, seq_lens, query_starts, alibi_slopes, prefix_lens,
                first_keys, workspace, err_flag=err_flag)
-    mods = pa_attention_mods(float(softcap), int(window), *(t.data_ptr() if t is not None else None
-                                                            for t in (alibi_slopes, prefix_lens, first_keys)))
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = lib.pa_attention(_ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables),
-                          _ptr(seq_lens), _ptr(query_starts), T, B, int(max_query_len), Hq, Hkv, D, bs,
-                          block_tables.shape[1], NB, stride, float(scale), ctypes.byref(mods),
-                          _dtype_of(q), _ptr(workspace), wbytes, _ptr(err_flag), _stream(stream))
-    _check(st, "pa_attention")
+    st = lib.pa_attention(out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                          block_tables.data_ptr(), seq_lens.data_ptr(), query_starts.data_ptr(), T, B,
+                          int(max_query_len), Hq, Hkv, D, bs, MB, NB, stride, float(scale), mods, _dtype_of(q),
+                          _ptr(workspace), wbytes, _ptr(err_flag), _stream(stream))
+    if st:
+        _check(st, "pa_attention")
     return out
 
 
@@ -581,41 +622,54 @@ def pa_beam_topk(scores, parents, tokens, logits, cum_scores, finished=None, eos
     """The k best candidates of every request (scores, parents, tokens: [N, k]) from logits
     [N, W, V] and the beams' scores so far [N, W] (see include/pa.h)."""
     import torch
-    _need(logits.dim() == 3, "logits must be [N, W, V]")
-    N, W, V = logits.shape
-    _need((logits.stride(2) == 1 or V == 1) and (N <= 1 or W <= 1 or logits.stride(0) == W * logits.stride(1)),
-          "logits: rows contiguous, at one stride")
-    row = logits.stride(1) if W > 1 else (logits.stride(0) if N > 1 else V)
-    _need(scores.dim() == 2 and scores.shape[0] == N and scores.dtype == torch.float32, "scores float32 [N, k]")
-    for t, name in ((parents, "parents"), (tokens, "tokens")):
-        _need(t.shape == scores.shape and t.dtype == torch.int32, f"{name} int32 [N, k]")
-    _need(cum_scores.dtype == torch.float32 and cum_scores.shape == (N, W), "cum_scores float32 [N, W]")
-    _need(finished is None or (finished.dtype in (torch.bool, torch.uint8) and finished.shape == (N, W)),
-          "finished bool or uint8 [N, W]")
-    for t in (scores, parents, tokens, cum_scores, finished):
-        _need(t is None or t.is_contiguous(), "tensors must be contiguous")
+    shape, stride = logits.shape, logits.stride()
+    if len(shape) != 3:
+        raise ValueError("logits must be [N, W, V]")
+    N, W, V = shape
+    if not ((stride[2] == 1 or V == 1) and (N <= 1 or W <= 1 or stride[0] == W * stride[1])):
+        raise ValueError("logits: rows contiguous, at one stride")
+    row = stride[1] if W > 1 else (stride[0] if N > 1 else V)
+    best = scores.shape
+    if len(best) != 2 or best[0] != N or scores.dtype != torch.float32:
+        raise ValueError("scores float32 [N, k]")
+    if parents.shape != best or parents.dtype != torch.int32:
+        raise ValueError("parents int32 [N, k]")
+    if tokens.shape != best or tokens.dtype != torch.int32:
+        raise ValueError("tokens int32 [N, k]")
+    if cum_scores.dtype != torch.float32 or tuple(cum_scores.shape) != (N, W):
+        raise ValueError("cum_scores float32 [N, W]")
+    if finished is not None and (finished.dtype not in (torch.bool, torch.uint8)
+                                 or tuple(finished.shape) != (N, W)):
+        raise ValueError("finished bool or uint8 [N, W]")
+    _contiguous("tensors", scores, parents, tokens, cum_scores, finished, workspace)
     _on_device(scores, parents, tokens, logits, cum_scores, finished, workspace)
     wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = lib.pa_beam_topk(_ptr(scores), _ptr(parents), _ptr(tokens), _ptr(logits), _ptr(cum_scores),
-                          _ptr(finished), int(eos_token), N, W, V, scores.shape[1], row,
+    st = lib.pa_beam_topk(scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), logits.data_ptr(),
+                          cum_scores.data_ptr(), _ptr(finished), int(eos_token), N, W, V, best[1], row,
                           _dtype_of(logits), _ptr(workspace), wbytes, _stream(stream))
-    _check(st, "pa_beam_topk")
+    if st:
+        _check(st, "pa_beam_topk")
 
 
 def pa_beam_gather(dst, src, parents, err_flag=None, stream=None):
     """dst[n][i] = src[n][parents[n][i]]: per-beam states [N, W, ...] in the order of parents [N, k]."""
     import torch
-    _need(parents.dim() == 2 and parents.dtype == torch.int32, "parents int32 [N, k]")
+    if parents.dim() != 2 or parents.dtype != torch.int32:
+        raise ValueError("parents int32 [N, k]")
     N, k = parents.shape
-    _need(src.dim() >= 2 and src.shape[0] == N, "src must be [N, W, ...]")
-    _need(dst.dtype == src.dtype and tuple(dst.shape) == (N, k, *src.shape[2:]), "dst must be [N, k, ...]")
-    for t in (dst, src, parents):
-        _need(t.is_contiguous(), "tensors must be contiguous")
+    shape = src.shape
+    if len(shape) < 2 or shape[0] != N:
+        raise ValueError("src must be [N, W, ...]")
+    if dst.dtype != src.dtype or tuple(dst.shape) != (N, k, *shape[2:]):
+        raise ValueError("dst must be [N, k, ...]")
+    _contiguous("tensors", dst, src, parents)
     _on_device(dst, src, parents, err_flag=err_flag)
-    row = src[0, 0].numel() * src.element_size() if src.numel() else 0
-    st = lib.pa_beam_gather(_ptr(dst), _ptr(src), _ptr(parents), N, max(src.shape[1], 1), max(k, 1) if row else 1,
-                            row if k else 0, _ptr(err_flag), _stream(stream))
-    _check(st, "pa_beam_gather")
+    W, n = shape[1], src.numel()
+    if n and k:
+        st = lib.pa_beam_gather(dst.data_ptr(), src.data_ptr(), parents.data_ptr(), N, W, k,
+                                n // (N * W) * src.element_size(), _ptr(err_flag), _stream(stream))
+        if st:
+            _check(st, "pa_beam_gather")
     return dst
 
 

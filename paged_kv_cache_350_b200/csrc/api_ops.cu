@@ -20,14 +20,6 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 // CTAs assumed per launch when no device can be asked.
 constexpr int kSmBound = 256;
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
 // The plan of a pa_attention call on `sms` multiprocessors: rows per item (and per softmax
 // group), keys per tile, CTAs.
 struct AttnShape {
@@ -108,6 +100,17 @@ bool attention_sizes_ok(int T, int B, int max_query_len, int Hq, int Hkv) {
 }
 
 }  // namespace
+
+int pa::device_sms() {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const bool kept = dev >= 0 && dev < kMaxDevices;
+  if (kept && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (kept) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
 
 extern "C" {
 
@@ -207,7 +210,7 @@ size_t pa_attention_workspace_size(int T, int B, int max_query_len, int Hq, int 
       !block_size_ok(block_size) || max_blocks <= 0)
     return static_cast<size_t>(-1);
   if (T == 0 || B == 0) return 0;
-  const int sms = sm_count() > 0 ? sm_count() : kSmBound;
+  const int known = pa::device_sms(), sms = known > 0 ? known : kSmBound;
   size_t n = 0;  // enough for either type
   const int most = std::max(max_query_len, 1), G = Hq / Hkv;
   for (const pa_dtype dtype : {PA_F32, PA_BF16})
@@ -243,7 +246,7 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
       (m.alibi_slopes && !aligned(m.alibi_slopes, 4)) || (m.prefix_lens && !aligned(m.prefix_lens, 4)) ||
       (m.first_keys && !aligned(m.first_keys, 4)))
     return PA_ERR_INVALID_ARG;
-  const int sms = sm_count();
+  const int sms = pa::device_sms();
   if (sms <= 0) return PA_ERR_CUDA;
   const int G = Hq / Hkv;
   const AttnKernel kernel = attention_kernel(B, max_query_len, G, block_size, dtype);

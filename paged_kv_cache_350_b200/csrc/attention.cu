@@ -483,29 +483,13 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnParams p)
     store4(o + (warp + 8 * c) * 4, make_float4(a[c].x * inv, a[c].y * inv, a[c].z * inv, a[c].w * inv));
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                   Args... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
 template <typename T, int D, int MR>
 cudaError_t run_generic(const AttnParams& p, cudaStream_t stream) {
   using C = GenCfg<D, MR>;
-  cudaError_t e = cudaFuncSetAttribute(attention_generic_kernel<T, D, MR>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static SmemGrant granted;
+  const cudaError_t e = grant_smem(granted, attention_generic_kernel<T, D, MR>, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch(attention_generic_kernel<T, D, MR>, dim3(static_cast<unsigned>(p.ctas)), kGenThreads, C::SMEM,
+  return launch_pdl(attention_generic_kernel<T, D, MR>, dim3(static_cast<unsigned>(p.ctas)), kGenThreads, C::SMEM,
                 stream, p);
 }
 
@@ -518,7 +502,7 @@ cudaError_t run_generic_t(const AttnParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_attention_plan(const AttnParams& p, cudaStream_t stream) {
-  return launch(attention_plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
+  return launch_pdl(attention_plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
 }
 
 cudaError_t launch_attention_generic(const AttnParams& p, pa_dtype dtype, cudaStream_t stream) {
@@ -528,10 +512,10 @@ cudaError_t launch_attention_generic(const AttnParams& p, pa_dtype dtype, cudaSt
 cudaError_t launch_attention_join(const AttnParams& p, pa_dtype dtype, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(p.ctas), static_cast<unsigned>((p.RT + 31) / 32));
   if (dtype == PA_BF16)
-    return p.D == 64 ? launch(attention_join_kernel<__nv_bfloat16, 64>, grid, 256, 0, stream, p)
-                     : launch(attention_join_kernel<__nv_bfloat16, 128>, grid, 256, 0, stream, p);
-  return p.D == 64 ? launch(attention_join_kernel<float, 64>, grid, 256, 0, stream, p)
-                   : launch(attention_join_kernel<float, 128>, grid, 256, 0, stream, p);
+    return p.D == 64 ? launch_pdl(attention_join_kernel<__nv_bfloat16, 64>, grid, 256, 0, stream, p)
+                     : launch_pdl(attention_join_kernel<__nv_bfloat16, 128>, grid, 256, 0, stream, p);
+  return p.D == 64 ? launch_pdl(attention_join_kernel<float, 64>, grid, 256, 0, stream, p)
+                   : launch_pdl(attention_join_kernel<float, 128>, grid, 256, 0, stream, p);
 }
 
 // By shared memory (228 KB per SM, 1 KB reserved per CTA), at most 4.

@@ -22,8 +22,6 @@
 // Every wait is bounded in time; on expiry the kernel records PA_DEVERR_TIMEOUT, every role
 // stops, loads and products in flight are drained (bounded) and the tensor memory is freed.
 
-#include <atomic>
-
 #include "attention.h"
 #include "tc05.cuh"
 
@@ -800,19 +798,11 @@ cudaError_t run(const AttnParams& p, cudaStream_t stream) {
       !make_pool_map(&tmv, p.v_pool, p.num_blocks, p.block_size, p.Hkv, C::D, p.block_size) ||
       !make_q_rows_map(&tmq, p.q, p.T, p.Hq, C::D, p.q_stride, p.G, tokens))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static SmemGrant granted;
+  const cudaError_t e = grant_smem(granted, attention_tc_kernel<C>, C::SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_tc_kernel<C>, tmk, tmv, tmq, p);
+  return launch_pdl(attention_tc_kernel<C>, dim3(static_cast<unsigned>(p.ctas)), kThreads, C::SMEM, stream, tmk, tmv,
+                    tmq, p);
 }
 
 }  // namespace

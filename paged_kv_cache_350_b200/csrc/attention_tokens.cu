@@ -450,21 +450,6 @@ __global__ void __launch_bounds__(1024) tokens_join_kernel(const AttnParams p, i
       make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kernel)(KArgs...), int grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
 template <class C>
 cudaError_t run(const AttnParams& p, cudaStream_t stream) {
   CUtensorMap tmk, tmv;
@@ -476,14 +461,16 @@ cudaError_t run(const AttnParams& p, cudaStream_t stream) {
                                       make_pool_map(&tmv, p.v_pool, p.num_blocks, C::BS, p.Hkv, C::D, C::BOXR);
   if (!maps) return cudaErrorInvalidValue;
   const size_t smem = tokens_smem<C>(p.B);
-  cudaError_t e = cudaFuncSetAttribute(attention_tokens_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e == cudaSuccess) e = launch(attention_tokens_kernel<C>, p.ctas / kWarps, kThreads, smem, stream, tmk, tmv, p);
+  static SmemGrant granted;
+  cudaError_t e = grant_smem(granted, attention_tokens_kernel<C>, static_cast<int>(smem));
+  if (e == cudaSuccess)
+    e = launch_pdl(attention_tokens_kernel<C>, dim3(static_cast<unsigned>(p.ctas / kWarps)), kThreads, smem, stream, tmk,
+                   tmv, p);
   if (e != cudaSuccess) return e;
   const int BT = (p.RT * C::D / 4 + 31) / 32 * 32;
   // several pieces per unit are the rule where units are fewer than ranges
   const int PS = static_cast<int64_t>(p.B) * p.Hkv < p.ctas ? (1024 / BT < 1 ? 1 : 1024 / BT < 4 ? 1024 / BT : 4) : 1;
-  return launch(tokens_join_kernel<C::D>, p.ctas, BT * PS, PS > 1 ? static_cast<size_t>(PS) * BT * 24 : 0, stream, p,
+  return launch_pdl(tokens_join_kernel<C::D>, dim3(static_cast<unsigned>(p.ctas)), BT * PS, PS > 1 ? static_cast<size_t>(PS) * BT * 24 : 0, stream, p,
                 BT, PS);
 }
 

@@ -301,26 +301,12 @@ __global__ void __launch_bounds__(kThreads) beam_gather_kernel(V* __restrict__ d
   for (int64_t i = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x; i < vecs; i += step) d[i] = s[i];
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, cudaStream_t stream, Args... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
 template <typename T>
 cudaError_t launch_rows(const BeamParams& p, cudaStream_t stream) {
   const bool vec = p.row_stride % Load<T>::N == 0 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
   const dim3 grid(static_cast<unsigned>(p.N * p.W * p.chunks));
-  return vec ? launch(beam_rows_kernel<T, true>, grid, stream, p)
-             : launch(beam_rows_kernel<T, false>, grid, stream, p);
+  return vec ? launch_pdl(beam_rows_kernel<T, true>, grid, kThreads, 0, stream, p)
+             : launch_pdl(beam_rows_kernel<T, false>, grid, kThreads, 0, stream, p);
 }
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -353,7 +339,7 @@ cudaError_t launch_beam_topk(BeamParams p, pa_dtype dtype, void* workspace, cuda
   p.ws_idx = reinterpret_cast<int32_t*>(ws + up256(n * 8) + up256(n * 4) + up256(n * p.k * 4));
   cudaError_t e = dtype == PA_BF16 ? launch_rows<__nv_bfloat16>(p, stream) : launch_rows<float>(p, stream);
   if (e != cudaSuccess) return e;
-  return launch(beam_join_kernel, dim3(static_cast<unsigned>(p.N)), stream, p);
+  return launch_pdl(beam_join_kernel, dim3(static_cast<unsigned>(p.N)), kThreads, 0, stream, p);
 }
 
 cudaError_t launch_beam_gather(void* dst, const void* src, const int32_t* parents, int N, int W, int k,
@@ -365,7 +351,7 @@ cudaError_t launch_beam_gather(void* dst, const void* src, const int32_t* parent
     const int64_t vecs = row_bytes / static_cast<int64_t>(sizeof(V));
     int64_t gy = (vecs + kThreads * 4 - 1) / (kThreads * 4);
     if (gy > 64) gy = 64;
-    return launch(beam_gather_kernel<V>, dim3(static_cast<unsigned>(N * k), static_cast<unsigned>(gy)), stream,
+    return launch_pdl(beam_gather_kernel<V>, dim3(static_cast<unsigned>(N * k), static_cast<unsigned>(gy)), kThreads, 0, stream,
                   static_cast<V*>(dst), static_cast<const V*>(src), parents, W, k, vecs, err);
   };
   if (a % 16 == 0) return go(static_cast<uint4*>(nullptr));

@@ -6,9 +6,53 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pa.h"
 
 namespace pa {
+
+// Devices that per-device state is kept for.
+constexpr int kMaxDevices = 64;
+
+// Multiprocessors of the current device, asked once per device; 0 if unknown.
+int device_sms();
+
+// Grant `kernel` its dynamic shared memory on the current device; `granted` (one per kernel and
+// device) holds what it has, so that most launches make no call.
+struct SmemGrant {
+  std::atomic<int> bytes[kMaxDevices];
+};
+template <typename K>
+cudaError_t grant_smem(SmemGrant& g, K kernel, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  int have = g.bytes[dev].load(std::memory_order_relaxed);
+  if (bytes <= have) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  while (e == cudaSuccess && have < bytes && !g.bytes[dev].compare_exchange_weak(have, bytes)) {
+  }
+  return e;
+}
+
+// Launch as a programmatic dependent of the previous kernel on the stream: the kernel calls
+// griddepcontrol.wait before it touches global memory.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                       const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
 
 // Parameters of one pa_decode call, as the kernels see them.
 struct DecodeParams {

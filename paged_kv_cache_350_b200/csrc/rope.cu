@@ -236,21 +236,6 @@ __global__ void __launch_bounds__(kThreads) rope_scalar_kernel(const RopeParams 
     for (int i = threadIdx.x; i < p.Hkv * D; i += kThreads) vp[i] = v[i];
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const RopeParams& p, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.T));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.R / 2) * sizeof(float2);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 template <typename T>
 cudaError_t launch_t(const RopeParams& p, cudaStream_t stream) {
   constexpr int N = Vec<T>::N;
@@ -259,9 +244,11 @@ cudaError_t launch_t(const RopeParams& p, cudaStream_t stream) {
                    mult(p.k_stride) && mult(p.v_stride) &&
                    (reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) |
                     reinterpret_cast<uintptr_t>(p.v)) % 16 == 0;
-  if (!vec) return launch(rope_scalar_kernel<T>, p, stream);
-  return p.half ? launch(rope_vec_kernel<T, true>, p, stream)
-                : launch(rope_vec_kernel<T, false>, p, stream);
+  const dim3 grid(static_cast<unsigned>(p.T));
+  const size_t smem = static_cast<size_t>(p.R / 2) * sizeof(float2);
+  if (!vec) return launch_pdl(rope_scalar_kernel<T>, grid, kThreads, smem, stream, p);
+  return p.half ? launch_pdl(rope_vec_kernel<T, true>, grid, kThreads, smem, stream, p)
+                : launch_pdl(rope_vec_kernel<T, false>, grid, kThreads, smem, stream, p);
 }
 
 }  // namespace
