@@ -34,6 +34,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanKept = 4096;  // sequences, items
 
 // ---- plan --------------------------------------------------------------------------------
 
@@ -72,6 +73,11 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ int sums[33];
+  // what the searches below read, in shared memory where it fits (each step of a search is a
+  // round trip)
+  __shared__ int seq_sh[kPlanKept], sum_sh[kPlanKept];
+  int* seq_items = p.B <= kPlanKept ? seq_sh : p.seq_items;
+  int* slots_before = p.max_items < kPlanKept ? sum_sh : p.tile_sum;
   int items = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
@@ -79,7 +85,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     if (b < p.B) n = (static_cast<int64_t>(attn_query_span(p, b, true, q0)) * p.G + p.RT - 1) / p.RT;
     int total;
     const int at = block_scan(n, sums, total);
-    if (b < p.B) p.seq_items[b] = items + at;
+    if (b < p.B) seq_items[b] = items + at;
     items += total;
   }
   // overlapping spans (malformed) could exceed the host's bound
@@ -96,13 +102,13 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
       int a = 0, z = p.B;  // the last sequence whose items begin at or before i
       while (z - a > 1) {
         const int mid = (a + z) >> 1;
-        if (p.seq_items[mid] <= i) a = mid; else z = mid;
+        if (seq_items[mid] <= i) a = mid; else z = mid;
       }
       AttnItem it;
       it.b = a;
       const int n = attn_query_span(p, a, false, it.q0);
       const int nrows = n * p.G;
-      it.row0 = (i - p.seq_items[a]) * p.RT;
+      it.row0 = (i - seq_items[a]) * p.RT;
       it.rows = min(p.RT, nrows - it.row0);
       it.L = attn_len(p, a, true);
       it.pos0 = it.L - n;
@@ -147,11 +153,11 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     }
     int total;
     const int at = block_scan(nt, sums, total);
-    if (i < items) p.tile_sum[i] = tiles + at;
+    if (i < items) slots_before[i] = p.tile_sum[i] = tiles + at;
     tiles += total;
   }
   if (threadIdx.x == 0) {
-    p.tile_sum[items] = tiles;
+    slots_before[items] = p.tile_sum[items] = tiles;
     p.header[0] = items;
     p.header[1] = tiles;
   }
@@ -166,10 +172,10 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
       int a = 0, z = items;  // the last item whose tiles begin at or before v (and has some)
       while (z - a > 1) {
         const int mid = (a + z) >> 1;
-        if (p.tile_sum[mid] <= v) a = mid; else z = mid;
+        if (slots_before[mid] <= v) a = mid; else z = mid;
       }
-      const int nt = p.tile_sum[a + 1] - p.tile_sum[a];
-      const int off = static_cast<int>(beg - static_cast<int64_t>(p.tile_sum[a]) * p.Hkv);
+      const int nt = slots_before[a + 1] - slots_before[a];
+      const int off = static_cast<int>(beg - static_cast<int64_t>(slots_before[a]) * p.Hkv);
       st.item = a;
       st.kvh = off / nt;
       st.tile = off - st.kvh * nt;

@@ -25,6 +25,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4, kThreads = kWarps * 32, kStages = 2;  // per CTA; ring stages per warp
+constexpr int kMinTiles = 4;
 
 template <int D_, int BS_, bool ROWS16_>
 struct TokensCfg : TileCfg<D_, BS_, ROWS16_, 16, true> {
@@ -208,7 +209,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   const int T = Hkv * P[B];
   const int S = static_cast<int>(gridDim.x) * kWarps;
-  const int per = max((T + S - 1) / S, 1);
+  // (no range below kMinTiles: where a single request leaves each warp less, a piece more costs
+  // the join as much as the tiles)
+  const int per = max((T + S - 1) / S, kMinTiles);
   const int s = static_cast<int>(blockIdx.x) * kWarps + warp;
   const int beg = min(T, s * per), end = min(T, beg + per), cnt = end - beg;
   const uint64_t policy = l2_policy_evict_first();
@@ -405,41 +408,44 @@ __global__ void __launch_bounds__(1024) tokens_join_kernel(const AttnParams p, i
   const int grp = threadIdx.x / BT, idx = threadIdx.x - grp * BT;
   const int r = idx / (D / 4), c = idx % (D / 4) * 4;
   const bool live = r < rows;
+  auto row_of = [&](int i) { return (static_cast<int64_t>(s + i) * 2 + (i == 0 ? cut.y : 0)) * p.RT + r; };
+  const float2* part = reinterpret_cast<const float2*>(p.part_ml);
+  // the maxima first: then the pieces' loads do not wait for one another
   float M = -INFINITY, l = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float m2, float l2, float4 o) {
-    const float Mn = fmaxf(M, m2);
-    if (Mn == -INFINITY) return;  // neither holds a key
-    const float so = exp2f(M - Mn), sn = exp2f(m2 - Mn);
-    l = l * so + l2 * sn;
-    a.x = a.x * so + o.x * sn;
-    a.y = a.y * so + o.y * sn;
-    a.z = a.z * so + o.z * sn;
-    a.w = a.w * so + o.w * sn;
-    M = Mn;
-  };
   if (live) {
+#pragma unroll 8
+    for (int i = 0; i < cut.z; ++i) M = fmaxf(M, part[row_of(i)].x);
+    const float ref = M == -INFINITY ? 0.f : M;  // no key at all: every weight is 0
 #pragma unroll 4
     for (int i = grp; i < cut.z; i += PS) {
-      const int64_t row = (static_cast<int64_t>(s + i) * 2 + (i == 0 ? cut.y : 0)) * p.RT + r;
-      const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[row];
-      add(ml.x, ml.y, *reinterpret_cast<const float4*>(p.part_acc + row * D + c));
+      const float2 ml = part[row_of(i)];
+      const float4 o = *reinterpret_cast<const float4*>(p.part_acc + row_of(i) * D + c);
+      const float w = exp2f(ml.x - ref);
+      l = fmaf(ml.y, w, l);
+      a.x = fmaf(o.x, w, a.x);
+      a.y = fmaf(o.y, w, a.y);
+      a.z = fmaf(o.z, w, a.z);
+      a.w = fmaf(o.w, w, a.w);
     }
   }
   if (PS > 1) {
-    extern __shared__ float red[];  // [PS][BT][6]
-    float* mine = red + (grp * BT + idx) * 6;
-    mine[0] = M;
-    mine[1] = l;
-    mine[2] = a.x;
-    mine[3] = a.y;
-    mine[4] = a.z;
-    mine[5] = a.w;
+    extern __shared__ float red[];  // [PS][BT][5]
+    float* mine = red + (grp * BT + idx) * 5;
+    mine[0] = l;
+    mine[1] = a.x;
+    mine[2] = a.y;
+    mine[3] = a.z;
+    mine[4] = a.w;
     __syncthreads();
     if (grp != 0) return;
     for (int k = 1; k < PS; ++k) {
-      const float* o = red + (k * BT + idx) * 6;
-      add(o[0], o[1], make_float4(o[2], o[3], o[4], o[5]));
+      const float* o = red + (k * BT + idx) * 5;
+      l += o[0];
+      a.x += o[1];
+      a.y += o[2];
+      a.z += o[3];
+      a.w += o[4];
     }
   }
   if (!live) return;
@@ -470,7 +476,7 @@ cudaError_t run(const AttnParams& p, cudaStream_t stream) {
   const int BT = (p.RT * C::D / 4 + 31) / 32 * 32;
   // several pieces per unit are the rule where units are fewer than ranges
   const int PS = static_cast<int64_t>(p.B) * p.Hkv < p.ctas ? (1024 / BT < 1 ? 1 : 1024 / BT < 4 ? 1024 / BT : 4) : 1;
-  return launch_pdl(tokens_join_kernel<C::D>, dim3(static_cast<unsigned>(p.ctas)), BT * PS, PS > 1 ? static_cast<size_t>(PS) * BT * 24 : 0, stream, p,
+  return launch_pdl(tokens_join_kernel<C::D>, dim3(static_cast<unsigned>(p.ctas)), BT * PS, PS > 1 ? static_cast<size_t>(PS) * BT * 20 : 0, stream, p,
                 BT, PS);
 }
 

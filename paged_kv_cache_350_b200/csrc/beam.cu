@@ -7,10 +7,13 @@
 // exponentials) and the k largest logits, and the scores are formed for those alone.
 //
 // Bound by reading the logits once.  Row chunks go to one CTA each; a warp walks its part
-// of the chunk in 16-byte vectors and keeps the k best so far sorted across its lanes (lane i
-// holds the i-th).  A batch none of whose values reaches the k-th best costs one comparison of
-// its maximum, which the softmax needs anyway.  A second, small kernel joins the chunks of each
-// beam and then the beams of each request.
+// of the chunk in 16-byte vectors (rows may begin anywhere: a row's positions are counted from the
+// 16-byte boundary before it) and keeps the k best so far sorted across its lanes (lane i holds
+// the i-th).  A batch none of whose values reaches the k-th best costs one comparison of its
+// maximum, which the softmax needs anyway; the first batch is filtered by the k-th largest of
+// the lanes' maxima, so few values are ever inserted.  A second, small kernel forms the scores of
+// the W * chunks * k values kept, spread over its warps, and keeps the best k of them.  Lists are
+// merged by bitonic steps across the lanes.
 //
 // lse and scores are 64-bit from the chunk sums on: the chosen indices compare scores of
 // different beams, which a 32-bit subtraction would round into ties.
@@ -63,9 +66,47 @@ struct TopList {
     thr_v = __shfl_sync(kFull, v, k - 1);
     thr_i = __shfl_sync(kFull, idx, k - 1);
   }
-  // Offer one pair per lane (`have`: the lane has one).
+  // Exchange with the lane `off` away (a power of two): the lower one of the two keeps the better
+  // pair where `down`, else the worse.
+  __device__ __forceinline__ static void step(F& v, int& i, int off, bool down, int lane) {
+    const F ov = __shfl_xor_sync(kFull, v, off);
+    const int oi = __shfl_xor_sync(kFull, i, off);
+    const bool first = ((lane & off) == 0) == down;  // this lane wants the better pair
+    if (before(ov, oi, v, i) == first) {
+      v = ov;
+      i = oi;
+    }
+  }
+  // Merge a list that is sorted over the lanes: the better of this list's i-th and that one's
+  // (31 - i)-th are the 32 best of both, and bitonic.
+  __device__ __forceinline__ void merge_sorted(F nv, int ni, int k, int lane) {
+    const F rv = __shfl_sync(kFull, nv, 31 - lane);
+    const int ri = __shfl_sync(kFull, ni, 31 - lane);
+    if (before(rv, ri, v, idx)) {
+      v = rv;
+      idx = ri;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) step(v, idx, off, true, lane);
+    thr_v = __shfl_sync(kFull, v, k - 1);
+    thr_i = __shfl_sync(kFull, idx, k - 1);
+  }
+  // Offer one pair per lane (`have`: the lane has one): inserted one by one where few can enter,
+  // else sorted and merged.
   __device__ __forceinline__ void offer(F nv, int ni, bool have, int k, int lane) {
     unsigned m = __ballot_sync(kFull, have && before(nv, ni, thr_v, thr_i));
+    if (__popc(m) > 8) {
+      if (!(m >> lane & 1)) {
+        nv = static_cast<F>(-CUDART_INF);
+        ni = INT_MAX;
+      }
+#pragma unroll
+      for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int off = size >> 1; off > 0; off >>= 1) step(nv, ni, off, (lane & size) == 0, lane);
+      merge_sorted(nv, ni, k, lane);
+      return;
+    }
     while (m) {
       const int src = __ffs(m) - 1;
       insert(__shfl_sync(kFull, nv, src), __shfl_sync(kFull, ni, src), k, lane);
@@ -74,6 +115,33 @@ struct TopList {
     }
   }
 };
+
+// The k-th largest of the lanes' values.
+__device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int off = size >> 1; off > 0; off >>= 1) {
+      const float o = __shfl_xor_sync(kFull, v, off);
+      v = ((lane & off) == 0) == ((lane & size) == 0) ? fmaxf(v, o) : fminf(v, o);
+    }
+  return __shfl_sync(kFull, v, k - 1);
+}
+
+// Join the warps' lists of a CTA in pairs; warp 0 ends with the k best.  Every thread calls it.
+template <typename F>
+__device__ __forceinline__ void join_lists(TopList<F>& top, F (*sm_v)[32], int (*sm_i)[32], int k, int warp,
+                                           int lane) {
+#pragma unroll
+  for (int half = kWarps / 2; half > 0; half >>= 1) {
+    if (warp >= half && warp < 2 * half) {
+      sm_v[warp][lane] = lane < k ? top.v : static_cast<F>(-CUDART_INF);
+      sm_i[warp][lane] = lane < k ? top.idx : INT_MAX;
+    }
+    __syncthreads();
+    if (warp < half) top.merge_sorted(sm_v[warp + half][lane], sm_i[warp + half][lane], k, lane);
+  }
+}
 
 template <typename T>
 struct Load;
@@ -114,42 +182,50 @@ struct Sum {
       m = mx;
     }
   }
-  __device__ __forceinline__ void add(float x) {
+  // what add subtracts: a lane that has seen nothing but -inf keeps the reference 0 (2^-inf = 0,
+  // NaN stays)
+  __device__ __forceinline__ float ref() const { return m == -INFINITY ? 0.f : m; }
+  __device__ __forceinline__ void add(float x, float ref) {
     // the difference first: it is exact next to the maximum, where the sum's weight lies (a
-    // product with log2 e of each term would shift the whole sum by its rounding).  A lane that
-    // has seen nothing but -inf keeps the reference 0: 2^-inf = 0, NaN stays.
-    s += ex2_approx((x - (m == -INFINITY ? 0.f : m)) * kLog2e);
+    // product with log2 e of each term would shift the whole sum by its rounding)
+    s += ex2_approx((x - ref) * kLog2e);
   }
 };
 
 // One chunk of one row per CTA: blockIdx.x = row * chunks + chunk.
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p) {
-  constexpr int N = VEC ? Load<T>::N : 1;
-  constexpr int U = VEC ? 32 / Load<T>::N / 2 : 4;  // vectors in flight per lane
+  constexpr int N = Load<T>::N;
+  constexpr int U = 32 / N / 2;  // vectors in flight per lane
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int row = blockIdx.x / p.chunks, chunk = blockIdx.x - row * p.chunks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int beg = chunk * p.chunk_len, end = min(p.V, beg + p.chunk_len);
   const T* x = static_cast<const T*>(p.logits) + static_cast<int64_t>(row) * p.row_stride;
+  // positions from the 16-byte boundary at or before the row: the row is [skip, skip + V)
+  const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
+  x -= skip;
+  const int beg = chunk * p.chunk_len;
+  const int end = static_cast<int>(min(static_cast<int64_t>(p.V) + skip, static_cast<int64_t>(beg) + p.chunk_len));
   const int k = p.k;
 
   TopList<float> top;
   top.init();
   Sum sum;
+  float filter = -INFINITY;  // no value below it is among the warp's k best
   // warps interleave: batch i of the chunk (32 * N * U values) goes to warp i % kWarps
   constexpr int BATCH = 32 * N * U;
+  bool first = true;
   for (int b0 = beg + warp * BATCH; b0 < end; b0 += kWarps * BATCH) {
     float e[U][N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int at = b0 + (u * 32 + lane) * N;
-      if (VEC && at + N <= end) {
+      if (at >= skip && at + N <= end) {
         Load<T>::vec(x + at, e[u]);
       } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j) e[u][j] = at + j < end ? Load<T>::one(x + at + j) : -INFINITY;
+        for (int j = 0; j < N; ++j) e[u][j] = at + j >= skip && at + j < end ? Load<T>::one(x + at + j) : -INFINITY;
       }
     }
     float mx = -INFINITY;
@@ -158,17 +234,22 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
 #pragma unroll
       for (int j = 0; j < N; ++j) mx = fmaxf(mx, e[u][j]);
     sum.raise(mx);
+    const float ref = sum.ref();
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < N; ++j) sum.add(e[u][j]);
-    if (__any_sync(kFull, mx >= top.thr_v)) {
+      for (int j = 0; j < N; ++j) sum.add(e[u][j], ref);
+    if (first) {
+      filter = kth_of_lanes(mx, k, lane);
+      first = false;
+    }
+    if (__any_sync(kFull, mx >= fmaxf(top.thr_v, filter))) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           const int at = b0 + (u * 32 + lane) * N + j;
-          top.offer(e[u][j], at, at < end, k, lane);
+          top.offer(e[u][j], at - skip, at >= skip && at < end && e[u][j] >= filter, k, lane);
         }
     }
   }
@@ -189,9 +270,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
     sm_m[warp] = m;
     sm_s[warp] = s;
   }
-  sm_v[warp][lane] = top.v;
-  sm_i[warp][lane] = top.idx;
-  __syncthreads();
+  join_lists(top, sm_v, sm_i, k, warp, lane);  // (its barriers order the sums as well)
   if (warp != 0) return;
   float M = -INFINITY;
   for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w]);
@@ -199,8 +278,6 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   for (int w = 0; w < kWarps; ++w)
     S += sm_m[w] == -INFINITY ? sm_s[w]
                               : sm_s[w] * exp2(static_cast<double>(sm_m[w] - M) * 1.4426950408889634);
-  for (int w = 1; w < kWarps; ++w)
-    top.offer(sm_v[w][lane], sm_i[w][lane], lane < k && sm_i[w][lane] != INT_MAX, k, lane);
   const int64_t at = static_cast<int64_t>(blockIdx.x);
   if (lane == 0) {
     p.ws_max[at] = M;
@@ -212,23 +289,30 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   }
 }
 
-// One request per CTA.  Warp w joins the chunks of beams w, w + kWarps, ... and merges them
-// into its list by score; warp 0 joins the warps' lists.
+// One request per CTA.  First the beams' log-sum-exp (a warp each, kept in shared memory for up to
+// kBeams at a time), then all the values kept of these beams, 32 at a time and warp.
+constexpr int kBeams = 64;
+
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int k = p.k;
+  __shared__ double sm_v[kWarps][32];
+  __shared__ int sm_i[kWarps][32];
+  __shared__ double lse_sh[kBeams];  // NaN: the beam has no ordinary candidate
+  __shared__ float cum_sh[kBeams];
   TopList<double> best;
   best.init();
-  for (int w = warp; w < p.W; w += kWarps) {
-    const int row = n * p.W + w;
-    const int64_t c0 = static_cast<int64_t>(row) * p.chunks;
-    const float cum = __ldg(p.cum + row);
-    const bool done = p.finished && __ldg(p.finished + row) != 0;
-    const int base = w * p.V;
-    if (!done) {
+  for (int w0 = 0; w0 < p.W; w0 += kBeams) {
+    const int beams = min(kBeams, p.W - w0);
+    __syncthreads();  // (the round before has read them)
+    for (int w = warp; w < beams; w += kWarps) {
+      const int row = n * p.W + w0 + w;
+      const int64_t c0 = static_cast<int64_t>(row) * p.chunks;
+      const float cum = __ldg(p.cum + row);
+      const bool done = p.finished && __ldg(p.finished + row) != 0;
       float m = -INFINITY;
       for (int c = lane; c < p.chunks; c += 32) m = fmaxf(m, p.ws_max[c0 + c]);
 #pragma unroll
@@ -242,39 +326,45 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p)
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
       const double lse = static_cast<double>(m) + log(s);
-      if (isfinite(lse) && isfinite(cum)) {
-        TopList<float> top;
-        top.init();
-        for (int c = 0; c < p.chunks; ++c) {
-          const bool in = lane < k;
-          const float v = in ? p.ws_val[(c0 + c) * k + lane] : -INFINITY;
-          const int i = in ? p.ws_idx[(c0 + c) * k + lane] : INT_MAX;
-          top.offer(v, i, in && i != INT_MAX, k, lane);
-        }
-        best.offer(static_cast<double>(cum) + (static_cast<double>(top.v) - lse), base + top.idx,
-                   lane < k && top.idx != INT_MAX, k, lane);
-        continue;
+      const bool ordinary = !done && isfinite(lse) && isfinite(cum);
+      if (lane == 0) {
+        lse_sh[w] = ordinary ? lse : CUDART_NAN;
+        cum_sh[w] = cum;
       }
+      if (ordinary) continue;
+      // a beam without an ordinary candidate: finished (its score stays, at the end token), dead
+      // (score -inf) or with a sum that is not finite.  All its other candidates score -inf and
+      // rank by index.
+      const int base = (w0 + w) * p.V;
+      if (done && isfinite(cum)) best.offer(static_cast<double>(cum), base + p.eos, lane == 0, k, lane);
+      const bool skip = done && isfinite(cum) && lane == p.eos;
+      // k + 1 of them: one may be the end token, ranked above already
+      best.offer(-CUDART_INF, base + lane, lane < p.V && !skip, k, lane);
+      if (done && k == 32) best.offer(-CUDART_INF, base + 32, lane == 0 && 32 < p.V && p.eos != 32, k, lane);
     }
-    // a beam without an ordinary candidate: finished (its score stays, at the end token), dead
-    // (score -inf) or with a sum that is not finite.  All its other candidates score -inf and
-    // rank by index.
-    if (done && isfinite(cum))
-      best.offer(static_cast<double>(cum), base + p.eos, lane == 0 && p.eos >= 0 && p.eos < p.V, k, lane);
-    const bool skip = done && isfinite(cum) && lane == p.eos;
-    // k + 1 of them: one may be the end token, ranked above already
-    best.offer(-CUDART_INF, base + lane, lane < p.V && !skip, k, lane);
-    if (done && k == 32) best.offer(-CUDART_INF, base + 32, lane == 0 && 32 < p.V && p.eos != 32, k, lane);
+    __syncthreads();
+    const int per = p.chunks * k, total = beams * per;  // (W * V < 2^31 bounds it)
+    const int64_t first = (static_cast<int64_t>(n) * p.W + w0) * per;
+    for (int e0 = warp * 32; e0 < total; e0 += kThreads) {
+      const int e = e0 + lane;
+      bool have = e < total;
+      double score = 0.0;
+      int at = INT_MAX;
+      if (have) {
+        const int w = e / per, i = p.ws_idx[first + e];
+        const double lse = lse_sh[w];
+        have = i != INT_MAX && lse == lse;
+        if (have) {
+          at = (w0 + w) * p.V + i;
+          score = static_cast<double>(cum_sh[w]) + (static_cast<double>(p.ws_val[first + e]) - lse);
+        }
+      }
+      best.offer(score, at, have, k, lane);
+    }
   }
-  __shared__ double sm_v[kWarps][32];
-  __shared__ int sm_i[kWarps][32];
-  sm_v[warp][lane] = best.v;
-  sm_i[warp][lane] = best.idx;
   __syncthreads();
-  if (warp != 0) return;
-  for (int w = 1; w < min(kWarps, p.W); ++w)
-    best.offer(sm_v[w][lane], sm_i[w][lane], lane < k && sm_i[w][lane] != INT_MAX, k, lane);
-  if (lane < k) {
+  join_lists(best, sm_v, sm_i, k, warp, lane);
+  if (warp == 0 && lane < k) {
     const int64_t at = static_cast<int64_t>(n) * k + lane;
     p.scores[at] = static_cast<float>(best.v);
     p.parents[at] = best.idx / p.V;
@@ -303,10 +393,8 @@ __global__ void __launch_bounds__(kThreads) beam_gather_kernel(V* __restrict__ d
 
 template <typename T>
 cudaError_t launch_rows(const BeamParams& p, cudaStream_t stream) {
-  const bool vec = p.row_stride % Load<T>::N == 0 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0;
   const dim3 grid(static_cast<unsigned>(p.N * p.W * p.chunks));
-  return vec ? launch_pdl(beam_rows_kernel<T, true>, grid, kThreads, 0, stream, p)
-             : launch_pdl(beam_rows_kernel<T, false>, grid, kThreads, 0, stream, p);
+  return launch_pdl(beam_rows_kernel<T>, grid, kThreads, 0, stream, p);
 }
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -314,15 +402,16 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 // Chunks per row: enough CTAs for four per SM, none below 2048 values (a shorter chunk is
-// all reduction); a multiple of 8 values, so that chunks start on vector boundaries.
+// all reduction); a multiple of 8 values, so that chunks start on vector boundaries.  A row's
+// positions begin up to 7 before it.
 void beam_plan(BeamParams* p) {
-  const int64_t rows = static_cast<int64_t>(p->N) * p->W;
+  const int64_t rows = static_cast<int64_t>(p->N) * p->W, V = static_cast<int64_t>(p->V) + 7;
   const int64_t want = (148 * 4 + rows - 1) / (rows > 0 ? rows : 1);
-  int64_t len = (p->V + want - 1) / want;
+  int64_t len = (V + want - 1) / want;
   if (len < 2048) len = 2048;
   len = (len + 7) / 8 * 8;
-  p->chunk_len = static_cast<int>(len < p->V ? len : (p->V + 7) / 8 * 8);
-  p->chunks = (p->V + p->chunk_len - 1) / p->chunk_len;
+  p->chunk_len = static_cast<int>(len < V ? len : (V + 7) / 8 * 8);
+  p->chunks = static_cast<int>((V + p->chunk_len - 1) / p->chunk_len);
 }
 
 size_t beam_workspace_bytes(const BeamParams& p) {
