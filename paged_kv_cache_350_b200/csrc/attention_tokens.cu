@@ -25,7 +25,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4, kThreads = kWarps * 32, kStages = 2;  // per CTA; ring stages per warp
-constexpr int kMinTiles = 4;
+constexpr int kMinTiles = 2;
 
 template <int D_, int BS_, bool ROWS16_>
 struct TokensCfg : TileCfg<D_, BS_, ROWS16_, 16, true> {

@@ -116,6 +116,15 @@ struct TopList {
   }
 };
 
+// Floats as integers of the same order (-0 below 0), and back.
+__device__ __forceinline__ int ordered(float v) {
+  const int i = __float_as_int(v);
+  return i < 0 ? i ^ 0x7fffffff : i;
+}
+__device__ __forceinline__ float unordered(int i) {
+  return i == INT_MIN ? -INFINITY : __int_as_float(i < 0 ? i ^ 0x7fffffff : i);
+}
+
 // The k-th largest of the lanes' values.
 __device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
 #pragma unroll
@@ -209,15 +218,26 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   const int end = static_cast<int>(min(static_cast<int64_t>(p.V) + skip, static_cast<int64_t>(beg) + p.chunk_len));
   const int k = p.k;
 
+  // No value below `filter` is among the CTA's k best: the k-th largest of the lanes' maxima of a
+  // warp's first batch, then the best of the warps' k-th values (shared as ordered integers).
+  __shared__ int shared_filter;
+  if (threadIdx.x == 0) shared_filter = INT_MIN;
+  __syncthreads();
+  float filter = -INFINITY;
+  auto raise_filter = [&](float v) {
+    if (v > filter) {
+      filter = v;
+      if (lane == 0) atomicMax(&shared_filter, ordered(v));
+    }
+  };
+
   TopList<float> top;
   top.init();
   Sum sum;
-  float filter = -INFINITY;  // no value below it is among the warp's k best
-  // warps interleave: batch i of the chunk (32 * N * U values) goes to warp i % kWarps
+  // warps interleave: batch i of the chunk (32 * N * U values) goes to warp i % kWarps; a batch is
+  // loaded while the one before it is worked on
   constexpr int BATCH = 32 * N * U;
-  bool first = true;
-  for (int b0 = beg + warp * BATCH; b0 < end; b0 += kWarps * BATCH) {
-    float e[U][N];
+  auto load = [&](int b0, float (&e)[U][N]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int at = b0 + (u * 32 + lane) * N;
@@ -228,6 +248,17 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
         for (int j = 0; j < N; ++j) e[u][j] = at + j >= skip && at + j < end ? Load<T>::one(x + at + j) : -INFINITY;
       }
     }
+  };
+  float nx[U][N];
+  int b0 = beg + warp * BATCH;
+  if (b0 < end) load(b0, nx);
+  for (bool first = true; b0 < end; b0 += kWarps * BATCH, first = false) {
+    float e[U][N];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < N; ++j) e[u][j] = nx[u][j];
+    if (b0 + kWarps * BATCH < end) load(b0 + kWarps * BATCH, nx);
     float mx = -INFINITY;
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -239,11 +270,9 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < N; ++j) sum.add(e[u][j], ref);
-    if (first) {
-      filter = kth_of_lanes(mx, k, lane);
-      first = false;
-    }
-    if (__any_sync(kFull, mx >= fmaxf(top.thr_v, filter))) {
+    if (first) raise_filter(kth_of_lanes(mx, k, lane));
+    filter = fmaxf(filter, unordered(*const_cast<volatile int*>(&shared_filter)));
+    if (__any_sync(kFull, mx >= filter && mx >= top.thr_v)) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -251,6 +280,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
           const int at = b0 + (u * 32 + lane) * N + j;
           top.offer(e[u][j], at - skip, at >= skip && at < end && e[u][j] >= filter, k, lane);
         }
+      raise_filter(top.thr_v);
     }
   }
 
@@ -401,12 +431,13 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// Chunks per row: enough CTAs for four per SM, none below 2048 values (a shorter chunk is
-// all reduction); a multiple of 8 values, so that chunks start on vector boundaries.  A row's
+// Chunks per row: as many as keep the CTAs within four per SM, which all run at once (five fit; the
+// 28 CTAs past one wave of 740 doubled the time of 256 rows of 131072), none below 2048 values (a
+// shorter chunk is all reduction); a multiple of 8 values, so that chunks start on vector boundaries.  A row's
 // positions begin up to 7 before it.
 void beam_plan(BeamParams* p) {
   const int64_t rows = static_cast<int64_t>(p->N) * p->W, V = static_cast<int64_t>(p->V) + 7;
-  const int64_t want = (148 * 4 + rows - 1) / (rows > 0 ? rows : 1);
+  const int64_t fit = 148 * 4 / (rows > 0 ? rows : 1), want = fit > 0 ? fit : 1;
   int64_t len = (V + want - 1) / want;
   if (len < 2048) len = 2048;
   len = (len + 7) / 8 * 8;
