@@ -203,7 +203,7 @@ struct Sum {
 
 // One chunk of one row per CTA: blockIdx.x = row * chunks + chunk.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams p) {
   constexpr int N = Load<T>::N;
   constexpr int U = 32 / N / 2;  // vectors in flight per lane
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -236,52 +236,67 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const BeamParams p)
   Sum sum;
   // warps interleave: batch i of the chunk (32 * N * U values) goes to warp i % kWarps; a batch is
   // loaded while the one before it is worked on
-  constexpr int BATCH = 32 * N * U;
-  auto load = [&](int b0, float (&e)[U][N]) {
+  constexpr int BATCH = 32 * N * U, STEP = kWarps * BATCH;
+  auto load = [&](int b0, float (&e)[U * N]) {
+    if (b0 >= skip && b0 + BATCH <= end) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) Load<T>::vec(x + b0 + (u * 32 + lane) * N, e + u * N);
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int at = b0 + (u * 32 + lane) * N;
-      if (at >= skip && at + N <= end) {
-        Load<T>::vec(x + at, e[u]);
-      } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j) e[u][j] = at + j >= skip && at + j < end ? Load<T>::one(x + at + j) : -INFINITY;
-      }
+      for (int j = 0; j < N; ++j)
+        e[u * N + j] = at + j >= skip && at + j < end ? Load<T>::one(x + at + j) : -INFINITY;
     }
   };
-  float nx[U][N];
-  int b0 = beg + warp * BATCH;
-  if (b0 < end) load(b0, nx);
-  for (bool first = true; b0 < end; b0 += kWarps * BATCH, first = false) {
-    float e[U][N];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < N; ++j) e[u][j] = nx[u][j];
-    if (b0 + kWarps * BATCH < end) load(b0 + kWarps * BATCH, nx);
+  __shared__ float2 cand_sh[kWarps][BATCH];
+  float2* cand = cand_sh[warp];
+  bool first = true;
+  auto work = [&](int b0, const float (&e)[U * N]) {
     float mx = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < N; ++j) mx = fmaxf(mx, e[u][j]);
+    for (int j = 0; j < U * N; ++j) mx = fmaxf(mx, e[j]);
     sum.raise(mx);
     const float ref = sum.ref();
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < N; ++j) sum.add(e[u][j], ref);
+    for (int j = 0; j < U * N; ++j) sum.add(e[j], ref);
     if (first) raise_filter(kth_of_lanes(mx, k, lane));
+    first = false;
     filter = fmaxf(filter, unordered(*const_cast<volatile int*>(&shared_filter)));
-    if (__any_sync(kFull, mx >= filter && mx >= top.thr_v)) {
+    const float least = fmaxf(filter, top.thr_v);
+    if (!__any_sync(kFull, mx >= least)) return;
+    // the candidates side by side in shared memory, then 32 at a time
+    int n = 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int at = b0 + (u * 32 + lane) * N + j;
-          top.offer(e[u][j], at - skip, at >= skip && at < end && e[u][j] >= filter, k, lane);
-        }
-      raise_filter(top.thr_v);
+    for (int j = 0; j < U * N; ++j) {
+      const bool in = e[j] >= least;
+      const unsigned m = __ballot_sync(kFull, in);
+      if (m) {
+        if (in)
+          cand[n + __popc(m & ((1u << lane) - 1))] = make_float2(e[j], __int_as_float(b0 + (j / N * 32 + lane) * N + j % N));
+        n += __popc(m);
+      }
     }
+    __syncwarp();
+    for (int c = lane; c - lane < n; c += 32) {
+      const float2 o = cand[min(c, n - 1)];
+      const int at = __float_as_int(o.y);
+      top.offer(o.x, at - skip, c < n && at >= skip && at < end, k, lane);
+    }
+    __syncwarp();
+    raise_filter(top.thr_v);
+  };
+  float ea[U * N], eb[U * N];
+  int b0 = beg + warp * BATCH;
+  if (b0 < end) load(b0, ea);
+  for (; b0 < end; b0 += 2 * STEP) {
+    if (b0 + STEP < end) load(b0 + STEP, eb);
+    work(b0, ea);
+    if (b0 + STEP >= end) break;
+    if (b0 + 2 * STEP < end) load(b0 + 2 * STEP, ea);
+    work(b0 + STEP, eb);
   }
 
   // join the lanes' sums, then the warps'
@@ -431,8 +446,8 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// Chunks per row: as many as keep the CTAs within four per SM, which all run at once (five fit; the
-// 28 CTAs past one wave of 740 doubled the time of 256 rows of 131072), none below 2048 values (a
+// Chunks per row: as many as keep the CTAs within four per SM, which all run at once (the few CTAs
+// past one wave doubled the time of 256 rows of 131072), none below 2048 values (a
 // shorter chunk is all reduction); a multiple of 8 values, so that chunks start on vector boundaries.  A row's
 // positions begin up to 7 before it.
 void beam_plan(BeamParams* p) {
