@@ -152,25 +152,29 @@ __device__ __forceinline__ void join_lists(TopList<F>& top, F (*sm_v)[32], int (
   }
 }
 
+// 16 bytes of logits, kept as loaded until they are used.
 template <typename T>
 struct Load;
 template <>
 struct Load<float> {
   static constexpr int N = 4;
-  __device__ static void vec(const float* p, float* x) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    x[0] = a.x;
-    x[1] = a.y;
-    x[2] = a.z;
-    x[3] = a.w;
+  static constexpr uint32_t kNone = 0xff800000u;  // -inf
+  __device__ static void unpack(const uint4& u, float* x) {
+    x[0] = __uint_as_float(u.x);
+    x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z);
+    x[3] = __uint_as_float(u.w);
   }
-  __device__ static float one(const float* p) { return __ldcs(p); }
+  // word w of a vector of which elements [from, to) are loaded, the others -inf
+  __device__ static uint32_t word(const float* p, int w, int from, int to) {
+    return w >= from && w < to ? __float_as_uint(p[w]) : kNone;
+  }
 };
 template <>
 struct Load<__nv_bfloat16> {
   static constexpr int N = 8;
-  __device__ static void vec(const __nv_bfloat16* p, float* x) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+  static constexpr uint32_t kNone = 0xff80u;  // -inf
+  __device__ static void unpack(const uint4& u, float* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -178,7 +182,12 @@ struct Load<__nv_bfloat16> {
       x[2 * i + 1] = bf16_hi(w[i]);
     }
   }
-  __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  __device__ static uint32_t word(const __nv_bfloat16* p, int w, int from, int to) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+    const uint32_t lo = 2 * w >= from && 2 * w < to ? q[2 * w] : kNone;
+    const uint32_t hi = 2 * w + 1 >= from && 2 * w + 1 < to ? q[2 * w + 1] : kNone;
+    return lo | hi << 16;
+  }
 };
 
 // Running (max, sum of 2^((x - max) log2 e)) of one lane.  NaN and +inf in a row end in a
@@ -237,24 +246,32 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
   // warps interleave: batch i of the chunk (32 * N * U values) goes to warp i % kWarps; a batch is
   // loaded while the one before it is worked on
   constexpr int BATCH = 32 * N * U, STEP = kWarps * BATCH;
-  auto load = [&](int b0, float (&e)[U * N]) {
+  auto load = [&](int b0, uint4 (&raw)[U]) {
     if (b0 >= skip && b0 + BATCH <= end) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) Load<T>::vec(x + b0 + (u * 32 + lane) * N, e + u * N);
+      for (int u = 0; u < U; ++u) raw[u] = __ldcs(reinterpret_cast<const uint4*>(x + b0 + (u * 32 + lane) * N));
       return;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int at = b0 + (u * 32 + lane) * N;
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        e[u * N + j] = at + j >= skip && at + j < end ? Load<T>::one(x + at + j) : -INFINITY;
+      const T* q = x + at;
+      if (at >= skip && at + N <= end) {
+        raw[u] = __ldcs(reinterpret_cast<const uint4*>(q));
+      } else {
+        const int from = skip - at, to = end - at;
+        raw[u] = make_uint4(Load<T>::word(q, 0, from, to), Load<T>::word(q, 1, from, to),
+                            Load<T>::word(q, 2, from, to), Load<T>::word(q, 3, from, to));
+      }
     }
   };
   __shared__ float2 cand_sh[kWarps][BATCH];
   float2* cand = cand_sh[warp];
   bool first = true;
-  auto work = [&](int b0, const float (&e)[U * N]) {
+  auto work = [&](int b0, const uint4 (&raw)[U]) {
+    float e[U * N];
+#pragma unroll
+    for (int u = 0; u < U; ++u) Load<T>::unpack(raw[u], e + u * N);
     float mx = -INFINITY;
 #pragma unroll
     for (int j = 0; j < U * N; ++j) mx = fmaxf(mx, e[j]);
@@ -288,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const BeamParams
     __syncwarp();
     raise_filter(top.thr_v);
   };
-  float ea[U * N], eb[U * N];
+  uint4 ea[U], eb[U];
   int b0 = beg + warp * BATCH;
   if (b0 < end) load(b0, ea);
   for (; b0 < end; b0 += 2 * STEP) {
@@ -348,6 +365,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p)
   __shared__ int sm_i[kWarps][32];
   __shared__ double lse_sh[kBeams];  // NaN: the beam has no ordinary candidate
   __shared__ float cum_sh[kBeams];
+  __shared__ float kth_sh[kWarps];
   TopList<double> best;
   best.init();
   for (int w0 = 0; w0 < p.W; w0 += kBeams) {
@@ -390,20 +408,33 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p)
     __syncthreads();
     const int per = p.chunks * k, total = beams * per;  // (W * V < 2^31 bounds it)
     const int64_t first = (static_cast<int64_t>(n) * p.W + w0) * per;
+    auto candidate = [&](int e, double& score, int& at) {
+      if (e >= total) return false;
+      const int w = e / per, i = p.ws_idx[first + e];
+      const double lse = lse_sh[w];
+      if (i == INT_MAX || lse != lse) return false;
+      at = (w0 + w) * p.V + i;
+      score = static_cast<double>(cum_sh[w]) + (static_cast<double>(p.ws_val[first + e]) - lse);
+      return true;
+    };
+    // as above, no score below the k-th largest of a warp's lanes' maxima is among the k best
+    // (rounded down, so that it is a bound)
+    double score = 0.0;
+    int at = INT_MAX;
+    float mx = -INFINITY;
+    for (int e0 = warp * 32; e0 < total; e0 += kThreads)
+      if (candidate(e0 + lane, score, at)) mx = fmaxf(mx, __double2float_rd(score));
+    if (lane == 0) kth_sh[warp] = -INFINITY;
+    if (warp * 32 < total) {
+      const float kth = kth_of_lanes(mx, k, lane);
+      if (lane == 0) kth_sh[warp] = kth;
+    }
+    __syncthreads();
+    float filter = kth_sh[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) filter = fmaxf(filter, kth_sh[i]);
     for (int e0 = warp * 32; e0 < total; e0 += kThreads) {
-      const int e = e0 + lane;
-      bool have = e < total;
-      double score = 0.0;
-      int at = INT_MAX;
-      if (have) {
-        const int w = e / per, i = p.ws_idx[first + e];
-        const double lse = lse_sh[w];
-        have = i != INT_MAX && lse == lse;
-        if (have) {
-          at = (w0 + w) * p.V + i;
-          score = static_cast<double>(cum_sh[w]) + (static_cast<double>(p.ws_val[first + e]) - lse);
-        }
-      }
+      const bool have = candidate(e0 + lane, score, at) && score >= filter;
       best.offer(score, at, have, k, lane);
     }
   }
@@ -447,14 +478,14 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 // Chunks per row: as many as keep the CTAs within four per SM, which all run at once (the few CTAs
-// past one wave doubled the time of 256 rows of 131072), none below 2048 values (a
-// shorter chunk is all reduction); a multiple of 8 values, so that chunks start on vector boundaries.  A row's
+// past one wave doubled the time of 256 rows of 131072), none below 4096 values, a
+// batch for each warp (a shorter chunk is all reduction); a multiple of 8 values, so that chunks start on vector boundaries.  A row's
 // positions begin up to 7 before it.
 void beam_plan(BeamParams* p) {
   const int64_t rows = static_cast<int64_t>(p->N) * p->W, V = static_cast<int64_t>(p->V) + 7;
   const int64_t fit = 148 * 4 / (rows > 0 ? rows : 1), want = fit > 0 ? fit : 1;
   int64_t len = (V + want - 1) / want;
-  if (len < 2048) len = 2048;
+  if (len < 4096) len = 4096;
   len = (len + 7) / 8 * 8;
   p->chunk_len = static_cast<int>(len < V ? len : (V + 7) / 8 * 8);
   p->chunks = static_cast<int>((V + p->chunk_len - 1) / p->chunk_len);
