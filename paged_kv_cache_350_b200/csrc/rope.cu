@@ -13,10 +13,15 @@
 // from there.  One CTA serves one token, so a token's R/2 sines and cosines are computed once
 // for all its Hq + Hkv heads.
 //
-// Bound by memory: q, k and v are read once and written once, in 16-byte vectors.  Each
-// thread issues the loads of its first pairs before the angles are computed, so that the two
-// latencies overlap.  Where a layout's pairs do not fall into whole 16-byte vectors, or a
-// stride is not a multiple of 16 bytes, a scalar variant runs.
+// Bound by memory: q, k and v are read once and written once, in 16-byte vectors.  A thread keeps
+// its place within a head and walks over the heads, so that its sines and cosines stay in
+// registers and no index is divided (where every vector's place was computed for itself the
+// instructions took as long as the memory).  The loads of its first kAhead heads come before
+// anything else: the latencies of the data, of the token's position and slot, and of the angles
+// overlap.  Three forms by where a pair lies: in two vectors R / 2 apart (half layout, R / 2 a
+// whole number of vectors), within one vector (interleaved), or anywhere (half layout otherwise:
+// the token's rows pass through shared memory).  Where a stride is not a multiple of 16 bytes a
+// scalar form runs.
 
 #include <cuda_bf16.h>
 
@@ -27,7 +32,7 @@ namespace pa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 template <typename T>
 struct Vec;  // 16 bytes of T
@@ -86,112 +91,119 @@ __device__ __forceinline__ void angles(const RopeParams& p, int pos, float2* cs)
   }
 }
 
-// A token's work in units of 16-byte vectors.  Rotated heads (q, then k): in the half layout a
-// unit is the vector pair (u, u + R/2/N); in the interleaved one a single vector; past R
-// a unit is a plain copy of one vector.  Then v's vectors.
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const RopeParams p) {
+enum Form { kHalf, kInterleaved, kStaged };
+
+// 1 << shift threads share a head of q, k or v (its place: w); in the kHalf form place w < R/2/N
+// takes the vectors at wN and wN + R/2, and the next ones the vectors from R on.
+template <typename T, Form FORM>
+__global__ void __launch_bounds__(kThreads, 8) rope_vec_kernel(const RopeParams p, int shift) {
   constexpr int N = Vec<T>::N;
+  constexpr bool HALF = FORM == kHalf;
+  constexpr int kAhead = HALF ? 3 : 6;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   extern __shared__ float2 cs[];
+  T* staged = reinterpret_cast<T*>(cs + (p.R / 2 + 1) / 2 * 2);  // kStaged: [Hq + Hkv][D]
   const int64_t t = blockIdx.x;
-  const int D = p.D, R = p.R;
-  const int rot = HALF ? R / 2 / N : R / N;  // rotating units of a head
-  const int uph = rot + (D - R) / N;         // units of a rotated head
-  const int units = (p.Hq + p.Hkv) * uph;
-  const int total = units + p.Hkv * (D / N);
+  const int D = p.D, R = p.R, half = R / 2;
+  const int w = threadIdx.x & ((1 << shift) - 1), step = kThreads >> shift;
+  const bool pair = HALF && w * N < half;  // two vectors
+  const int lead = !HALF || pair ? w * N : R + w * N - half;
+  const bool turns = HALF ? pair : lead < R;  // of a head of q or k
+  const int rotated = p.Hq + p.Hkv;
+  const int heads = lead < D ? rotated + p.Hkv : 0;  // (places past the head are idle)
+  const T* q = static_cast<const T*>(p.q) + t * p.q_stride + lead;
+  const T* k = static_cast<const T*>(p.k) + t * p.k_stride + lead;
+  const T* v = static_cast<const T*>(p.v) + t * p.v_stride + lead;
+  auto load = [&](int h, uint4& a, uint4& b) {
+    const T* src = h < p.Hq ? q + h * D : h < rotated ? k + (h - p.Hq) * D : v + (h - rotated) * D;
+    a = *reinterpret_cast<const uint4*>(src);
+    if (pair) b = *reinterpret_cast<const uint4*>(src + half);
+  };
+
+  const int h0 = threadIdx.x >> shift;
+  uint4 a[kAhead], b[kAhead];
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s)
+    if (h0 + s * step < heads) load(h0 + s * step, a[s], b[s]);
   const int64_t slot = __ldg(p.slots + t);
+  angles(p, __ldg(p.positions + t), cs);
   const bool bad = slot >= p.num_slots;
   if (bad && threadIdx.x == 0) flag_error(p.err, PA_DEVERR_BAD_SLOT);
   const bool write = slot >= 0 && !bad;
-  const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
-  const T* k = static_cast<const T*>(p.k) + t * p.k_stride;
-  const T* v = static_cast<const T*>(p.v) + t * p.v_stride;
-  T* qo = static_cast<T*>(p.q_out) + t * p.Hq * D;
-  T* kp = static_cast<T*>(p.k_pool) + (write ? slot : 0) * p.Hkv * D;
-  T* vp = static_cast<T*>(p.v_pool) + (write ? slot : 0) * p.Hkv * D;
-
-  struct Unit {
-    const T* src;
-    T* dst;
-    int lead;  // first element within the head
-    bool rotates;
-  };
-  auto unit = [&](int i) -> Unit {
-    Unit u;
-    if (i < units) {
-      const int h = i / uph, w = i - h * uph;
-      u.rotates = w < rot;
-      u.lead = u.rotates ? w * N : R + (w - rot) * N;
-      if (h < p.Hq) {
-        u.src = q + h * D + u.lead;
-        u.dst = qo + h * D + u.lead;
-      } else {
-        u.src = write ? k + (h - p.Hq) * D + u.lead : nullptr;
-        u.dst = kp + (h - p.Hq) * D + u.lead;
-      }
-    } else {
-      const int w = i - units;
-      u.rotates = false;
-      u.lead = 0;
-      u.src = write ? v + w * N : nullptr;
-      u.dst = vp + w * N;
+  T* qo = static_cast<T*>(p.q_out) + t * p.Hq * D + lead;
+  T* kp = static_cast<T*>(p.k_pool) + (write ? slot : 0) * p.Hkv * D + lead;
+  T* vp = static_cast<T*>(p.v_pool) + (write ? slot : 0) * p.Hkv * D + lead;
+  if (FORM == kStaged) {
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+      if (h0 + s * step < min(heads, rotated))
+        *reinterpret_cast<uint4*>(staged + (h0 + s * step) * D + lead) = a[s];
+    for (int h = h0 + kAhead * step; h < min(heads, rotated); h += step) {
+      uint4 x, none;
+      load(h, x, none);
+      *reinterpret_cast<uint4*>(staged + h * D + lead) = x;
     }
-    return u;
-  };
-  auto load = [&](const Unit& u, uint4& a, uint4& b) {
-    if (!u.src) return;
-    a = *reinterpret_cast<const uint4*>(u.src);
-    if (HALF && u.rotates) b = *reinterpret_cast<const uint4*>(u.src + R / 2);
-  };
-  auto store = [&](const Unit& u, const uint4& a, const uint4& b) {
-    if (!u.src) return;
-    if (!u.rotates) {
-      *reinterpret_cast<uint4*>(u.dst) = a;
+  }
+  __syncthreads();
+  float2 c[N];  // of this place's elements (pairs)
+  if (turns) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int e = lead + j;
+      if (HALF) c[j] = cs[e];
+      if (FORM == kInterleaved && j % 2 == 0) c[j] = e < R ? cs[e / 2] : make_float2(1.f, 0.f);
+      if (FORM == kStaged) c[j] = e < half ? cs[e] : e < R ? cs[e - half] : make_float2(1.f, 0.f);
+    }
+  }
+  auto store = [&](int h, const uint4& a0, const uint4& b0) {
+    if (h >= p.Hq && !write) return;
+    T* dst = h < p.Hq ? qo + h * D : h < rotated ? kp + (h - p.Hq) * D : vp + (h - rotated) * D;
+    if (!turns || h >= rotated) {
+      *reinterpret_cast<uint4*>(dst) = a0;
+      if (pair) *reinterpret_cast<uint4*>(dst + half) = b0;
       return;
     }
+    float x[N];
+    Vec<T>::unpack(a0, x);
     if (HALF) {
-      float x[N], y[N];
-      Vec<T>::unpack(a, x);
-      Vec<T>::unpack(b, y);
+      float y[N];
+      Vec<T>::unpack(b0, y);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float2 c = cs[u.lead + j];
-        const float xr = x[j] * c.x - y[j] * c.y;
-        y[j] = x[j] * c.y + y[j] * c.x;
+        const float xr = x[j] * c[j].x - y[j] * c[j].y;
+        y[j] = x[j] * c[j].y + y[j] * c[j].x;
         x[j] = xr;
       }
-      *reinterpret_cast<uint4*>(u.dst) = Vec<T>::pack(x);
-      *reinterpret_cast<uint4*>(u.dst + R / 2) = Vec<T>::pack(y);
-    } else {
-      float x[N];
-      Vec<T>::unpack(a, x);
+      *reinterpret_cast<uint4*>(dst + half) = Vec<T>::pack(y);
+    } else if (FORM == kInterleaved) {
 #pragma unroll
       for (int j = 0; j < N; j += 2) {
-        const float2 c = cs[(u.lead + j) / 2];
-        const float xr = x[j] * c.x - x[j + 1] * c.y;
-        x[j + 1] = x[j] * c.y + x[j + 1] * c.x;
+        if (lead + j >= R) break;  // (what is not rotated stays as it is: exact both ways)
+        const float xr = x[j] * c[j].x - x[j + 1] * c[j].y;
+        x[j + 1] = x[j] * c[j].y + x[j + 1] * c[j].x;
         x[j] = xr;
       }
-      *reinterpret_cast<uint4*>(u.dst) = Vec<T>::pack(x);
+    } else {
+      const T* row = staged + h * D;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int e = lead + j;
+        if (e >= R) break;
+        const bool second = e >= half;
+        const float other = as_f(row[second ? e - half : e + half]);
+        x[j] = second ? other * c[j].y + x[j] * c[j].x : x[j] * c[j].x - other * c[j].y;
+      }
     }
+    *reinterpret_cast<uint4*>(dst) = Vec<T>::pack(x);
   };
-
-  Unit u0{}, u1{};
-  uint4 a0{}, b0{}, a1{}, b1{};
-  const int i0 = threadIdx.x, i1 = threadIdx.x + kThreads;
-  if (i0 < total) load(u0 = unit(i0), a0, b0);
-  if (i1 < total) load(u1 = unit(i1), a1, b1);
-  angles(p, __ldg(p.positions + t), cs);
-  __syncthreads();
-  if (i0 < total) store(u0, a0, b0);
-  if (i1 < total) store(u1, a1, b1);
-  for (int i = i1 + kThreads; i < total; i += kThreads) {
-    const Unit u = unit(i);
-    uint4 a{}, b{};
-    load(u, a, b);
-    store(u, a, b);
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s)
+    if (h0 + s * step < heads) store(h0 + s * step, a[s], b[s]);
+  for (int h = h0 + kAhead * step; h < heads; h += step) {
+    uint4 x, y;
+    load(h, x, y);
+    store(h, x, y);
   }
 }
 
@@ -240,15 +252,21 @@ template <typename T>
 cudaError_t launch_t(const RopeParams& p, cudaStream_t stream) {
   constexpr int N = Vec<T>::N;
   auto mult = [](int64_t a) { return a % N == 0; };
-  const bool vec = (p.half ? mult(p.R / 2) : mult(p.R)) && mult(p.R) && mult(p.q_stride) &&
-                   mult(p.k_stride) && mult(p.v_stride) &&
+  const bool vec = mult(p.q_stride) && mult(p.k_stride) && mult(p.v_stride) &&
                    (reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) |
                     reinterpret_cast<uintptr_t>(p.v)) % 16 == 0;
   const dim3 grid(static_cast<unsigned>(p.T));
-  const size_t smem = static_cast<size_t>(p.R / 2) * sizeof(float2);
-  if (!vec) return launch_pdl(rope_scalar_kernel<T>, grid, kThreads, smem, stream, p);
-  return p.half ? launch_pdl(rope_vec_kernel<T, true>, grid, kThreads, smem, stream, p)
-                : launch_pdl(rope_vec_kernel<T, false>, grid, kThreads, smem, stream, p);
+  const size_t smem = static_cast<size_t>((p.R / 2 + 1) / 2 * 2) * sizeof(float2);
+  const size_t rows = static_cast<size_t>(p.Hq + p.Hkv) * p.D * sizeof(T);
+  int shift = 0;  // threads of a head: a power of two, at least its places
+  const int places = p.half && mult(p.R / 2) ? (p.D - p.R / 2) / N : p.D / N;
+  while ((1 << shift) < places) ++shift;
+  if (vec && !p.half) return launch_pdl(rope_vec_kernel<T, kInterleaved>, grid, kThreads, smem, stream, p, shift);
+  if (vec && mult(p.R / 2)) return launch_pdl(rope_vec_kernel<T, kHalf>, grid, kThreads, smem, stream, p, shift);
+  // (in the shared memory that needs no grant)
+  if (vec && smem + rows <= 48 * 1024)
+    return launch_pdl(rope_vec_kernel<T, kStaged>, grid, kThreads, smem + rows, stream, p, shift);
+  return launch_pdl(rope_scalar_kernel<T>, grid, kThreads, smem, stream, p);
 }
 
 }  // namespace
