@@ -26,6 +26,12 @@ prompt's blocks are grouped (``pa_alloc_prefix_groups``), the new tokens' K/V go
 slots with ``pa_reshape_and_cache``, and ``pa_decode_shared_prefix`` reads each group's
 shared blocks once.
 
+``extend`` takes device tensors and any number of new tokens per sequence (prompts, chunks,
+single tokens in one batch): rotary positions and the cache write (``pa_rope_and_cache``), then
+``pa_attention`` with capped or biased scores and masks.  ``beam_step`` selects the next tokens
+of beam searches (``pa_beam_topk``), re-points the beams' blocks (``pa_alloc_beam_select``) and
+reorders other per-beam states (``pa_beam_gather``).
+
 ``pipeline`` (``StepPipeline``, the C ``pa_pipeline_*`` calls) queues such steps back to
 back, one C call per step: staging in several slots, the copies on their own streams, so
 the host and the copy engines work on neighbouring steps while the GPU decodes the
@@ -275,6 +281,139 @@ class PagedKVCache:
             self._out_h.copy_(self._out_d, non_blocking=True)
         stream.synchronize()
         return self._out_h, (used, self._out_h.numel() * self._out_h.element_size())
+
+    # -- prompts, chunks and single tokens, device tensors in and out --------------------
+    def _append_tokens(self, seq_ids, query_lens):
+        """Slots of query_lens[b] more tokens of every sequence (a new one is registered), all or
+        nothing; returns (slots int64 [T], positions int32 [T], copy pairs)."""
+        slots, positions, pairs, grown = [], [], [], []
+        try:
+            for sid, n in zip(seq_ids, query_lens):
+                try:
+                    _, have = self.alloc.block_table(sid)
+                except _b.PAError as e:
+                    if e.status != _b.PA_ERR_NOT_FOUND:
+                        raise
+                    self.alloc.add_seq(sid, n)
+                    grown.append((sid, None))
+                    slots.extend(self.alloc.seq_slots(sid).tolist())
+                    positions.extend(range(n))
+                    continue
+                grown.append((sid, have))
+                for i in range(n):
+                    slot, src, dst = self.alloc.append_slot(sid)
+                    slots.append(slot)
+                    if src >= 0:
+                        pairs.append((src, dst))
+                positions.extend(range(have, have + n))
+        except _b.PAError:
+            for sid, have in reversed(grown):
+                if have is None:
+                    self.alloc.free_seq(sid)
+                else:
+                    self.alloc.truncate(sid, have)
+            # a shared last block that was to be written is the sequence's own now: it keeps its tokens
+            self._copy_pairs(pairs)
+            raise
+        return slots, positions, pairs
+
+    def _copy_pairs(self, pairs, stream=None):
+        if pairs:
+            d = torch.tensor(pairs, dtype=torch.int32).to(self.device)
+            _b.pa_copy_blocks(self.k_pool, self.v_pool, d, err_flag=self.err, stream=stream)
+
+    def extend(self, seq_ids, query_lens, q, k, v, scale, inv_freq=None, layout=_b.PA_ROPE_HALF,
+               attn_factor=1.0, softcap=0.0, alibi_slopes=None, window=0, prefix_lens=None,
+               first_keys=None, out=None, stream=None):
+        """Append query_lens[b] tokens to every sequence, cache their K/V, attend.
+
+        q [T,Hq,D], k and v [T,Hkv,D] are device tensors of the pool dtype (parts of a projection's
+        output may be passed as they lie), the sequences' tokens one after the other; a sequence id
+        that is not known yet is registered (its prompt or the first chunk of it).  With inv_freq
+        (float64 device tensor, ``pa_rope_frequencies``) q and k are rotated by the tokens'
+        positions first.  softcap, alibi_slopes, window, prefix_lens and first_keys as in
+        ``pa_attention`` (device tensors).  Copy on write as in ``step``.  Returns out [T,Hq,D];
+        the work is queued on the stream.
+        """
+        lens = [int(n) for n in query_lens]
+        ids = [int(i) for i in seq_ids]
+        T, Hq, D = q.shape
+        # refused before the allocator or the pools change
+        if len(ids) != len(lens) or len(set(ids)) != len(ids) or min(lens, default=0) < 0 or sum(lens) != T:
+            raise ValueError("extend: distinct sequences, with query_lens that add up to q's tokens")
+        if tuple(k.shape) != (T, self.Hkv, self.D) or v.shape != k.shape or D != self.D:
+            raise ValueError("extend: q [T,Hq,D], k and v [T,Hkv,D]")
+        if not (q.dtype == k.dtype == v.dtype == self.dtype) or Hq % self.Hkv:
+            raise ValueError("extend: the pool's dtype, and query heads a multiple of its heads")
+        for t in (q, k, v, inv_freq, alibi_slopes, prefix_lens, first_keys, out):
+            if t is not None and t.device != self.k_pool.device:
+                raise ValueError("extend: tensors must be on the cache's device")
+        if inv_freq is not None and not (inv_freq.dtype == torch.float64 and inv_freq.dim() == 1
+                                         and 1 <= inv_freq.numel() <= D // 2):
+            raise ValueError("extend: inv_freq float64 [rotary_dim / 2]")
+        if T == 0:
+            return out if out is not None else torch.empty_like(q)
+        stream = stream or torch.cuda.current_stream(self.device)
+        B = len(ids)
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            slots, positions, pairs = self._append_tokens(ids, lens)
+            MB = max(1, max(-(-self.alloc.block_table(i)[1] // self.block_size) for i in ids))
+            tables, seq_lens = self.alloc.block_tables(ids, MB)
+            # everything of the step in one copy (the host array is staged before the call returns)
+            ints = np.concatenate([np.asarray(positions, np.int32), seq_lens,
+                                   np.concatenate([[0], np.cumsum(lens)]).astype(np.int32), tables.ravel()])
+            host = np.concatenate([np.asarray(slots, np.int64).view(np.int32), ints])
+            dev = torch.from_numpy(host).to(self.device)
+            slots_d, at = dev[:2 * T].view(torch.int64), 2 * T
+            pos_d, lens_d, starts_d, tables_d = (dev[at:at + T], dev[at + T:at + T + B],
+                                                 dev[at + T + B:at + T + 2 * B + 1], dev[at + T + 2 * B + 1:])
+            self._copy_pairs(pairs, stream)
+            if inv_freq is None:
+                _b.pa_reshape_and_cache(k.contiguous(), v.contiguous(), self.k_pool, self.v_pool, slots_d,
+                                        err_flag=self.err, stream=stream)
+                qr = q if q.stride(2) == 1 and q.stride(1) == D else q.contiguous()
+            else:
+                qr = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
+                _b.pa_rope_and_cache(qr, q, k, v, self.k_pool, self.v_pool, pos_d.contiguous(), slots_d, inv_freq,
+                                     layout=layout, attn_factor=attn_factor, err_flag=self.err, stream=stream)
+            most = max(lens)
+            n = _b.pa_attention_workspace_size(T, B, most, Hq, self.Hkv, D, self.block_size, MB)
+            ws = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+            if out is None:
+                out = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
+            _b.pa_attention(out, qr, self.k_pool, self.v_pool, tables_d.view(B, MB), lens_d, starts_d, most, scale,
+                            softcap=softcap, alibi_slopes=alibi_slopes, window=window, prefix_lens=prefix_lens,
+                            first_keys=first_keys, workspace=ws, err_flag=self.err, stream=stream)
+        return out
+
+    def beam_step(self, seq_ids, logits, cum_scores, finished=None, eos_token=0, states=(), stream=None):
+        """One selection of beam searches: seq_ids [N][W] (the beams' sequences), logits [N,W,V],
+        cum_scores [N,W] fp32, device tensors.
+
+        Beam i of request n continues from beam parents[n][i] with tokens[n][i]: its sequence is
+        re-pointed at the parent's blocks, and the states ([N,W,...] tensors) are reordered into
+        new ones.  Returns (scores [N,W], parents [N,W], tokens [N,W], states); waits for the
+        parents, which the host allocator needs.
+        """
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        N, W, V = logits.shape
+        if ids.shape != (N, W) or np.unique(ids).size != ids.size:
+            raise ValueError("beam_step: distinct sequences, one per beam of logits")
+        for i in ids.ravel().tolist():
+            self.alloc.block_table(i)  # every beam is live, or nothing changes
+        stream = stream or torch.cuda.current_stream(self.device)
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            ws = torch.empty(max(_b.pa_beam_topk_workspace_size(N, W, V, W), 1), dtype=torch.uint8, device=self.device)
+            scores = torch.empty((N, W), dtype=torch.float32, device=self.device)
+            parents, tokens = (torch.empty((N, W), dtype=torch.int32, device=self.device) for _ in range(2))
+            _b.pa_beam_topk(scores, parents, tokens, logits, cum_scores, finished=finished, eos_token=eos_token,
+                            workspace=ws, stream=stream)
+            moved = tuple(_b.pa_beam_gather(torch.empty_like(s), s, parents, err_flag=self.err, stream=stream)
+                          for s in states)
+            host = parents.cpu().numpy()
+        for n in range(N):
+            self.alloc.beam_select(ids[n], host[n])
+        return scores, parents, tokens, moved
 
     def pipeline(self, B, Hq, max_blocks, depth=2, stream=None, shared_prefix_members=0):
         """A StepPipeline over this cache: decode steps queued back to back (with
