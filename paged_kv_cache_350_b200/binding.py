@@ -1,4 +1,5 @@
-"""ctypes binding of libpagedattn (include/pa.h): argument marshalling only.
+"""Binding of libpagedattn (include/pa.h), by ctypes and, for the step calls that are made once
+per layer, by the module _calls: argument marshalling only.
 
 Every function keeps the C name and takes torch tensors (device memory and
 streams come from PyTorch); shapes are read from the tensors, pointers and
@@ -495,61 +496,22 @@ def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=PA_ROPE_SCALE_NONE, fa
     return out, f.value
 
 
-# The calls of a step take a few microseconds on the GPU, so their checks are written to take as
-# little on the host: attributes are read once, messages are built on failure only.
+# The step calls are in a module of their own (csrc/calls.cpp): the same checks and errors as here,
+# at a tenth of the time.
+try:
+    import torch as _torch  # noqa: F401  (its libraries, before the module that uses them)
 
-def _token_rows(t, name):
-    """Elements between the tokens of [T, H, D] rows whose heads lie side by side."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3:
-        raise ValueError(f"{name} must be [T, heads, D]")
-    T, H, D = shape
-    if not ((stride[2] == 1 or D == 1) and (stride[1] == D or H == 1)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if T <= 1:  # (the stride of a single token is arbitrary)
-        return H * D
-    if stride[0] < H * D:
-        raise ValueError(f"{name}: tokens must not overlap")
-    return stride[0]
+    from . import _calls
+except ImportError as e:
+    raise ImportError("the step calls (_calls.so) are not built; build them with "
+                      "`python -m paged_kv_cache_350_b200.build`") from e
 
-
-def _contiguous(names, *ts):
-    for t in ts:
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{names} must be contiguous")
-
-
-def pa_rope_and_cache(q_out, q, k, v, k_pool, v_pool, positions, slot_mapping, inv_freq,
-                      layout=PA_ROPE_HALF, attn_factor=1.0, err_flag=None, stream=None):
-    """Rotate q [T,Hq,D] into q_out and k [T,Hkv,D] into its slots, v unchanged into its own
-    (see include/pa.h); the rotated part of a head is 2 * inv_freq.numel() elements."""
-    import torch
-    pool, dt = k_pool.shape, q.dtype
-    if len(pool) != 4 or v_pool.shape != pool:
-        raise ValueError("pools must be [NB, bs, Hkv, D]")
-    NB, bs, Hkv, D = pool
-    qs, ks, vs = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
-    T, Hq, Dq = q.shape
-    if Dq != D or tuple(k.shape) != (T, Hkv, D) or v.shape != k.shape:
-        raise ValueError("q/k/v shape mismatch")
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    if positions.dtype != torch.int32 or positions.numel() != T:
-        raise ValueError("positions int32 [T]")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
-        raise ValueError("slot_mapping int64 [T]")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
-        raise ValueError("inv_freq float64 [rotary_dim / 2]")
-    if not (dt == k.dtype == v.dtype == q_out.dtype == k_pool.dtype == v_pool.dtype):
-        raise ValueError("q, k, v, q_out and pools share a dtype")
-    _contiguous("q_out, pools and index tensors", q_out, k_pool, v_pool, positions, slot_mapping, inv_freq)
-    _on_device(q_out, q, k, v, k_pool, v_pool, positions, slot_mapping, inv_freq, err_flag=err_flag)
-    st = lib.pa_rope_and_cache(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pool.data_ptr(),
-                               v_pool.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(),
-                               inv_freq.data_ptr(), T, Hq, Hkv, D, bs, NB, qs, ks, vs, 2 * inv_freq.numel(),
-                               layout, float(attn_factor), _dtype_of(q), _ptr(err_flag), _stream(stream))
-    if st:
-        _check(st, "pa_rope_and_cache")
+_calls.bind(PAError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+    lib.pa_rope_and_cache, lib.pa_attention, lib.pa_beam_topk, lib.pa_beam_gather)))
+pa_rope_and_cache = _calls.pa_rope_and_cache
+pa_attention = _calls.pa_attention
+pa_beam_topk = _calls.pa_beam_topk
+pa_beam_gather = _calls.pa_beam_gather
 
 
 def pa_attention_workspace_size(T, B, max_query_len, Hq, Hkv, D, block_size, max_blocks):
@@ -559,118 +521,11 @@ def pa_attention_workspace_size(T, B, max_query_len, Hq, Hkv, D, block_size, max
     return n
 
 
-def pa_attention(out, q, k_pool, v_pool, block_tables, seq_lens, query_starts, max_query_len, scale,
-                 softcap=0.0, alibi_slopes=None, window=0, prefix_lens=None, first_keys=None,
-                 workspace=None, err_flag=None, stream=None):
-    """out[T,Hq,D] = attention of q's ragged query tokens over the paged cache (see
-    include/pa.h): sequence b's tokens are rows query_starts[b] .. query_starts[b + 1] - 1."""
-    import torch
-    stride = _token_rows(q, "q")
-    shape, pool, i32 = q.shape, k_pool.shape, torch.int32
-    if out.shape != shape:
-        raise ValueError("out must have q's shape")
-    if len(pool) != 4 or v_pool.shape != pool:
-        raise ValueError("pools must be [NB, bs, Hkv, D]")
-    if block_tables.dim() != 2 or block_tables.dtype != i32:
-        raise ValueError("block_tables int32 [B, MB]")
-    T, Hq, D = shape
-    NB, bs, Hkv, D2 = pool
-    B, MB = block_tables.shape
-    if D2 != D:
-        raise ValueError("head dim mismatch")
-    if seq_lens.dtype != i32 or seq_lens.numel() != B:
-        raise ValueError("seq_lens int32 [B]")
-    if query_starts.dtype != i32 or query_starts.numel() != B + 1:
-        raise ValueError("query_starts int32 [B + 1]")
-    mods = None
-    if softcap or window or alibi_slopes is not None or prefix_lens is not None or first_keys is not None:
-        for t, n, dt, name in ((alibi_slopes, Hq, torch.float32, "alibi_slopes float32 [Hq]"),
-                               (prefix_lens, B, i32, "prefix_lens int32 [B]"),
-                               (first_keys, T, i32, "first_keys int32 [T]")):
-            if t is not None and (t.dtype != dt or t.numel() != n):
-                raise ValueError(name)
-        mods = ctypes.byref(pa_attention_mods(float(softcap), int(window),
-                                              None if alibi_slopes is None else alibi_slopes.data_ptr(),
-                                              None if prefix_lens is None else prefix_lens.data_ptr(),
-                                              None if first_keys is None else first_keys.data_ptr()))
-    dt = q.dtype
-    if not (dt == out.dtype == k_pool.dtype == v_pool.dtype):
-        raise ValueError("q, out and pools share a dtype")
-    _contiguous("out, pools and index tensors", out, k_pool, v_pool, block_tables, seq_lens, query_starts,
-                alibi_slopes, prefix_lens, first_keys, workspace)
-    _on_device(out, q, k_pool, v_pool, block_tables, seq_lens, query_starts, alibi_slopes, prefix_lens,
-               first_keys, workspace, err_flag=err_flag)
-    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = lib.pa_attention(out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-                          block_tables.data_ptr(), seq_lens.data_ptr(), query_starts.data_ptr(), T, B,
-                          int(max_query_len), Hq, Hkv, D, bs, MB, NB, stride, float(scale), mods, _dtype_of(q),
-                          _ptr(workspace), wbytes, _ptr(err_flag), _stream(stream))
-    if st:
-        _check(st, "pa_attention")
-    return out
-
-
 def pa_beam_topk_workspace_size(N, W, V, k):
     n = lib.pa_beam_topk_workspace_size(N, W, V, k)
     if n == ctypes.c_size_t(-1).value:
         raise PAError(PA_ERR_INVALID_ARG, "pa_beam_topk_workspace_size")
     return n
-
-
-def pa_beam_topk(scores, parents, tokens, logits, cum_scores, finished=None, eos_token=0,
-                 workspace=None, stream=None):
-    """The k best candidates of every request (scores, parents, tokens: [N, k]) from logits
-    [N, W, V] and the beams' scores so far [N, W] (see include/pa.h)."""
-    import torch
-    shape, stride = logits.shape, logits.stride()
-    if len(shape) != 3:
-        raise ValueError("logits must be [N, W, V]")
-    N, W, V = shape
-    if not ((stride[2] == 1 or V == 1) and (N <= 1 or W <= 1 or stride[0] == W * stride[1])):
-        raise ValueError("logits: rows contiguous, at one stride")
-    row = stride[1] if W > 1 else (stride[0] if N > 1 else V)
-    best = scores.shape
-    if len(best) != 2 or best[0] != N or scores.dtype != torch.float32:
-        raise ValueError("scores float32 [N, k]")
-    if parents.shape != best or parents.dtype != torch.int32:
-        raise ValueError("parents int32 [N, k]")
-    if tokens.shape != best or tokens.dtype != torch.int32:
-        raise ValueError("tokens int32 [N, k]")
-    if cum_scores.dtype != torch.float32 or tuple(cum_scores.shape) != (N, W):
-        raise ValueError("cum_scores float32 [N, W]")
-    if finished is not None and (finished.dtype not in (torch.bool, torch.uint8)
-                                 or tuple(finished.shape) != (N, W)):
-        raise ValueError("finished bool or uint8 [N, W]")
-    _contiguous("tensors", scores, parents, tokens, cum_scores, finished, workspace)
-    _on_device(scores, parents, tokens, logits, cum_scores, finished, workspace)
-    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = lib.pa_beam_topk(scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), logits.data_ptr(),
-                          cum_scores.data_ptr(), _ptr(finished), int(eos_token), N, W, V, best[1], row,
-                          _dtype_of(logits), _ptr(workspace), wbytes, _stream(stream))
-    if st:
-        _check(st, "pa_beam_topk")
-
-
-def pa_beam_gather(dst, src, parents, err_flag=None, stream=None):
-    """dst[n][i] = src[n][parents[n][i]]: per-beam states [N, W, ...] in the order of parents [N, k]."""
-    import torch
-    if parents.dim() != 2 or parents.dtype != torch.int32:
-        raise ValueError("parents int32 [N, k]")
-    N, k = parents.shape
-    shape = src.shape
-    if len(shape) < 2 or shape[0] != N:
-        raise ValueError("src must be [N, W, ...]")
-    if dst.dtype != src.dtype or tuple(dst.shape) != (N, k, *shape[2:]):
-        raise ValueError("dst must be [N, k, ...]")
-    _contiguous("tensors", dst, src, parents)
-    _on_device(dst, src, parents, err_flag=err_flag)
-    W, n = shape[1], src.numel()
-    if n and k:
-        st = lib.pa_beam_gather(dst.data_ptr(), src.data_ptr(), parents.data_ptr(), N, W, k,
-                                n // (N * W) * src.element_size(), _ptr(err_flag), _stream(stream))
-        if st:
-            _check(st, "pa_beam_gather")
-    return dst
 
 
 def pa_selftest_bounded_wait(err_flag, limit_us, stream=None):

@@ -5,7 +5,8 @@
 Compiles every source under ``csrc/`` with nvcc (``-gencode
 arch=compute_100a,code=sm_100a -lineinfo -O3``), links one shared library with
 the CUDA runtime linked statically, and places it next to this file, where the
-Python binding loads it.  Objects go to ``_build/`` at the repository root.
+Python binding loads it.  ``_calls.so``, the Python module with the step calls on torch
+tensors, is compiled beside it with the host compiler.  Objects go to ``_build/`` at the repository root.
 Rebuilds only what changed unless ``--force``.
 """
 
@@ -24,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
+CALLS = os.path.join(PKG, "_calls.so")  # the step calls on torch tensors (csrc/calls.cpp)
 
 SOURCES = ["api.cu", "decode_tc.cu", "decode_stream.cu", "decode_generic.cu", "cache_ops.cu", "allocator.cpp",
            "decode_noalloc.cu", "decode_prefix.cu", "selftest.cu", "pipeline.cpp",
@@ -88,7 +90,36 @@ def build(force=False, verbose=False, extra_flags=(), out=None, build_dir=None):
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("linking libpagedattn.so failed")
         os.replace(tmp, lib_path)
+    if out is None:
+        build_calls(force=force, verbose=verbose)
     return lib_path
+
+
+def build_calls(force=False, verbose=False):
+    """The Python extension module with the step calls: host code against torch's headers."""
+    src = os.path.join(CSRC, "calls.cpp")
+    if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "pa.h")]):
+        return CALLS
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    lib = os.path.join(root, "lib")
+    tmp = CALLS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp,
+           "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode:
+        raise RuntimeError("compiling _calls.so failed")
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def main(argv=None):
