@@ -177,6 +177,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   // sequences whose rows see nothing have no tile: their rows are zero (one CTA each)
   for (int b = blockIdx.x; b < B; b += gridDim.x) {
     if (P[b] != 0) continue;
+    if (p.by_unit)
+      for (int h = threadIdx.x; h < Hkv; h += kThreads)
+        reinterpret_cast<int4*>(p.cuts)[b * Hkv + h] = make_int4(0, 0, 0, 0);
     int q0;
     const int n = attn_query_span(p, b, false, q0);
     uint4* o = reinterpret_cast<uint4*>(out + static_cast<int64_t>(q0) * p.Hq * D);
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   const int g = lane >> 2, tig = lane & 3;
   const int r0 = C::ROWS16 ? g : 2 * tig, r1 = C::ROWS16 ? g + 8 : 2 * tig + 1;  // score rows of this lane
-  int own_u = -1, own_slot = 0, own_n = 0;
+  int4 own = make_int4(0, 0, 0, 0);  // the cut unit that begins here: pieces, first partial, KV head and rows, token
   int i = 0;  // tiles consumed (ring position)
   bool ok = true;
   using Acc = WarpAcc<C, true>;
@@ -343,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       return out + (static_cast<int64_t>(sq.q0 + tok) * p.Hq + t.kvh * G + (r - tok * G)) * D;
     };
     if (gpos == ubeg && pend == uend) {
+      if (p.by_unit && lane == 0) reinterpret_cast<int4*>(p.cuts)[t.b * Hkv + t.kvh] = make_int4(0, 0, 0, 0);
       auto inverse = [](float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); };  // NaN stays
       if (g < rows) {
         const float inv = inverse(acc.l_lo);
@@ -376,9 +380,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           *reinterpret_cast<float2*>(o + 8 * D) = make_float2(acc.o_hi[jn][0], acc.o_hi[jn][1]);
       }
       if (ubeg >= beg) {  // the unit begins here: its pieces are those of s .. (uend - 1) / per
-        own_u = t.b * Hkv + t.kvh;
-        own_slot = slot;
-        own_n = (uend - 1) / per - s + 1;
+        own = make_int4((uend - 1) / per - s + 1, 2 * s + slot, t.kvh << 8 | rows, sq.q0);
+        if (p.by_unit && lane == 0) reinterpret_cast<int4*>(p.cuts)[t.b * Hkv + t.kvh] = own;
       }
     }
     gpos = pend;
@@ -389,70 +392,95 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int k = i; k < cnt && k < i + kStages; ++k)
       mbar_wait(smem_addr(&full_bar[warp * kStages + k % kStages]), (k / kStages) & 1, p.err);
   }
-  if (lane == 0) reinterpret_cast<int4*>(p.cuts)[s] = make_int4(ok ? own_u : -1, own_slot, own_n, 0);
+  if (!p.by_unit && lane == 0) reinterpret_cast<int4*>(p.cuts)[s] = own;
 }
 
-// Merge the pieces of the unit that begins in range s and goes on in the next ones: piece i is in
-// slot 0 of range s + i, but the first in the slot recorded.  PS groups of BT threads (one per row
-// and 4 columns) take pieces k, k + PS, .., and are then combined in order.
+// Merge the pieces of a unit that is cut: piece i is in slot 0 of range s + i, but the first in the
+// slot recorded.  Records lie by unit where units are fewer than ranges (most blocks would find
+// none), else by the range the unit begins in; no pieces: not cut.  PS groups of BT threads (one per
+// row and 4 columns) take pieces k, k + PS, .., kBatch of them at a time (one round trip), and are
+// then combined in order.
 template <int D>
 __global__ void __launch_bounds__(1024) tokens_join_kernel(const AttnParams p, int BT, int PS) {
+  constexpr int kBatch = 8;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int s = blockIdx.x;
-  const int4 cut = reinterpret_cast<const int4*>(p.cuts)[s];
-  if (cut.x < 0) return;
-  const int b = cut.x / p.Hkv, kvh = cut.x - b * p.Hkv;
-  int q0;
-  const int rows = attn_query_span(p, b, false, q0) * p.G;
+  const int4 cut = reinterpret_cast<const int4*>(p.cuts)[blockIdx.x];
+  const int n = cut.x;
+  if (n == 0) return;
+  const int kvh = cut.z >> 8, rows = cut.z & 255;
+  // a record that a warp which gave up (flagged) left unwritten is not followed out of range
+  if (n < 0 || cut.y < 0 || (cut.y >> 1) + n > p.ctas || kvh < 0 || kvh >= p.Hkv || rows < 1 || rows > p.RT ||
+      cut.w < 0 || cut.w + (rows - 1) / p.G >= p.T)
+    return;
   const int grp = threadIdx.x / BT, idx = threadIdx.x - grp * BT;
   const int r = idx / (D / 4), c = idx % (D / 4) * 4;
   const bool live = r < rows;
-  auto row_of = [&](int i) { return (static_cast<int64_t>(s + i) * 2 + (i == 0 ? cut.y : 0)) * p.RT + r; };
-  const float2* part = reinterpret_cast<const float2*>(p.part_ml);
-  // the maxima first: then the pieces' loads do not wait for one another
   float M = -INFINITY, l = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  // scale what there is to the maximum `m`; a maximum of -inf stands for no key at all
+  auto rescale = [&](float m) {
+    const float w = m == -INFINITY ? 0.f : exp2f(M - m);
+    l *= w;
+    a.x *= w;
+    a.y *= w;
+    a.z *= w;
+    a.w *= w;
+    M = m;
+  };
+  auto add = [&](float w, float l2, const float4& o) {
+    l = fmaf(l2, w, l);
+    a.x = fmaf(o.x, w, a.x);
+    a.y = fmaf(o.y, w, a.y);
+    a.z = fmaf(o.z, w, a.z);
+    a.w = fmaf(o.w, w, a.w);
+  };
   if (live) {
-#pragma unroll 8
-    for (int i = 0; i < cut.z; ++i) M = fmaxf(M, part[row_of(i)].x);
-    const float ref = M == -INFINITY ? 0.f : M;  // no key at all: every weight is 0
-#pragma unroll 4
-    for (int i = grp; i < cut.z; i += PS) {
-      const float2 ml = part[row_of(i)];
-      const float4 o = *reinterpret_cast<const float4*>(p.part_acc + row_of(i) * D + c);
-      const float w = exp2f(ml.x - ref);
-      l = fmaf(ml.y, w, l);
-      a.x = fmaf(o.x, w, a.x);
-      a.y = fmaf(o.y, w, a.y);
-      a.z = fmaf(o.z, w, a.z);
-      a.w = fmaf(o.w, w, a.w);
+    for (int i0 = grp; i0 < n; i0 += PS * kBatch) {
+      float2 ml[kBatch];
+      float4 o[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int i = i0 + b * PS;
+        ml[b] = make_float2(-INFINITY, 0.f);
+        o[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) {
+          const int64_t row = (static_cast<int64_t>(i == 0 ? cut.y : (cut.y & ~1) + 2 * i)) * p.RT + r;
+          ml[b] = reinterpret_cast<const float2*>(p.part_ml)[row];
+          o[b] = *reinterpret_cast<const float4*>(p.part_acc + row * D + c);
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) top = fmaxf(top, ml[b].x);
+      rescale(top);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) add(top == -INFINITY ? 0.f : exp2f(ml[b].x - top), ml[b].y, o[b]);
     }
   }
   if (PS > 1) {
-    extern __shared__ float red[];  // [PS][BT][5]
-    float* mine = red + (grp * BT + idx) * 5;
-    mine[0] = l;
-    mine[1] = a.x;
-    mine[2] = a.y;
-    mine[3] = a.z;
-    mine[4] = a.w;
+    extern __shared__ float red[];  // [PS][BT][6]
+    float* mine = red + (grp * BT + idx) * 6;
+    mine[0] = M;
+    mine[1] = l;
+    mine[2] = a.x;
+    mine[3] = a.y;
+    mine[4] = a.z;
+    mine[5] = a.w;
     __syncthreads();
     if (grp != 0) return;
     for (int k = 1; k < PS; ++k) {
-      const float* o = red + (k * BT + idx) * 5;
-      l += o[0];
-      a.x += o[1];
-      a.y += o[2];
-      a.z += o[3];
-      a.w += o[4];
+      const float* o = red + (k * BT + idx) * 6;
+      const float top = fmaxf(M, o[0]);
+      rescale(top);
+      add(top == -INFINITY ? 0.f : exp2f(o[0] - top), o[1], make_float4(o[2], o[3], o[4], o[5]));
     }
   }
   if (!live) return;
   const int t = r / p.G;
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
-                            (static_cast<int64_t>(q0 + t) * p.Hq + kvh * p.G + (r - t * p.G)) * D + c) =
+                            (static_cast<int64_t>(cut.w + t) * p.Hq + kvh * p.G + (r - t * p.G)) * D + c) =
       make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
 }
 
@@ -475,9 +503,9 @@ cudaError_t run(const AttnParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int BT = (p.RT * C::D / 4 + 31) / 32 * 32;
   // several pieces per unit are the rule where units are fewer than ranges
-  const int PS = static_cast<int64_t>(p.B) * p.Hkv < p.ctas ? (1024 / BT < 1 ? 1 : 1024 / BT < 4 ? 1024 / BT : 4) : 1;
-  return launch_pdl(tokens_join_kernel<C::D>, dim3(static_cast<unsigned>(p.ctas)), BT * PS, PS > 1 ? static_cast<size_t>(PS) * BT * 20 : 0, stream, p,
-                BT, PS);
+  const int PS = p.by_unit ? (1024 / BT < 1 ? 1 : 1024 / BT < 4 ? 1024 / BT : 4) : 1;
+  return launch_pdl(tokens_join_kernel<C::D>, dim3(static_cast<unsigned>(p.by_unit ? p.B * p.Hkv : p.ctas)), BT * PS,
+                    PS > 1 ? static_cast<size_t>(PS) * BT * 24 : 0, stream, p, BT, PS);
 }
 
 template <int D, int BS>
@@ -495,7 +523,9 @@ bool attention_tokens_eligible(int max_query_len, int G, int B) {
 
 int attention_tokens_ranges(int sms) { return sms * 2 * kWarps; }
 
-cudaError_t launch_attention_tokens(const AttnParams& p, cudaStream_t stream) {
+cudaError_t launch_attention_tokens(const AttnParams& params, cudaStream_t stream) {
+  AttnParams p = params;
+  p.by_unit = static_cast<int64_t>(p.B) * p.Hkv < p.ctas;
   switch (p.D * 100 + p.block_size) {
     case 6408: return run_rows<64, 8>(p, stream);
     case 6416: return run_rows<64, 16>(p, stream);
