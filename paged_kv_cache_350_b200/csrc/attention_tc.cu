@@ -6,8 +6,8 @@
 // serves M tile g; both read the same K and V tiles, so a tile of 128 keys is loaded once for up to
 // 256 rows.  Group g skips the tiles that none of its rows sees.
 //
-// Warps: 0-7 softmax (group g = warps 4g .. 4g + 3, a thread per row), 8 MMA, 9 K/V loads, 10
-// schedule and Q loads.  The schedule warp writes records of the CTA's pieces (a piece is the part
+// Warps: 0-7 softmax (group g = warps 4g .. 4g + 3, a thread per row), 8 and 11 the products of
+// group 0 and 1, 9 K/V loads, 10 schedule and Q loads.  The schedule warp writes records of the CTA's pieces (a piece is the part
 // of a unit in the range) into a small ring that all others follow.  K and V tiles share a ring
 // of slots in load order (K0 V0 K1 V1 ..), one TMA box per block and 64-column chunk.
 //
@@ -33,15 +33,15 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kKT = 128;        // keys per tile
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;  // (11 only rounds up the warpgroup)
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;  // and 11: the other group's products
 // Registers of a softmax thread and of another one: together what 384 threads are launched with.
 constexpr int kSoftRegs = 208, kOtherRegs = 88;
 constexpr int kPieces = 4;      // records in flight
 constexpr int kMaxSlots = 10;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kColS = 0, kColO = 256, kGroupCols = 128, kTmemCols = 512;
-// released by the MMA warp, the K/V load warp and each softmax warp
-constexpr int kPieceUsers = 2 + kSoftWarps;
+// released by the two MMA warps, the K/V load warp and each softmax warp
+constexpr int kPieceUsers = 3 + kSoftWarps;
 
 // CAP, BIAS: what is done to the scores, fixed at compile time so that the loop of a call is short
 // straight code (instruction fetches bound the kernel that decided at run time).
@@ -74,9 +74,9 @@ struct Piece {
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t qfull, qempty;
-  uint64_t sfull[2], pfull[2], ofull[2];  // per group
+  uint64_t sfull[2], pfull[2][2], ofull[2];  // per group; P in two halves
   uint64_t pc_full[kPieces], pc_empty[kPieces];
-  uint64_t drain_bar;
+  uint64_t drain_bar[2];
   Piece pc[kPieces];
   uint32_t tmem;
   volatile int abort_flag;
@@ -260,20 +260,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(smem_addr(&sh.full[i]), 1);
-      mbar_init(smem_addr(&sh.empty[i]), 1);
+      mbar_init(smem_addr(&sh.empty[i]), 2);  // both groups' products have read it
     }
     mbar_init(smem_addr(&sh.qfull), 1);
-    mbar_init(smem_addr(&sh.qempty), 1);
+    mbar_init(smem_addr(&sh.qempty), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.sfull[i]), 1);
-      mbar_init(smem_addr(&sh.pfull[i]), 128);
+      mbar_init(smem_addr(&sh.pfull[i][0]), 128);
+      mbar_init(smem_addr(&sh.pfull[i][1]), 128);
       mbar_init(smem_addr(&sh.ofull[i]), 1);
+      mbar_init(smem_addr(&sh.drain_bar[i]), 1);
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(smem_addr(&sh.pc_full[i]), 1);
       mbar_init(smem_addr(&sh.pc_empty[i]), kPieceUsers);
     }
-    mbar_init(smem_addr(&sh.drain_bar), 1);
     sh.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -453,20 +454,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok)  // loads issued but perhaps never waited for: the last of each slot
         for (int k = 0; k < NST; ++k)
           if (used >> k & 1) mbar_wait(smem_addr(&sh.full[k]), k < slot ? phase : phase ^ 1, nullptr);
-    } else if (warp == kMmaWarp) {
+    } else {
       // ============================ products ============================
+      // A warp per softmax group: what one does between products overlaps the other's products, and
+      // neither waits for the other group's P.  This loop is the latency between a group's P and its
+      // next S, so it is kept short: what it needs of a piece lies in (uniform) registers and ring
+      // slots are counted.
       constexpr uint32_t id_s = tc05::instr_desc_bf16(128, kKT, 0);
       constexpr uint32_t id_pv = tc05::instr_desc_bf16(128, D, 1);
-      // This loop is the latency between a group's P and its next S, so it is kept short: what it
-      // needs of a piece lies in (uniform) registers and ring slots are counted.
       // (a reduction over the warp tells the compiler that a value is the same in all lanes)
       auto uni = [](int v) { return __reduce_max_sync(kFull, v); };
-      const uint32_t q_base = smem_addr(smem), ring_base = smem_addr(ring);
+      const int g = uni(warp == kMmaWarp ? 0 : 1);
+      const uint32_t q_base = smem_addr(smem) + g * C::SLOT, ring_base = smem_addr(ring);
       const uint32_t full0 = smem_addr(&sh.full[0]), empty0 = smem_addr(&sh.empty[0]);
+      const uint32_t ts = tmem + kColS + g * kGroupCols, to = tmem + kColO + g * kGroupCols;
+      const uint32_t sfull = smem_addr(&sh.sfull[g]), ofull = smem_addr(&sh.ofull[g]);
+      const uint32_t pfull = smem_addr(&sh.pfull[g][0]);
       bool ok = true;
       int kslot = 0, vslot = 1;
-      uint32_t kphase = 0, vphase = 0;
-      uint32_t ppar = 0;  // bit g: parity of the group's P
+      uint32_t kphase = 0, vphase = 0, ppar = 0;  // parities of K's and V's slots, and of P
       auto next_slot = [](int& slot, uint32_t& phase) {
         slot += 2;
         if (slot >= NST) {
@@ -474,16 +480,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1;
         }
       };
-      auto issue_s = [&](int g) {
-        const uint64_t dq = tc05::smem_desc(q_base + g * C::SLOT, 16, 1024);
+      auto issue_s = [&] {
+        const uint64_t dq = tc05::smem_desc(q_base, 16, 1024);
         const uint64_t dk = tc05::smem_desc(ring_base + kslot * C::SLOT, 16, 1024);
-        const uint32_t ts = tmem + kColS + g * kGroupCols;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * C::CHUNK + (k & 3) * 32;
           tc05::mma_ss_warp(ts, dq + (off >> 4), dk + (off >> 4), id_s, k > 0);
         }
-        tc05::commit_warp(smem_addr(&sh.sfull[g]));
+        tc05::commit_warp(sfull);
       };
       for (int n = 0; ok; ++n) {
         if (!(ok = piece_wait(n))) break;
@@ -491,25 +496,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cnt = uni(pc.cnt);
         if (cnt == 0) break;
         const int k00 = uni(pc.kt0) * kKT, lo = uni(pc.lo) - k00, hi = uni(pc.hi) - k00;
-        const int a0 = uni(pc.ga[0]), b0 = uni(pc.gb[0]), a1 = uni(pc.ga[1]), b1 = uni(pc.gb[1]);
+        const int ga = uni(pc.ga[g]), gb = uni(pc.gb[g]);
         piece_done(n);
         // S of the first tile
         if (!(ok = wait_warp(smem_addr(&sh.qfull), n & 1, p.err, abort_flag) &&
                    wait_warp(full0 + 8 * kslot, kphase, p.err, abort_flag)))
           break;
         tc05::fence_after_sync();
-        if (a0 == 0 && b0 > 0) issue_s(0);
-        if (a1 == 0 && b1 > 0) issue_s(1);
+        if (ga == 0 && gb > 0) issue_s();
         tc05::commit_warp(empty0 + 8 * kslot);
         if (cnt == 1) tc05::commit_warp(smem_addr(&sh.qempty));
         next_slot(kslot, kphase);
         for (int j = 0; j < cnt; ++j) {
-          const bool more = j + 1 < cnt;
           if (!(ok = wait_warp(full0 + 8 * vslot, vphase, p.err, abort_flag))) break;
           const int a = max(lo - j * kKT, 0), z = min(hi - j * kKT, kKT);  // the item's keys within the tile
           if (a > 0 || z < kKT) {
             // V rows outside them may hold anything (0 * Inf is NaN): zero those that the product
-            // reads, up to the 16-key steps
+            // reads, up to the 16-key steps (both warps write the same zeros)
             const int na = a & 15, nz = -z & 15;
             uint8_t* v = ring + vslot * C::SLOT;
             for (int e = lane; e < (na + nz) * DCH * 8; e += 32) {
@@ -520,39 +523,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
-          const uint64_t dv = tc05::smem_desc(ring_base + vslot * C::SLOT, C::CHUNK, 1024);
-          const int s0 = a >> 4, s1 = (z + 15) >> 4;
-          bool k_there = false;
-#pragma unroll 1
-          for (int g = 0; g < 2; ++g) {
-            const int ga = g ? a1 : a0, gb = g ? b1 : b0;
-            if (j >= ga && j < gb) {
-              const uint32_t tp = tmem + kColS + g * kGroupCols, to = tmem + kColO + g * kGroupCols;
-              // the group's first tile of the piece overwrites O
-              uint32_t acc = j != ga;
-              if (!(ok = wait_warp(smem_addr(&sh.pfull[g]), ppar >> g & 1, p.err, abort_flag))) break;
+          if (j >= ga && j < gb) {
+            const uint64_t dv = tc05::smem_desc(ring_base + vslot * C::SLOT, C::CHUNK, 1024);
+            const int s0 = a >> 4, s1 = (z + 15) >> 4;
+            uint32_t acc = j != ga;  // the group's first tile of the piece overwrites O
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // P comes in two halves
+              if (!(ok = wait_warp(pfull + 8 * h, ppar, p.err, abort_flag))) break;
               tc05::fence_after_sync();
 #pragma unroll
-              for (int k = 0; k < kKT / 16; ++k) {
+              for (int k = 4 * h; k < 4 * h + 4; ++k) {
                 if (k >= s0 && k < s1) {
-                  tc05::mma_ts_warp(to, tp + 8 * k, dv + (k * 2048 >> 4), id_pv, acc);
+                  tc05::mma_ts_warp(to, ts + 8 * k, dv + (k * 2048 >> 4), id_pv, acc);
                   acc = 1;
                 }
               }
-              ppar ^= 1u << g;
-              if (j == gb - 1) tc05::commit_warp(smem_addr(&sh.ofull[g]));
             }
-            if (more && j + 1 >= ga && j + 1 < gb) {
-              if (!k_there && !(ok = wait_warp(full0 + 8 * kslot, kphase, p.err, abort_flag))) break;
-              k_there = true;
-              issue_s(g);
-            }
+            if (!ok) break;
+            ppar ^= 1;
+            if (j == gb - 1) tc05::commit_warp(ofull);
           }
-          if (!ok) break;
           tc05::commit_warp(empty0 + 8 * vslot);
           next_slot(vslot, vphase);
-          if (more) {
-            if (!k_there && !(ok = wait_warp(full0 + 8 * kslot, kphase, p.err, abort_flag))) break;
+          if (j + 1 < cnt) {
+            if (!(ok = wait_warp(full0 + 8 * kslot, kphase, p.err, abort_flag))) break;
+            if (j + 1 >= ga && j + 1 < gb) issue_s();
             tc05::commit_warp(empty0 + 8 * kslot);
             if (j + 2 == cnt) tc05::commit_warp(smem_addr(&sh.qempty));
             next_slot(kslot, kphase);
@@ -562,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) *abort_flag = 1;
       // every product issued has completed before the memory is freed
       __syncwarp();
-      tc05::commit_warp(smem_addr(&sh.drain_bar));
-      mbar_wait(smem_addr(&sh.drain_bar), 0, p.err);
+      tc05::commit_warp(smem_addr(&sh.drain_bar[g]));
+      mbar_wait(smem_addr(&sh.drain_bar[g]), 0, p.err);
     }
   } else {
     // ============================ softmax ============================
@@ -627,7 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc05::fence_after_sync();
         if (32 * w >= rows) {  // none of the warp's rows is a row of the item
           tc05::fence_before_sync();
-          mbar_arrive(smem_addr(&sh.pfull[g]));
+          mbar_arrive(smem_addr(&sh.pfull[g][0]));
+          mbar_arrive(smem_addr(&sh.pfull[g][1]));
           continue;
         }
         const int key0 = (pc.kt0 + j) * kKT;
@@ -688,6 +684,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[e] = pack_bf16x2(y.x, y.y);
           }
           tc05::st32(ts + 32 * h, v);
+          // the product of this half runs while the other is computed
+          tc05::wait_st();
+          tc05::fence_before_sync();
+          mbar_arrive(smem_addr(&sh.pfull[g][h]));
         };
         if constexpr (CAP_ONLY) {
 #pragma unroll 1
@@ -709,11 +709,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           weights(x, 0);
           weights(x + 64, 1);
         }
-        // (P as a whole: where its halves were signalled one by one, the products waited for the
-        // second half of one group while the other group's P lay ready: 790 us against 700)
-        tc05::wait_st();
-        tc05::fence_before_sync();
-        mbar_arrive(smem_addr(&sh.pfull[g]));
         l += (l0.x + l0.y) + (l1.x + l1.y);
       }
       if (!ok) break;
