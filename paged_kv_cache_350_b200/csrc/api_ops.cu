@@ -271,6 +271,16 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
   p.scale_log2 = static_cast<float>(scale * log2e);
   p.cap_in = m.softcap > 0.f ? static_cast<float>(static_cast<double>(scale) / m.softcap) : 0.f;
   p.cap_out = m.softcap > 0.f ? static_cast<float>(m.softcap * log2e) : 0.f;
+  {
+    // tanh(t) / t in powers of t^2 (attention_tc.cu), of t = cap_in * x and times cap_out; where the
+    // powers of cap_in leave the range of 32 bits the polynomial is not used (a bound of inf)
+    static const double kTanh[5] = {0.9999918341636658, -0.3330950140953064, 0.13136771321296692,
+                                    -0.04714450612664223, 0.01063788216561079};
+    const double ci = m.softcap > 0.f ? static_cast<double>(scale) / m.softcap : 0.0;
+    for (int k = 0; k < 5; ++k) p.cap_poly[k] = static_cast<float>(kTanh[k] * m.softcap * log2e * std::pow(ci, 2 * k + 1));
+    const bool usable = std::fabs(ci) >= 1e-3 && std::fabs(ci) <= 1e3 && m.softcap >= 1e-6f && m.softcap <= 1e6f;
+    p.cap_small = usable ? static_cast<float>(std::fabs(ci)) : INFINITY;
+  }
   p.window = m.window;
   p.T = T;
   p.B = B;

@@ -138,11 +138,25 @@ __device__ __forceinline__ bool wait_lane0(uint32_t bar, uint32_t parity, int32_
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// The same for a whole warp: every lane waits, and the warp agrees.
+// The same for a whole warp: every lane waits, and the warp agrees.  The loop is a try and a vote
+// (what a wait costs when it need not wait is on the kernels' critical paths); the time is looked
+// at every 4096th try, in milliseconds.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* err,
                                           volatile int* abort_flag) {
-  const bool ok = wait_or_abort(bar, parity, err, abort_flag);
-  return __all_sync(0xffffffffu, ok) != 0;
+  uint32_t since = 0;
+#pragma unroll 1
+  for (uint32_t n = 1;; ++n) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((n & 4095) != 0) continue;
+    if (__any_sync(0xffffffffu, *abort_flag)) return false;
+    const uint32_t now = static_cast<uint32_t>(global_timer_ns() >> 20);
+    if (n == 4096) since = now;
+    if (__any_sync(0xffffffffu, now - since > static_cast<uint32_t>(kWaitLimitNs >> 20))) {
+      flag_error(err, PA_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
 }
 
 // Order this thread's generic-proxy shared-memory writes before later async-proxy
