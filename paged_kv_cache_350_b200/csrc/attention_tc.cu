@@ -173,15 +173,24 @@ __device__ __forceinline__ void cap_scores(float (&x)[N], const AttnParams& p, b
   }
 }
 
-// Maximum of op(x) where op is max (SIGN 1) or of -x (SIGN -1); NaN are passed over.
-template <int SIGN, int N>
-__device__ __forceinline__ float extreme(const float (&x)[N]) {
+// Largest and smallest of a row's scores; NaN are passed over.
+template <int N>
+__device__ __forceinline__ float largest(const float (&x)[N]) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
   for (int j = 0; j < N; j += 8)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(SIGN * x[j + 2 * e], SIGN * x[j + 2 * e + 1]));
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(x[j + 2 * e], x[j + 2 * e + 1]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+template <int N>
+__device__ __forceinline__ float smallest(const float (&x)[N]) {
+  float m[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
+#pragma unroll
+  for (int j = 0; j < N; j += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = fminf(m[e], fminf(x[j + 2 * e], x[j + 2 * e + 1]));
+  return fminf(fminf(m[0], m[1]), fminf(m[2], m[3]));
 }
 
 // Elements of columns outside [a, b) become `v`.
@@ -200,7 +209,7 @@ __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& 
   constexpr int E = 8;
   if constexpr (CAP) {
     if (masked) mask_scores(x, r.lo - key0, r.hi - key0, 0.f);  // what lies there must not choose the formula
-    cap_scores(x, p, cap_is_small(p, fmaxf(extreme<1>(x), extreme<-1>(x))), 0.f);
+    cap_scores(x, p, cap_is_small(p, fmaxf(largest(x), -smallest(x))), 0.f);
   }
   if constexpr (BIAS) {
     const float d0 = static_cast<float>(r.pos - key0);
@@ -228,7 +237,7 @@ __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& 
     }
   }
   if (masked) mask_scores(x, r.lo - key0, r.hi - key0, -INFINITY);
-  return extreme<1>(x);
+  return largest(x);
 }
 
 template <int N>
@@ -666,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the cap is monotone: the extremes of the raw scores give the maximum and the formula,
           // and the scores are capped half by half below (short code, few registers)
           if (masked) mask_scores(x, row.lo - key0, row.hi - key0, __int_as_float(0x7fffffff));
-          const float mx = extreme<1>(x), mn = -extreme<-1>(x);
+          const float mx = largest(x), mn = smallest(x);
           small = cap_is_small(p, fmaxf(fabsf(mx), fabsf(mn)));
           float top[1] = {p.cap_in >= 0.f ? mx : mn};
           const bool none = mx == -INFINITY && mn == INFINITY;
