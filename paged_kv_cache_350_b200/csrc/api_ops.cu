@@ -69,7 +69,7 @@ size_t attention_carve(const AttnShape& s, int B, int D, char* ws, pa::AttnParam
     off += up256(bytes);
     return at;
   };
-  const int64_t header = take(8), seq = take(int64_t(B) * 4);
+  const int64_t header = take(16), seq = take(int64_t(B) * 4);
   const int64_t items = take(int64_t(s.max_items) * sizeof(pa::AttnItem));
   const int64_t sums = take((int64_t(s.max_items) + 1) * 4);
   const int64_t starts = take(int64_t(s.ctas) * sizeof(pa::AttnStart)), cuts = take(int64_t(s.ctas) * 16);
@@ -293,6 +293,7 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
   p.max_blocks = max_blocks;
   p.num_blocks = num_blocks;
   p.err = dev_err_flag;
+  p.dynamic = kernel == kTensor;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (kernel == kTokens) {

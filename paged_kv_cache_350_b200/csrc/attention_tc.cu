@@ -332,6 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const AttnStart st = p.starts[s];
         int left = st.count, item = st.item, kvh = st.kvh, at = st.tile, n = 0;
         int loaded = 0;  // Q loads issued
+        // many units: each CTA takes the next one when it has room for it, else its own range (attention.cu)
+        const bool dynamic = p.header[2] != 0;
+        const int units = p.header[0] * p.Hkv;
         int4 cut = make_int4(-1, 0, 0, 0);
         AttnItem it{};
         int sum = 0, slots = 0;
@@ -340,16 +343,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           while ((slots = p.tile_sum[item + 1] - sum) == 0) ++item;
           it = p.items[item];
         };
-        if (left > 0) load_item();
+        if (!dynamic && left > 0) load_item();
         for (;; ++n) {
           const int slot = n % kPieces;
           if (n >= kPieces &&
               !(ok = wait_or_abort(smem_addr(&sh.pc_empty[slot]), (n / kPieces - 1) & 1, p.err, abort_flag)))
             break;
           UnitPart u{0, 0, 0, 0};
-          if (left > 0) u = unit_part(p, slots, at, left);
-          left -= u.slots;
-          if (u.cnt == 0) left = -1;  // (the range ends before the unit's first tile)
+          if (dynamic) {
+            left = -1;
+            for (int next; left < 0 && (next = atomicAdd(p.header + 3, 1)) < units;) {
+              item = units / p.Hkv - 1 - next / p.Hkv;  // the last items of a sequence see the most
+              kvh = next % p.Hkv;
+              slots = p.tile_sum[item + 1] - p.tile_sum[item];
+              if (slots == 0) continue;
+              it = p.items[item];
+              u = unit_part(p, slots, 0, slots);
+              left = 1;
+            }
+          } else {
+            if (left > 0) u = unit_part(p, slots, at, left);
+            left -= u.slots;
+            if (u.cnt == 0) left = -1;  // (the range ends before the unit's first tile)
+          }
           at = 0;
           Piece* pc = &sh.pc[slot];
           if (left < 0) {
@@ -393,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < DCH; ++c)
               tma_load_3d(q + m * C::SLOT + c * C::CHUNK, &tmq, c * 64, kvh * p.G, tok + m * ht, bar, policy);
           ++loaded;
-          if (++kvh == p.Hkv) {
+          if (!dynamic && ++kvh == p.Hkv) {
             kvh = 0;
             ++item;
             if (left > 0) load_item();
@@ -838,7 +854,7 @@ cudaError_t run(const AttnParams& p, cudaStream_t stream) {
 }  // namespace
 
 // What a unit costs beside its tiles, in tiles.
-int attention_tc_extra() { return 1; }
+int attention_tc_extra() { return 2; }
 
 // Rows per item: two M tiles of whole tokens.
 int attention_tc_rows(int G) { return 2 * (128 / G) * G; }

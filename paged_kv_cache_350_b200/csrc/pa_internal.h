@@ -194,7 +194,9 @@ struct AttnParams {
   int RT, KT, ctas, max_items;
   int extra;                    // what a unit costs beside its tiles, in tiles
   int HR;                       // rows of a softmax group of the tensor-core kernel (RT, or RT / 2)
-  int32_t* header;              // [2]: items, slots (tiles and extra ones, of one KV head)
+  int dynamic;                  // units may be taken one by one
+  int32_t* header;              // [4]: items, slots (tiles and extra ones, of one KV head), whether
+                                // units are taken one by one, the next unit then
   int32_t* seq_items;           // [B] items before the sequence
   AttnItem* items;              // [max_items]
   int32_t* tile_sum;            // [max_items + 1] slots before the item
