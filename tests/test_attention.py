@@ -290,6 +290,93 @@ def test_large_scores_and_equal_keys(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mods", [{}, dict(softcap=30.0, spread=3.0), dict(bias=True, window=50)])
+def test_many_short_units(mods):
+    """More units than the ranges of one wave: they are taken one by one, empty ones skipped."""
+    n = [33 if i % 7 else 0 for i in range(190)]
+    L = [a + (i * 37) % 150 for i, a in enumerate(n)]
+    Case("bf16", n, L, 16, 8, 64, 16, seed=2, **mods).check()
+
+
+@pytest.mark.gpu
+def test_more_sequences_than_the_token_kernel_scans():
+    Case("bf16", [1] * 2100, [i % 40 for i in range(2100)], 2, 1, 64, 8, softcap=10.0).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_wide_groups(dtype):
+    """More query heads per KV head than a product's rows."""
+    Case(dtype, [3, 1], [50, 200], 130, 1, 64, 16, bias=True).check()
+    Case(dtype, [3, 1], [50, 200], 128, 1, 64, 16, window=30).check()
+    Case(dtype, [9, 1], [50, 200], 33, 1, 64, 16, softcap=20.0).check()
+
+
+@pytest.mark.gpu
+def test_negative_and_zero_scales_and_extreme_caps():
+    for scale, cap in ((-0.1, 0.0), (0.0, 0.0), (-0.1, 5.0), (0.1, 1e-3), (1e-6, 30.0), (0.1, 1e5)):
+        for n in ([1, 1], [40, 3]):
+            c = Case("bf16", n, [70, 300], 4, 2, 64, 16, softcap=cap)
+            c.scale = scale
+            c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [[1, 1], [70, 1]])
+def test_infinities_behind_a_mask_reach_nobody(dtype, n):
+    """Slots past the lengths and before every window hold infinities of both signs."""
+    c = Case(dtype, n, [100, 333], 8, 2, 64, 16, window=20)
+    for pool in (c.k_pool, c.v_pool):
+        pool[pool != pool] = math.inf
+        pool[:, ::2][pool[:, ::2] == math.inf] = -math.inf
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [[1, 1], [40, 70]])
+def test_blocks_past_32_bits(n):
+    """The blocks lie behind 2^32 bytes (2^31 elements) of the pools."""
+    c = Case("bf16", n, [100, 300], 8, 8, 128, 32)
+    far = (1 << 31) // (32 * 8 * 128) + 5
+    small = c.k_pool.shape[0]
+    kd, vd = (torch.empty((far + small, 32, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kd[far:], vd[far:] = c.k_pool.cuda(), c.v_pool.cuda()
+    _, (args, kw) = c.run()
+    args[2], args[3] = kd, vd
+    args[4] = torch.where(args[4] >= 0, args[4] + far, args[4])
+    args[0].fill_(7.0)
+    pa.pa_attention(*args, **kw)
+    torch.cuda.synchronize()
+    assert int(kw["err_flag"].item()) == 0
+    c.close(args[0][:sum(n)].cpu().double())
+    # the cache write reaches them as well
+    T = 3
+    q, k, v = (torch.randn(T, 8, 128, device="cuda").bfloat16() for _ in range(3))
+    slots = torch.tensor([far * 32 + 1, (far + small) * 32 - 1, far * 32 + 40], device="cuda")
+    inv = torch.zeros(64, dtype=torch.float64, device="cuda")   # no rotation: the rows themselves
+    pa.pa_rope_and_cache(torch.empty_like(q), q, k, v, kd, vd, torch.zeros(T, dtype=torch.int32, device="cuda"), slots,
+                         inv)
+    assert torch.equal(kd.view(-1, 8, 128)[slots], k) and torch.equal(vd.view(-1, 8, 128)[slots], v)
+
+
+@pytest.mark.gpu
+def test_two_streams_with_a_workspace_each():
+    cases = [Case("bf16", [64] * 4, [500, 64, 700, 90], 8, 2, 128, 16, seed=s, softcap=20.0) for s in (1, 2)]
+    runs = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for (_, (args, _)) in runs:
+        args[0].fill_(0)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, (_, (args, kw)) in zip(streams, runs):
+            pa.pa_attention(*args, stream=s, **kw)
+    torch.cuda.synchronize()
+    for got, (args, _) in runs:
+        assert torch.equal(args[0].cpu().double(), got)
+
+
+@pytest.mark.gpu
 def test_matches_pa_decode_on_single_tokens():
     c = Case("bf16", [1] * 20, [1 + 37 * i for i in range(20)], 32, 8, 128, 16)
     got, (args, _) = c.check()

@@ -170,6 +170,28 @@ def test_topk_strided_rows(dtype, stride, offset):
 
 
 @pytest.mark.gpu
+def test_topk_identical_beams_and_a_repeated_call():
+    """The first step of a search whose beams are all alike: every tie goes to beam 0; twice the same."""
+    x, cum = random_case(3, 1, 4000, torch.bfloat16, 8)
+    x, cum = x.expand(3, 4, 4000).contiguous(), cum.expand(3, 4).contiguous()
+    check(x, cum, 8)
+    assert all(torch.equal(a, b) for a, b in zip(select(x.cuda(), cum.cuda(), 8), select(x.cuda(), cum.cuda(), 8)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_topk_rows_past_32_bits(dtype):
+    """Rows that lie behind 2^31 elements of the logits."""
+    N, W, V = 2, 2, 3000
+    stride = (1 << 30) + 24
+    buf = torch.empty(3 * stride + V, dtype=dtype, device="cuda")
+    x, cum = random_case(N, W, V, dtype, 4)
+    d = torch.as_strided(buf, (N, W, V), (2 * stride, stride, 1))
+    d.copy_(x)
+    check(x, cum, 4, device_logits=d)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shape,dtype", [((7,), torch.int32), ((8, 16), torch.float32), ((3,), torch.uint8),
                                          ((5, 1, 3), torch.bfloat16), ((100003,), torch.int16)])
 def test_gather(shape, dtype):

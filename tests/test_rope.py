@@ -190,6 +190,38 @@ def test_rope_in_place_and_all_padded():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("R", [64, 50])
+def test_rope_in_a_graph_on_another_stream(layout, R):
+    """Captured and replayed: it follows its inputs, and the same inputs give the same bits."""
+    T, Hq, Hkv, D, bs = 40, 6, 2, 64, 8
+    q, k, v = (torch.randn(T, h, D, device="cuda").bfloat16() for h in (Hq, Hkv, Hkv))
+    kp, vp = (torch.zeros(8, bs, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = torch.randperm(64, device="cuda")[:T]
+    inv = torch.from_numpy(pa.pa_rope_frequencies(R)[0]).cuda()
+    out = torch.empty_like(q)
+    call = lambda s=None: pa.pa_rope_and_cache(out, q, k, v, kp, vp, pos, slots, inv, layout=layout, stream=s)  # noqa: E731
+    torch.cuda.synchronize()
+    call(torch.cuda.Stream())
+    torch.cuda.synchronize()
+    first = out.clone(), kp.clone(), vp.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for t in (out, kp, vp):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, (out, kp, vp)))
+    pos.add_(7)
+    graph.replay()
+    torch.cuda.synchronize()
+    ref, size = rotate(q.cpu().double(), pos.cpu(), inv.cpu().numpy(), 1.0, layout == 1)
+    assert bool(((out.cpu().double() - ref).abs() <= tolerance(ref, size, torch.bfloat16)).all())
+
+
+@pytest.mark.gpu
 def test_rope_bad_slot_is_flagged_and_skipped():
     T, Hq, Hkv, D, bs, NB = 4, 2, 1, 64, 16, 2
     q, k, v = (torch.randn(T, h, D, device="cuda") for h in (Hq, Hkv, Hkv))
