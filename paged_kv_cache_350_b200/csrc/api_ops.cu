@@ -26,13 +26,14 @@ struct AttnShape {
   int RT, HR, KT, ctas, max_items, extra;
 };
 
-// Which kernel a call takes.  The tensor-core ones take bf16 and blocks of whole swizzle atoms (8
-// rows): the tokens kernel a few rows per sequence, bound by the cache's bytes; the other groups
-// of at most the 128 rows of its M tile.
+// Which kernel a call takes.  The tensor-core ones take bf16 (a block of 4 tokens is half a swizzle
+// atom: the pattern goes by shared-memory address, so its box lands like any other): the tokens
+// kernel a few rows per sequence, bound by the cache's bytes; the other groups of at most the 128
+// rows of its M tile.
 enum AttnKernel { kGeneric, kTensor, kTokens };
 
-AttnKernel attention_kernel(int B, int max_query_len, int G, int block_size, pa_dtype dtype) {
-  if (dtype != PA_BF16 || block_size < 8) return kGeneric;
+AttnKernel attention_kernel(int B, int max_query_len, int G, pa_dtype dtype) {
+  if (dtype != PA_BF16) return kGeneric;
   if (pa::attention_tokens_eligible(max_query_len, G, B)) return kTokens;
   return G <= 128 ? kTensor : kGeneric;
 }
@@ -214,7 +215,7 @@ size_t pa_attention_workspace_size(int T, int B, int max_query_len, int Hq, int 
   size_t n = 0;  // enough for either type
   const int most = std::max(max_query_len, 1), G = Hq / Hkv;
   for (const pa_dtype dtype : {PA_F32, PA_BF16})
-    n = std::max(n, attention_carve(attention_shape(T, B, most, G, D, attention_kernel(B, most, G, block_size, dtype), sms),
+    n = std::max(n, attention_carve(attention_shape(T, B, most, G, D, attention_kernel(B, most, G, dtype), sms),
                                     B, D, nullptr, nullptr));
   return n;
 }
@@ -249,7 +250,7 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
   const int sms = pa::device_sms();
   if (sms <= 0) return PA_ERR_CUDA;
   const int G = Hq / Hkv;
-  const AttnKernel kernel = attention_kernel(B, max_query_len, G, block_size, dtype);
+  const AttnKernel kernel = attention_kernel(B, max_query_len, G, dtype);
   const AttnShape sh = attention_shape(T, B, max_query_len, G, D, kernel, sms);
   // tile counts are summed in 32 bits: of one KV head, or of all in the tokens kernel
   const int64_t rows = kernel == kTokens ? static_cast<int64_t>(B) * Hkv : sh.max_items;

@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kLoadWarp) {
       // ============================ K and V tiles ============================
-      const int BPT = kKT / BS;  // blocks per tile, at most 16
+      const int BPT = kKT / BS;  // blocks per tile, at most 32: a lane each
       const uint64_t policy = l2_policy_evict_normal();
       bool ok = true;
       int slot = 0;

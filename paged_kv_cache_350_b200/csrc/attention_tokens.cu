@@ -527,9 +527,11 @@ cudaError_t launch_attention_tokens(const AttnParams& params, cudaStream_t strea
   AttnParams p = params;
   p.by_unit = static_cast<int64_t>(p.B) * p.Hkv < p.ctas;
   switch (p.D * 100 + p.block_size) {
+    case 6404: return run_rows<64, 4>(p, stream);
     case 6408: return run_rows<64, 8>(p, stream);
     case 6416: return run_rows<64, 16>(p, stream);
     case 6432: return run_rows<64, 32>(p, stream);
+    case 12804: return run_rows<128, 4>(p, stream);
     case 12808: return run_rows<128, 8>(p, stream);
     case 12816: return run_rows<128, 16>(p, stream);
     case 12832: return run_rows<128, 32>(p, stream);

@@ -34,7 +34,7 @@ struct TileCfg {
   static constexpr int KSTEPS = D / 16;
   static constexpr int NT = D / 8;                      // output n-tiles of 8 columns
   static_assert(D == 64 || D == 128, "head dim");
-  static_assert(BS == 8 || BS == 16 || BS == 32, "block size");
+  static_assert(BS == 4 || BS == 8 || BS == 16 || BS == 32, "block size");
   static_assert(TILE_T % 16 == 0 && BPS <= 4 && (TILE_T % BS == 0 || BS % TILE_T == 0),
                 "stage tokens");
 };
