@@ -73,7 +73,7 @@ size_t attention_carve(const AttnShape& s, int B, int D, char* ws, pa::AttnParam
   const int64_t header = take(16), seq = take(int64_t(B) * 4);
   const int64_t items = take(int64_t(s.max_items) * sizeof(pa::AttnItem));
   const int64_t sums = take((int64_t(s.max_items) + 1) * 4);
-  const int64_t starts = take(int64_t(s.ctas) * sizeof(pa::AttnStart)), cuts = take(int64_t(s.ctas) * 16);
+  const int64_t starts = take(int64_t(s.ctas) * sizeof(pa::AttnStart)), cuts = take(int64_t(s.ctas) * sizeof(pa::AttnCut));
   const int64_t ml = take(int64_t(s.ctas) * 2 * s.RT * 8);
   const int64_t acc = take(int64_t(s.ctas) * 2 * s.RT * D * 4);
   if (p) {

@@ -138,12 +138,12 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
             }
           };
           if (p.first_keys) {
-            for (int t = t0; t <= t1; t += 8) {
-              int first[8];
+            for (int t = t0; t <= t1; t += 32) {  // (one round trip for the usual item)
+              int first[32];
 #pragma unroll
-              for (int u = 0; u < 8; ++u) first[u] = __ldg(p.first_keys + it.q0 + min(t + u, t1));
+              for (int u = 0; u < 32; ++u) first[u] = __ldg(p.first_keys + it.q0 + min(t + u, t1));
 #pragma unroll
-              for (int u = 0; u < 8; ++u) take(min(t + u, t1), first[u]);
+              for (int u = 0; u < 32; ++u) take(min(t + u, t1), first[u]);
             }
           } else {  // both ends are monotone in the token (from position 0 on, which sees key 0)
             take(max(t0, min(-it.pos0, t1)), 0);
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kGenThreads) attention_generic_kernel(const At
       }
   }
 
-  int own_item = -1, own_kvh = 0, own_slot = 0, own_n = 0;
+  AttnCut own{};
   int left = st.count, item = st.item, kvh = st.kvh, tile = st.tile;
   bool first_piece = true;
   while (left > 0) {
@@ -435,11 +435,8 @@ __global__ void __launch_bounds__(kGenThreads) attention_generic_kernel(const At
       }
     }
     if (!whole && tile == 0) {  // the unit begins here: its pieces follow in the next CTAs
-      own_item = item;
-      own_kvh = kvh;
-      own_slot = slot;
       const int64_t ubeg = static_cast<int64_t>(p.tile_sum[item]) * p.Hkv + static_cast<int64_t>(kvh) * slots;
-      own_n = static_cast<int>((ubeg + slots - 1) / per) - s + 1;
+      own = AttnCut{static_cast<int>((ubeg + slots - 1) / per) - s + 1, slot, kvh, it.q0, it.row0, it.rows, 0, 0};
     }
     first_piece = false;
     tile = 0;
@@ -448,7 +445,7 @@ __global__ void __launch_bounds__(kGenThreads) attention_generic_kernel(const At
       ++item;
     }
   }
-  if (tid == 0) reinterpret_cast<int4*>(p.cuts)[s] = make_int4(own_item, own_kvh, own_slot, own_n);
+  if (tid == 0) reinterpret_cast<AttnCut*>(p.cuts)[s] = own;
 }
 
 // ---- join -----------------------------------------------------------------------------------
@@ -460,43 +457,59 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) attention_join_kernel(const AttnParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kBatch = 4;
   const int s = blockIdx.x;
-  const int4 cut = reinterpret_cast<const int4*>(p.cuts)[s];
-  if (cut.x < 0) return;
-  const AttnItem it = p.items[cut.x];
+  const AttnCut cut = reinterpret_cast<const AttnCut*>(p.cuts)[s];
+  if (cut.pieces == 0) return;
   const int RT = p.RT;
   const int r = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
-  if (r >= it.rows) return;
+  if (r >= cut.rows) return;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   const float4* acc = reinterpret_cast<const float4*>(p.part_acc);
-  auto base = [&](int i) { return static_cast<int64_t>(s + i) * 2 + (i == 0 ? cut.z : 0); };
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i < cut.w; ++i) M = fmaxf(M, ml[base(i) * RT + r].x);
-  const float ref = M == -INFINITY ? 0.f : M;
+  auto base = [&](int i) { return static_cast<int64_t>(s + i) * 2 + (i == 0 ? cut.slot : 0); };
   constexpr int NC = D / 4 / 8;
+  float M = -INFINITY, l = 0.f;
   float4 a[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 2
-  for (int i = 0; i < cut.w; ++i) {
-    const float2 v = ml[base(i) * RT + r];
-    const float w = exp2f(v.x - ref);
-    l += v.y * w;
+  // kBatch pieces at a time: their loads are one round trip
+  for (int i0 = 0; i0 < cut.pieces; i0 += kBatch) {
+    float2 v[kBatch];
+    float4 o[kBatch][NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const float4 o = acc[(base(i) * (D / 4) + warp + 8 * c) * RT + r];
-      a[c].x = fmaf(o.x, w, a[c].x);
-      a[c].y = fmaf(o.y, w, a[c].y);
-      a[c].z = fmaf(o.z, w, a[c].z);
-      a[c].w = fmaf(o.w, w, a[c].w);
+    for (int b = 0; b < kBatch; ++b) {
+      const bool in = i0 + b < cut.pieces;
+      v[b] = in ? ml[base(i0 + b) * RT + r] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        o[b][c] = in ? acc[(base(i0 + b) * (D / 4) + warp + 8 * c) * RT + r] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float top = M;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) top = fmaxf(top, v[b].x);
+    const float ref = top == -INFINITY ? 0.f : top;  // no key yet: every weight is 0
+    const float old = exp2f(M - ref);
+    M = top;
+    l *= old;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) a[c] = make_float4(a[c].x * old, a[c].y * old, a[c].z * old, a[c].w * old);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const float w = exp2f(v[b].x - ref);
+      l = fmaf(v[b].y, w, l);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        a[c].x = fmaf(o[b][c].x, w, a[c].x);
+        a[c].y = fmaf(o[b][c].y, w, a[c].y);
+        a[c].z = fmaf(o[b][c].z, w, a[c].z);
+        a[c].w = fmaf(o[b][c].w, w, a[c].w);
+      }
     }
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  const int f = it.row0 + r;
+  const int f = cut.row0 + r;
   T* o = static_cast<T*>(p.out) +
-         (static_cast<int64_t>(it.q0 + f / p.G) * p.Hq + cut.y * p.G + f % p.G) * D;
+         (static_cast<int64_t>(cut.q0 + f / p.G) * p.Hq + cut.kvh * p.G + f % p.G) * D;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
     store4(o + (warp + 8 * c) * 4, make_float4(a[c].x * inv, a[c].y * inv, a[c].z * inv, a[c].w * inv));

@@ -20,6 +20,12 @@ struct AttnItem {
   int glo[2], ghi[2];  // the same of its rows [0, HR) and [HR, 2 HR)
 };
 
+// The cut unit that begins in a CTA's range: its pieces (0: none), the slot of the first one's
+// partial, and where its rows go.
+struct __align__(16) AttnCut {
+  int pieces, slot, kvh, q0, row0, rows, pad0, pad1;
+};
+
 // Where a CTA's range begins: the slot (extra ones, then tiles) of a unit, and the range's slots.
 struct AttnStart {
   int item, kvh, tile, count;

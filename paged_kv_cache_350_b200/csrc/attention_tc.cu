@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // many units: each CTA takes the next one when it has room for it, else its own range (attention.cu)
         const bool dynamic = p.header[2] != 0;
         const int units = p.header[0] * p.Hkv;
-        int4 cut = make_int4(-1, 0, 0, 0);
+        AttnCut cut{};
         AttnItem it{};
         int sum = 0, slots = 0;
         auto load_item = [&] {  // the item at or after `item` that has tiles
@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(smem_addr(&sh.pc_full[slot]));
           if (u.tile == 0 && cnt != u.nt) {  // the unit begins here and goes on in the next CTAs
             const int64_t ubeg = static_cast<int64_t>(sum) * p.Hkv + static_cast<int64_t>(kvh) * slots;
-            cut = make_int4(item, kvh, n == 0 ? 0 : 1, static_cast<int>((ubeg + slots - 1) / per) - s + 1);
+            cut = AttnCut{static_cast<int>((ubeg + slots - 1) / per) - s + 1, n == 0 ? 0 : 1, kvh, it.q0, it.row0,
+                          it.rows, 0, 0};
           }
           // its Q, once the products of the piece before have read theirs
           if (n > 0 && !(ok = wait_or_abort(smem_addr(&sh.qempty), (n - 1) & 1, p.err, abort_flag))) break;
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (left > 0) load_item();
           }
         }
-        reinterpret_cast<int4*>(p.cuts)[s] = cut;
+        reinterpret_cast<AttnCut*>(p.cuts)[s] = cut;
         if (!ok && loaded > 0) mbar_wait(smem_addr(&sh.qfull), (loaded - 1) & 1, nullptr);
       }
     } else if (warp == kLoadWarp) {

@@ -201,8 +201,7 @@ struct AttnParams {
   AttnItem* items;              // [max_items]
   int32_t* tile_sum;            // [max_items + 1] slots before the item
   AttnStart* starts;            // [ctas]
-  int32_t* cuts;                // [ctas][4]: item, KV head, slot, pieces of the cut unit that
-                                // begins in the CTA (item -1: none); the tokens kernel has its own
+  int32_t* cuts;                // [ctas] records of the cut units (AttnCut; the tokens kernel has its own)
   int by_unit;                  // tokens kernel: cuts lie by unit
   float* part_ml;               // [ctas][2][RT][2]: (max, sum) of a cut unit's piece, base 2
   float* part_acc;              // [ctas][2][D / 4][RT][4]: its unnormalised output
