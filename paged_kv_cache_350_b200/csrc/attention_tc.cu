@@ -83,6 +83,9 @@ struct Shared {
   volatile int abort_flag;
 };
 
+// What most tiles do not take is kept out of the way of the instructions that they do.
+__device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, 0); }
+
 __device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
 
 // What a row of a piece sees and how its scores are biased.
@@ -129,7 +132,7 @@ __device__ __forceinline__ bool cap_is_small(const AttnParams& p, float top) {
 template <int N>
 __device__ __forceinline__ void cap_scores(float (&x)[N], const AttnParams& p, bool small, float add) {
   constexpr int E = 8;  // elements taken step by step, so that the steps of one do not wait
-  if (small) {
+  if (__builtin_expect(small, 1)) {
     // tanh(t) / t as a polynomial in t^2 (iterated reweighted least squares on |t| <= 0.85, where
     // |t P(t^2) - tanh t| < 6.9e-7 in 32 bits): on the FMA pipe alone, the exponentials need the
     // other.  Scale and cap are in the coefficients.
@@ -208,12 +211,12 @@ __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& 
                                                bool masked, bool ahead) {
   constexpr int E = 8;
   if constexpr (CAP) {
-    if (masked) mask_scores(x, r.lo - key0, r.hi - key0, 0.f);  // what lies there must not choose the formula
+    if (rare(masked)) mask_scores(x, r.lo - key0, r.hi - key0, 0.f);  // what lies there must not choose the formula
     cap_scores(x, p, cap_is_small(p, fmaxf(largest(x), -smallest(x))), 0.f);
   }
   if constexpr (BIAS) {
     const float d0 = static_cast<float>(r.pos - key0);
-    if (ahead) {
+    if (rare(ahead)) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float y = CAP ? x[j] : x[j] * p.scale_log2;
@@ -236,7 +239,7 @@ __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& 
       }
     }
   }
-  if (masked) mask_scores(x, r.lo - key0, r.hi - key0, -INFINITY);
+  if (rare(masked)) mask_scores(x, r.lo - key0, r.hi - key0, -INFINITY);
   return largest(x);
 }
 
@@ -537,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool more = j + 1 < cnt, mine = j >= ga && j < gb;
           if (!(ok = wait_warp(full0 + 8 * vslot, vphase, p.err, abort_flag))) break;
           const int a = max(lo - j * kKT, 0), z = min(hi - j * kKT, kKT);  // the item's keys within the tile
-          if (a > 0 || z < kKT) {
+          if (rare(a > 0 || z < kKT)) {
             // V rows outside them may hold anything (0 * Inf is NaN): zero those that the product
             // reads, up to the 16-key steps (both warps write the same zeros)
             const int na = a & 15, nz = -z & 15;
@@ -665,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_warp(smem_addr(&sh.sfull[g]), done & 1, p.err, abort_flag))) break;
         tc05::fence_after_sync();
         const bool turn = kTurns && j >= turn_lo && j < turn_hi;
-        if (32 * w >= rows) {  // none of the warp's rows is a row of the item
+        if (rare(32 * w >= rows)) {  // none of the warp's rows is a row of the item
           if (turn) {
             if (!(ok = my_turn())) break;
             turn_over();
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (CAP_ONLY) {
           // the cap is monotone: the extremes of the raw scores give the maximum and the formula,
           // and the scores are capped half by half below (short code, few registers)
-          if (masked) mask_scores(x, row.lo - key0, row.hi - key0, __int_as_float(0x7fffffff));
+          if (rare(masked)) mask_scores(x, row.lo - key0, row.hi - key0, __int_as_float(0x7fffffff));
           const float mx = largest(x), mn = smallest(x);
           small = cap_is_small(p, fmaxf(fabsf(mx), fabsf(mn)));
           float top[1] = {p.cap_in >= 0.f ? mx : mn};
@@ -703,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool raise = mt > m_ref + kRescaleLog2;
         // (earlier P.V of the group are complete: S was issued behind them)
-        if (__any_sync(kFull, raise)) {
+        if (rare(__any_sync(kFull, raise))) {
           const float alpha = raise ? ex2_approx(m_ref - mt) : 1.f;
           if (j > ja) {
 #pragma unroll 1
@@ -753,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 64; ++e) y[e] = __uint_as_float(again[e / 32][e % 32]);
             cap_scores(y, p, small, ref2.x);
-            if (masked) mask_scores(y, row.lo - key0 - 64 * h, row.hi - key0 - 64 * h, -INFINITY);
+            if (rare(masked)) mask_scores(y, row.lo - key0 - 64 * h, row.hi - key0 - 64 * h, -INFINITY);
             weights(y, h);
           }
         } else {
