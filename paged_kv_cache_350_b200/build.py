@@ -29,7 +29,8 @@ CALLS = os.path.join(PKG, "_calls.so")  # the step calls on torch tensors (csrc/
 
 SOURCES = ["api.cu", "decode_tc.cu", "decode_stream.cu", "decode_generic.cu", "cache_ops.cu", "allocator.cpp",
            "decode_noalloc.cu", "decode_prefix.cu", "selftest.cu", "pipeline.cpp",
-           "rope.cu", "attention.cu", "attention_tc.cu", "attention_tokens.cu", "beam.cu", "api_ops.cu"]
+           "rope.cu", "attention.cu", "attention_tc.cu", "attention_tokens.cu",
+           "attention_tokens32.cu", "beam.cu", "api_ops.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -26,22 +26,21 @@ struct AttnShape {
   int RT, HR, KT, ctas, max_items, extra;
 };
 
-// Which kernel a call takes.  The tensor-core ones take bf16 (a block of 4 tokens is half a swizzle
-// atom: the pattern goes by shared-memory address, so its box lands like any other): the tokens
-// kernel a few rows per sequence, bound by the cache's bytes; the other groups of at most the 128
-// rows of its M tile.
+// Which kernel a call takes: the tokens kernels (one per type) a few rows per sequence, bound by the
+// cache's bytes; the tensor-core kernel bf16 with groups of at most the 128 rows of its M tile (a
+// block of 4 tokens is half a swizzle atom: the pattern goes by shared-memory address, so its box
+// lands like any other); CUDA cores the rest.
 enum AttnKernel { kGeneric, kTensor, kTokens };
 
 AttnKernel attention_kernel(int B, int max_query_len, int G, pa_dtype dtype) {
-  if (dtype != PA_BF16) return kGeneric;
   if (pa::attention_tokens_eligible(max_query_len, G, B)) return kTokens;
-  return G <= 128 ? kTensor : kGeneric;
+  return dtype == PA_BF16 && G <= 128 ? kTensor : kGeneric;
 }
 
 AttnShape attention_shape(int T, int B, int max_query_len, int G, int D, AttnKernel kernel, int sms) {
   AttnShape s{};
   if (kernel == kTokens) {
-    s.KT = 16;
+    s.KT = 8;  // (16 in bf16)
     s.RT = s.HR = max_query_len * G;
     s.ctas = pa::attention_tokens_ranges(sms);
     s.max_items = 0;
@@ -298,7 +297,7 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (kernel == kTokens) {
-    e = pa::launch_attention_tokens(p, s);
+    e = dtype == PA_BF16 ? pa::launch_attention_tokens(p, s) : pa::launch_attention_tokens32(p, s);
   } else {
     e = pa::launch_attention_plan(p, s);
     if (e == cudaSuccess)

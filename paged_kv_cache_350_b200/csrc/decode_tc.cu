@@ -321,6 +321,21 @@ bool make_q_map(CUtensorMap* map, const void* q, int B, int Hq, int D, int G) {
   return r == CUDA_SUCCESS;
 }
 
+bool make_pool_map_f32(CUtensorMap* map, const void* pool, int NB, int BS, int Hkv, int D, int box_rows) {
+  auto encode = get_encode_fn();
+  if (!encode) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(BS),
+                        static_cast<cuuint64_t>(NB)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 4, static_cast<cuuint64_t>(Hkv) * D * 4,
+                           static_cast<cuuint64_t>(BS) * Hkv * D * 4};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(D), 1, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(pool), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool make_q_rows_map(CUtensorMap* map, const void* q, int T, int Hq, int D, int64_t q_stride, int G,
                      int tokens) {
   auto encode = get_encode_fn();

@@ -129,6 +129,8 @@ bool make_pool_map_rows(CUtensorMap* map, const void* pool, int NB, int BS, int 
 // Tensor map over q viewed as [B][Hq][D] (bf16): boxes of 64 columns x G heads of one
 // batch row, 128-byte swizzled.
 bool make_q_map(CUtensorMap* map, const void* q, int B, int Hq, int D, int G);
+// The same view of an fp32 pool: box = box_rows rows of one head, all D columns, not swizzled.
+bool make_pool_map_f32(CUtensorMap* map, const void* pool, int NB, int BS, int Hkv, int D, int box_rows);
 // Tensor map over q as T tokens of [Hq][D], q_stride elements apart: boxes of 64 columns x G
 // heads x `tokens` tokens, 128-byte swizzled.
 bool make_q_rows_map(CUtensorMap* map, const void* q, int T, int Hq, int D, int64_t q_stride, int G,
@@ -211,7 +213,9 @@ cudaError_t launch_attention_generic(const AttnParams& p, pa_dtype dtype, cudaSt
 cudaError_t launch_attention_tc(const AttnParams& p, cudaStream_t stream);
 int attention_tc_rows(int G);
 int attention_tc_extra();
-cudaError_t launch_attention_tokens(const AttnParams& p, cudaStream_t stream);  // its join included
+// (their joins included)
+cudaError_t launch_attention_tokens(const AttnParams& p, cudaStream_t stream);
+cudaError_t launch_attention_tokens32(const AttnParams& p, cudaStream_t stream);
 bool attention_tokens_eligible(int max_query_len, int G, int B);
 int attention_tokens_ranges(int sms);
 cudaError_t launch_attention_join(const AttnParams& p, pa_dtype dtype, cudaStream_t stream);
