@@ -398,7 +398,9 @@ typedef struct pa_attention_mods {
  * reach up to 255 neighbouring (token, head) rows that do not see it.
  * mods may be NULL.  Workspace: pa_attention_workspace_size bytes, 256-byte aligned; its contents
  * need no initialisation, and calls whose kernels may overlap on the GPU must not share one.
- * Any Hq / Hkv, D in {64, 128}, block_size in {4, 8, 16, 32}, bf16 or fp32. */
+ * Any Hq / Hkv, D in {64, 128}, block_size in {4, 8, 16, 32}, bf16 or fp32.  In bf16 with more than
+ * 16 (token, head of the group) rows per sequence the softmax weights are rounded to bf16 for their
+ * product with V.  A batch whose tile counts could pass 2^31 is PA_ERR_UNSUPPORTED. */
 size_t pa_attention_workspace_size(int T, int B, int max_query_len, int Hq, int Hkv, int D,
                                    int block_size, int max_blocks);
 pa_status pa_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
@@ -421,8 +423,10 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
  *   finished    [N][W] bytes, nullable: a beam with a non-zero byte only continues with
  *               eos_token, its score unchanged
  *   scores [N][k] fp32, parents and tokens [N][k] int32: outputs
- * Sums and scores are 64-bit, rounded once to fp32.  A beam whose logits hold a NaN or +inf, or
- * nothing but -inf, has no candidate above -inf.  Candidates at -inf rank by index.
+ * Exponentials and a lane's sums are 32-bit, the rest 64-bit, scores rounded once to fp32: candidates
+ * of different beams whose scores agree to about 1e-6 may come in either order (beams with equal
+ * logits tie exactly).  A beam whose logits hold a NaN or +inf, or nothing but -inf, has no candidate
+ * above -inf.  Candidates at -inf rank by index.
  * 1 <= k <= 32, k <= W * V, W * V < 2^31.  The parents are what pa_alloc_beam_select takes
  * (k == W).  Workspace as pa_beam_topk_workspace_size, 256-byte aligned, no initialisation;
  * not shared by calls that may overlap. */

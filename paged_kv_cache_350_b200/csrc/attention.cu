@@ -21,11 +21,11 @@
 // join are saved (8 prompts of 2048 tokens: 381 -> 341 us).  Each unit is computed in the same way
 // whichever CTA takes it.
 //
-// CUDA-core kernel: fp32 inputs (no TF32), bf16 with more than 128 query heads per KV head.  A CTA holds a tile
-// of RT rows of Q, and K and V tiles of 64 keys as fp32 in shared memory; a thread computes MR x 4
-// scores and MR x D/16 outputs in registers.  With 16 rows or fewer per sequence and KV head
-// (single tokens) the 16-row variant reads the cache at the same rate with a quarter of the
-// arithmetic.
+// CUDA-core kernel: fp32 inputs (no TF32) and bf16 with more than 128 query heads per KV head, from 17
+// rows per sequence on.  A CTA holds a tile of RT rows of Q, and K and V tiles of 64 keys as fp32
+// in shared memory; a thread computes MR x 4 scores and MR x D/16 outputs in registers.  Bound by the
+// products' shared-memory reads (17 TFLOP/s for 8 prompts of 512 tokens).  The 16-row variant is
+// for batches of more sequences than the kernels for few rows scan.
 
 #include <cuda_bf16.h>
 #include <limits.h>

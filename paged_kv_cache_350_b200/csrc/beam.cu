@@ -13,7 +13,9 @@
 // maximum, which the softmax needs anyway; the first batch is filtered by the k-th largest of
 // the lanes' maxima, so few values are ever inserted.  A second, small kernel forms the scores of
 // the W * chunks * k values kept, spread over its warps, and keeps the best k of them.  Lists are
-// merged by bitonic steps across the lanes.
+// merged by bitonic steps across the lanes.  64 requests of 4 beams over 131072 fp32 logits: 31 us
+// (4.3 TB/s, issue at 54 %: an exponential and six more operations a logit) and 5 us for the join;
+// one request of 4 x 32000: 11 us with the gather, which is launches.
 //
 // lse and scores are 64-bit from the chunk sums on: the chosen indices compare scores of
 // different beams, which a 32-bit subtraction would round into ties.

@@ -299,8 +299,9 @@ def test_many_short_units(mods):
 
 
 @pytest.mark.gpu
-def test_more_sequences_than_the_token_kernel_scans():
-    Case("bf16", [1] * 2100, [i % 40 for i in range(2100)], 2, 1, 64, 8, softcap=10.0).check()
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_sequences_than_the_token_kernel_scans(dtype):
+    Case(dtype, [1] * 2100, [i % 40 for i in range(2100)], 2, 1, 64, 8, softcap=10.0).check()
 
 
 @pytest.mark.gpu
