@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "pa.h"
 
@@ -22,17 +23,18 @@ int device_sms();
 // device) holds what it has, so that most launches make no call.
 struct SmemGrant {
   std::atomic<int> bytes[kMaxDevices];
+  std::mutex mutex;  // a smaller grant of another thread must not follow a larger one
 };
 template <typename K>
 cudaError_t grant_smem(SmemGrant& g, K kernel, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
-  int have = g.bytes[dev].load(std::memory_order_relaxed);
-  if (bytes <= have) return cudaSuccess;
+  if (bytes <= g.bytes[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(g.mutex);
+  if (bytes <= g.bytes[dev].load(std::memory_order_relaxed)) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  while (e == cudaSuccess && have < bytes && !g.bytes[dev].compare_exchange_weak(have, bytes)) {
-  }
+  if (e == cudaSuccess) g.bytes[dev].store(bytes, std::memory_order_relaxed);
   return e;
 }
 
