@@ -44,29 +44,30 @@ constexpr int kDynamicUnits = 8;  // units a CTA
 // ---- plan --------------------------------------------------------------------------------
 
 // Exclusive scan over the CTA's threads; returns the total too.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+template <typename I>
+__device__ __forceinline__ I block_scan(I v, I* warp_sums, I& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
+  I incl = v;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(kFull, incl, off);
+    const I o = __shfl_up_sync(kFull, incl, off);
     if (lane >= off) incl += o;
   }
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    const int w = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
-    int s = w;
+    const I w = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
+    I s = w;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(kFull, s, off);
+      const I o = __shfl_up_sync(kFull, s, off);
       if (lane >= off) s += o;
     }
     warp_sums[lane] = s - w;
     if (lane == 31) warp_sums[32] = s;
   }
   __syncthreads();
-  const int r = warp_sums[warp] + incl - v;
+  const I r = warp_sums[warp] + incl - v;
   total = warp_sums[32];
   __syncthreads();
   return r;
@@ -83,21 +84,20 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
   __shared__ int seq_sh[kPlanKept], sum_sh[kPlanKept];
   int* seq_items = p.B <= kPlanKept ? seq_sh : p.seq_items;
   int* slots_before = p.max_items < kPlanKept ? sum_sh : p.tile_sum;
-  int items = 0;
+  // overlapping spans (malformed) could exceed the host's bound, and 32 bits
+  __shared__ int64_t wide_sums[33];
+  int64_t counted = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
-    int n = 0, q0;
+    int64_t n = 0, total;
+    int q0;
     if (b < p.B) n = (static_cast<int64_t>(attn_query_span(p, b, true, q0)) * p.G + p.RT - 1) / p.RT;
-    int total;
-    const int at = block_scan(n, sums, total);
-    if (b < p.B) seq_items[b] = items + at;
-    items += total;
+    const int64_t at = block_scan(n, wide_sums, total);
+    if (b < p.B) seq_items[b] = static_cast<int>(min(counted + at, static_cast<int64_t>(INT_MAX)));
+    counted += total;
   }
-  // overlapping spans (malformed) could exceed the host's bound
-  if (items > p.max_items) {
-    if (threadIdx.x == 0) flag_error(p.err, PA_DEVERR_BAD_SEQ_LEN);
-    items = p.max_items;
-  }
+  if (counted > p.max_items && threadIdx.x == 0) flag_error(p.err, PA_DEVERR_BAD_SEQ_LEN);
+  const int items = static_cast<int>(min(counted, static_cast<int64_t>(p.max_items)));
   __syncthreads();
   __shared__ int filled;  // items with tiles
   if (threadIdx.x == 0) filled = 0;
