@@ -345,7 +345,7 @@ pa_status pa_rope_frequencies(int rotary_dim, double base, pa_rope_scaling scali
  * the first rotary_dim elements of every head of q[t] and k[t] become
  *   f * (a cos theta_i - b sin theta_i, a sin theta_i + b cos theta_i)
  * and the elements from rotary_dim on stay.  q goes to q_out[t] ([T][Hq][D], contiguous; may be
- * q itself where q is contiguous), k and the unchanged v to slot slot_mapping[t] of the pools
+ * q itself where q is contiguous, and must not overlap q otherwise), k and the unchanged v to slot slot_mapping[t] of the pools
  * (as pa_reshape_and_cache; a slot < 0 rotates q only).  Angles are formed and reduced in 64
  * bits; the rotation is fp32, rounded once.
  *   inv_freq      [rotary_dim / 2] DEVICE array (pa_rope_frequencies, copied there once)
@@ -368,7 +368,7 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const voi
 /* What is done to the scores, and which keys a query token sees.  All zero / NULL: the plain
  * causal attention. */
 typedef struct pa_attention_mods {
-  float softcap;               /* > 0: x = softcap * tanh(x / softcap); 0: none */
+  float softcap;               /* > 0 (1e-30 .. 1e30): x = softcap * tanh(x / softcap); 0: none */
   int window;                  /* > 0: only the last `window` keys up to the token's own position
                                   (and later ones of the prefix); 0: no limit */
   const float* alibi_slopes;   /* [Hq] device, nullable: x -= slopes[h] * |p - j| (after the cap) */
@@ -392,10 +392,11 @@ typedef struct pa_attention_mods {
  *   query_starts [B + 1] int32 device, not decreasing, query_starts[B] <= T
  *   max_query_len  an upper bound on the query tokens of a sequence (chooses the kernel: 1 means
  *                single tokens); a sequence with more raises PA_DEVERR_BAD_SEQ_LEN
- * Table entries of blocks that hold no key visible to any token of the call are not read (a
- * window's freed blocks may be -1).  Slots past seq_lens[b] may hold anything.  A key that some
- * query token of the sequence sees must hold finite values: a NaN or infinity there may also
- * reach up to 255 neighbouring (token, head) rows that do not see it.
+ * Table entries of blocks that lie before the first key that any token of the sequence sees (a
+ * window's freed blocks may be -1) or past seq_lens[b] are not read.  Slots past seq_lens[b], and
+ * before that first key, may hold anything.  Between the first and the last key seen the cache must
+ * hold finite values: a NaN or infinity there may also reach up to 255 neighbouring (token, head)
+ * rows that do not see it.  out must not overlap q; |scale| and |scale| / softcap are at most 1e30.
  * mods may be NULL.  Workspace: pa_attention_workspace_size bytes, 256-byte aligned; its contents
  * need no initialisation, and calls whose kernels may overlap on the GPU must not share one.
  * Any Hq / Hkv, D in {64, 128}, block_size in {4, 8, 16, 32}, bf16 or fp32.  In bf16 with more than
@@ -422,12 +423,13 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
  *   cum_scores  [N][W] fp32 device; a beam at -inf (not yet in use) has no candidate above -inf
  *   finished    [N][W] bytes, nullable: a beam with a non-zero byte only continues with
  *               eos_token, its score unchanged
- *   scores [N][k] fp32, parents and tokens [N][k] int32: outputs
+ *   scores [N][k] fp32, parents and tokens [N][k] int32: outputs (scores may be cum_scores itself
+ *   where k == W)
  * Exponentials and a lane's sums are 32-bit, the rest 64-bit, scores rounded once to fp32: candidates
  * of different beams whose scores agree to about 1e-6 may come in either order (beams with equal
  * logits tie exactly).  A beam whose logits hold a NaN or +inf, or nothing but -inf, has no candidate
  * above -inf.  Candidates at -inf rank by index.
- * 1 <= k <= 32, k <= W * V, W * V < 2^31.  The parents are what pa_alloc_beam_select takes
+ * 1 <= k <= 32, k <= W * V, V <= 2^30, W * V < 2^31.  The parents are what pa_alloc_beam_select takes
  * (k == W).  Workspace as pa_beam_topk_workspace_size, 256-byte aligned, no initialisation;
  * not shared by calls that may overlap. */
 size_t pa_beam_topk_workspace_size(int N, int W, int V, int k);

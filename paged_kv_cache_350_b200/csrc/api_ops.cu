@@ -17,6 +17,12 @@ bool block_size_ok(int bs) { return bs == 4 || bs == 8 || bs == 16 || bs == 32; 
 bool dtype_ok(pa_dtype t) { return t == PA_F32 || t == PA_BF16; }
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
+// Whether [a, a + an) and [b, b + bn) bytes overlap.
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uint64_t>(bn) && y < x + static_cast<uint64_t>(an);
+}
+
 // CTAs assumed per launch when no device can be asked.
 constexpr int kSmBound = 256;
 
@@ -178,7 +184,10 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, const void* k, const voi
       !aligned(inv_freq, 8) || (dev_err_flag && !aligned(dev_err_flag, 4)))
     return PA_ERR_INVALID_ARG;
   // in place only where every thread reads what it writes
-  if (q_out == q && q_stride != static_cast<int64_t>(Hq) * D) return PA_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(Hq) * D;
+  if (!(q_out == q && (q_stride == row || T == 1)) &&
+      overlap(q_out, T * row * esize, q, ((T - 1) * q_stride + row) * esize))
+    return PA_ERR_INVALID_ARG;
   pa::RopeParams p{};
   p.q_out = q_out;
   p.q = q;
@@ -228,9 +237,11 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
   const pa_attention_mods none{};
   const pa_attention_mods& m = mods ? *mods : none;
   if (!attention_sizes_ok(T, B, max_query_len, Hq, Hkv) || max_blocks <= 0 || num_blocks <= 0 ||
-      block_size <= 0 || !std::isfinite(scale) || !dtype_ok(dtype) || !(m.softcap >= 0.f) ||
-      !std::isfinite(m.softcap) || m.window < 0)
+      block_size <= 0 || !(std::fabs(scale) <= 1e30f) || !dtype_ok(dtype) || m.window < 0 ||
+      !(m.softcap == 0.f || (m.softcap >= 1e-30f && m.softcap <= 1e30f)))
     return PA_ERR_INVALID_ARG;
+  // (scale / softcap is held in 32 bits)
+  if (m.softcap > 0.f && !(std::fabs(static_cast<double>(scale) / m.softcap) <= 1e30)) return PA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return PA_ERR_UNSUPPORTED;
   if (!block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
   const int64_t max_seq = static_cast<int64_t>(max_blocks) * block_size;
@@ -246,6 +257,9 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
       (m.alibi_slopes && !aligned(m.alibi_slopes, 4)) || (m.prefix_lens && !aligned(m.prefix_lens, 4)) ||
       (m.first_keys && !aligned(m.first_keys, 4)))
     return PA_ERR_INVALID_ARG;
+  // (a unit's output may be written before another one has read its queries)
+  const int64_t row = static_cast<int64_t>(Hq) * D;
+  if (overlap(out, T * row * esize, q, ((T - 1) * q_stride + row) * esize)) return PA_ERR_INVALID_ARG;
   const int sms = pa::device_sms();
   if (sms <= 0) return PA_ERR_CUDA;
   const int G = Hq / Hkv;
@@ -308,8 +322,8 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
 }
 
 static bool beam_sizes_ok(int N, int W, int V, int k) {
-  return N >= 0 && W > 0 && V > 0 && k > 0 && static_cast<int64_t>(W) * V < (int64_t(1) << 31) &&
-         k <= static_cast<int64_t>(W) * V;
+  return N >= 0 && W > 0 && V > 0 && V <= (1 << 30) && k > 0 &&
+         static_cast<int64_t>(W) * V < (int64_t(1) << 31) && k <= static_cast<int64_t>(W) * V;
 }
 
 size_t pa_beam_topk_workspace_size(int N, int W, int V, int k) {
@@ -336,6 +350,10 @@ pa_status pa_beam_topk(float* scores, int32_t* parents, int32_t* tokens, const v
   if (!scores || !parents || !tokens || !logits || !cum_scores || !workspace) return PA_ERR_INVALID_ARG;
   if (!aligned(scores, 4) || !aligned(parents, 4) || !aligned(tokens, 4) ||
       !aligned(logits, dtype == PA_BF16 ? 2 : 4) || !aligned(cum_scores, 4) || !aligned(workspace, 256))
+    return PA_ERR_INVALID_ARG;
+  // a request's scores so far are read before its new ones are written
+  if (!(scores == cum_scores && k == W) &&
+      overlap(scores, static_cast<int64_t>(N) * k * 4, cum_scores, static_cast<int64_t>(N) * W * 4))
     return PA_ERR_INVALID_ARG;
   pa::BeamParams p{};
   p.scores = scores;
@@ -364,9 +382,8 @@ pa_status pa_beam_gather(void* dst, const void* src, const int32_t* parents, int
   if (N == 0 || row_bytes == 0) return PA_OK;
   if (!dst || !src || !parents || !aligned(parents, 4) || (dev_err_flag && !aligned(dev_err_flag, 4)))
     return PA_ERR_INVALID_ARG;
-  const char *d = static_cast<const char*>(dst), *s = static_cast<const char*>(src);
-  if (d < s + static_cast<int64_t>(N) * W * row_bytes && s < d + static_cast<int64_t>(N) * k * row_bytes)
-    return PA_ERR_INVALID_ARG;  // overlap
+  if (overlap(dst, static_cast<int64_t>(N) * k * row_bytes, src, static_cast<int64_t>(N) * W * row_bytes))
+    return PA_ERR_INVALID_ARG;
   return pa::launch_beam_gather(dst, src, parents, N, W, k, row_bytes, dev_err_flag,
                                 reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

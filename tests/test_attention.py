@@ -167,7 +167,7 @@ def test_workspace_size_and_refusals():
     p = 0x10000
 
     def call(T=4, B_=2, most=2, Hq=4, Hkv=2, D=64, bs=16, MB=4, NB=8, stride=256, scale=0.125, mods=None, dt=B.PA_BF16,
-             out=p, q=p, ws=p, wbytes=1 << 40, tables=p):
+             out=p, q=0x20000, ws=p, wbytes=1 << 40, tables=p):
         return B.lib.pa_attention(out, q, p, p, tables, p, p, T, B_, most, Hq, Hkv, D, bs, MB, NB, stride, scale,
                                   mods, dt, ws, wbytes, None, None)
     M = B.pa_attention_mods
@@ -175,7 +175,8 @@ def test_workspace_size_and_refusals():
                 dict(scale=NAN), dict(dt=5), dict(stride=255), dict(stride=260), dict(mods=M(-1.0)), dict(mods=M(NAN)),
                 dict(mods=M(0.0, -1)), dict(out=None), dict(q=0x10008), dict(ws=0x10010), dict(ws=None),
                 dict(tables=None), dict(mods=M(0.0, 0, 0x1002)), dict(mods=M(0.0, 0, None, 0x1002)),
-                dict(mods=M(0.0, 0, None, None, 0x1002))):
+                dict(mods=M(0.0, 0, None, None, 0x1002)), dict(scale=1e31), dict(mods=M(1e-31)), dict(mods=M(1e31)),
+                dict(scale=10.0, mods=M(1e-30)), dict(out=0x20000), dict(out=0x207f0), dict(out=0x1f810)):
         assert call(**bad) == B.PA_ERR_INVALID_ARG, bad
     for bad in (dict(D=80, stride=320), dict(bs=64)):
         assert call(**bad) == B.PA_ERR_UNSUPPORTED, bad

@@ -65,7 +65,7 @@ def random_case(N, W, V, dtype, seed, spread=3.0):
 
 def test_sizes_and_refusals():
     for a in ((-1, 1, 10, 1), (1, 0, 10, 1), (1, 1, 0, 1), (1, 1, 10, 0), (1, 1, 10, 11), (1, 2, 100, 33),
-              (1, 1 << 16, 1 << 15, 1)):
+              (1, 1 << 16, 1 << 15, 1), (1, 1, (1 << 30) + 1, 1)):
         with pytest.raises(pa.PAError):
             pa.pa_beam_topk_workspace_size(*a)
     assert pa.pa_beam_topk_workspace_size(0, 4, 100, 4) == 0
@@ -73,10 +73,11 @@ def test_sizes_and_refusals():
 
     p = 0x1000
 
-    def call(N=2, W=2, V=64, k=2, stride=64, dt=B.PA_F32, ws=1 << 20, eos=0, fin=None, wsp=p, x=p):
-        return B.lib.pa_beam_topk(p, p, p, x, p, fin, eos, N, W, V, k, stride, dt, wsp, ws, None)
+    def call(N=2, W=2, V=64, k=2, stride=64, dt=B.PA_F32, ws=1 << 20, eos=0, fin=None, wsp=p, x=p, cum=0x8000):
+        return B.lib.pa_beam_topk(p, p, p, x, cum, fin, eos, N, W, V, k, stride, dt, wsp, ws, None)
     for bad in (dict(N=-1), dict(W=0), dict(V=0), dict(k=0), dict(k=129), dict(stride=63), dict(dt=9), dict(ws=10),
-                dict(wsp=None), dict(wsp=0x1010), dict(x=0x1002), dict(fin=p, eos=64), dict(fin=p, eos=-1)):
+                dict(wsp=None), dict(wsp=0x1010), dict(x=0x1002), dict(fin=p, eos=64), dict(fin=p, eos=-1),
+                dict(cum=p, k=3), dict(cum=p + 4), dict(cum=p - 12)):
         assert call(**bad) == B.PA_ERR_INVALID_ARG, bad
     assert call(k=33) == B.PA_ERR_UNSUPPORTED
     assert call(N=0) == B.PA_OK
@@ -240,3 +241,15 @@ def test_topk_in_a_graph_follows_its_inputs():
         torch.cuda.synchronize()
         _, rp, rt = reference(y, cum2, 4)
         assert torch.equal(p.cpu(), rp) and torch.equal(t.cpu(), rt)
+
+
+@pytest.mark.gpu
+def test_topk_writes_over_the_scores_so_far():
+    x, cum = random_case(5, 3, 9000, torch.float32, 12)
+    d, c = x.cuda(), cum.cuda()
+    ws = torch.empty(pa.pa_beam_topk_workspace_size(5, 3, 9000, 3), dtype=torch.uint8, device="cuda")
+    s = torch.empty(5, 3, device="cuda")
+    p, t, p2, t2 = (torch.empty(5, 3, dtype=torch.int32, device="cuda") for _ in range(4))
+    pa.pa_beam_topk(s, p, t, d, c, workspace=ws)
+    pa.pa_beam_topk(c, p2, t2, d, c, workspace=ws)
+    assert torch.equal(s, c) and torch.equal(p, p2) and torch.equal(t, t2)

@@ -100,7 +100,7 @@ def test_rope_refusals_on_the_host():
                                        a["dt"], None, None)
     for bad in (dict(T=-1), dict(Hq=0), dict(Hkv=0), dict(NB=0), dict(R=0), dict(R=63), dict(R=66), dict(layout=2),
                 dict(f=float("nan")), dict(dt=7), dict(qs=255), dict(ks=127), dict(vs=0), dict(q_out=None),
-                dict(q_out=0x1001), dict(q_out=0x2000, qs=512)):
+                dict(q_out=0x1001), dict(q_out=0x2000, qs=512), dict(q_out=0x2010), dict(q_out=0x1810)):
         assert call(**bad) == B.PA_ERR_INVALID_ARG, bad
     for bad in (dict(D=96), dict(bs=5)):
         assert call(**bad) == B.PA_ERR_UNSUPPORTED, bad
