@@ -592,6 +592,23 @@ class Allocator:
                                         ctypes.byref(dst)), "pa_alloc_append_slot")
         return slot.value, src.value, dst.value
 
+    def append_tokens(self, seq_id, n):
+        """append_slot n times; (slots int64[n], copy pairs).  Where the pool runs out, the tokens so
+        far stay and the pairs are on the error (``pairs``)."""
+        slot, src, dst = ctypes.c_int64(), ctypes.c_int32(-1), ctypes.c_int32(-1)
+        args = (self._h, seq_id, ctypes.byref(slot), ctypes.byref(src), ctypes.byref(dst))
+        slots, pairs, append = np.empty(n, np.int64), [], lib.pa_alloc_append_slot
+        for i in range(n):
+            st = append(*args)
+            if st:
+                e = PAError(st, "pa_alloc_append_slot")
+                e.pairs = pairs
+                raise e
+            slots[i] = slot.value
+            if src.value >= 0:
+                pairs.append((src.value, dst.value))
+        return slots, pairs
+
     def append_slots(self, seq_ids, slot_out=None, pairs_out=None):
         """append_slot for every id, all or nothing; returns (slots int64[n], pairs int32[k,2])."""
         ids = np.ascontiguousarray(seq_ids, dtype=np.int64)

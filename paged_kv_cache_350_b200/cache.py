@@ -283,10 +283,11 @@ class PagedKVCache:
         return self._out_h, (used, self._out_h.numel() * self._out_h.element_size())
 
     # -- prompts, chunks and single tokens, device tensors in and out --------------------
-    def _append_tokens(self, seq_ids, query_lens):
-        """Slots of query_lens[b] more tokens of every sequence (a new one is registered), all or
-        nothing; returns (slots int64 [T], positions int32 [T], copy pairs)."""
-        slots, positions, pairs, grown = [], [], [], []
+    def _append_tokens(self, seq_ids, query_lens, grown):
+        """Slots of query_lens[b] more tokens of every sequence (a new one is registered); returns
+        (slots int64 [T], positions int32 [T]).  A shared last block that is written is copied.  What
+        `_take_back` needs is appended to `grown`."""
+        slots, positions, pairs = [np.empty(0, np.int64)], [np.empty(0, np.int32)], []
         try:
             for sid, n in zip(seq_ids, query_lens):
                 try:
@@ -296,31 +297,33 @@ class PagedKVCache:
                         raise
                     self.alloc.add_seq(sid, n)
                     grown.append((sid, None))
-                    slots.extend(self.alloc.seq_slots(sid).tolist())
-                    positions.extend(range(n))
+                    slots.append(self.alloc.seq_slots(sid))
+                    positions.append(np.arange(n, dtype=np.int32))
                     continue
                 grown.append((sid, have))
-                for i in range(n):
-                    slot, src, dst = self.alloc.append_slot(sid)
-                    slots.append(slot)
-                    if src >= 0:
-                        pairs.append((src, dst))
-                positions.extend(range(have, have + n))
-        except _b.PAError:
-            for sid, have in reversed(grown):
-                if have is None:
-                    self.alloc.free_seq(sid)
-                else:
-                    self.alloc.truncate(sid, have)
-            # a shared last block that was to be written is the sequence's own now: it keeps its tokens
-            self._copy_pairs(pairs)
+                new, copies = self.alloc.append_tokens(sid, n)
+                slots.append(new)
+                pairs += copies
+                positions.append(np.arange(have, have + n, dtype=np.int32))
+        except _b.PAError as e:
+            pairs += getattr(e, "pairs", [])
             raise
-        return slots, positions, pairs
+        finally:
+            # (after an error as well: the copied block is the sequence's own now and keeps its tokens)
+            self._copy_pairs(pairs)
+        return np.concatenate(slots), np.concatenate(positions)
 
-    def _copy_pairs(self, pairs, stream=None):
+    def _take_back(self, grown):
+        for sid, have in reversed(grown):
+            if have is None:
+                self.alloc.free_seq(sid)
+            else:
+                self.alloc.truncate(sid, have)
+
+    def _copy_pairs(self, pairs):
         if pairs:
             d = torch.tensor(pairs, dtype=torch.int32).to(self.device)
-            _b.pa_copy_blocks(self.k_pool, self.v_pool, d, err_flag=self.err, stream=stream)
+            _b.pa_copy_blocks(self.k_pool, self.v_pool, d, err_flag=self.err)
 
     def extend(self, seq_ids, query_lens, q, k, v, scale, inv_freq=None, layout=_b.PA_ROPE_HALF,
                attn_factor=1.0, softcap=0.0, alibi_slopes=None, window=0, prefix_lens=None,
@@ -333,7 +336,7 @@ class PagedKVCache:
         (float64 device tensor, ``pa_rope_frequencies``) q and k are rotated by the tokens'
         positions first.  softcap, alibi_slopes, window, prefix_lens and first_keys as in
         ``pa_attention`` (device tensors).  Copy on write as in ``step``.  Returns out [T,Hq,D];
-        the work is queued on the stream.
+        the work is queued on the stream.  A call that raises leaves every sequence as it was.
         """
         lens = [int(n) for n in query_lens]
         ids = [int(i) for i in seq_ids]
@@ -351,36 +354,49 @@ class PagedKVCache:
         if inv_freq is not None and not (inv_freq.dtype == torch.float64 and inv_freq.dim() == 1
                                          and 1 <= inv_freq.numel() <= D // 2):
             raise ValueError("extend: inv_freq float64 [rotary_dim / 2]")
-        if T == 0:
-            return out if out is not None else torch.empty_like(q)
+        if out is not None and not (out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()):
+            raise ValueError("extend: out must be contiguous, of q's shape and dtype")
         stream = stream or torch.cuda.current_stream(self.device)
-        B = len(ids)
-        with torch.cuda.device(self.device), torch.cuda.stream(stream):
-            slots, positions, pairs = self._append_tokens(ids, lens)
+        grown = []
+        try:
+            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                return self._extend(ids, lens, q, k, v, scale, inv_freq, layout, attn_factor, softcap, alibi_slopes,
+                                    window, prefix_lens, first_keys, out, stream, grown)
+        except BaseException:
+            self._take_back(grown)
+            raise
+
+    def _extend(self, ids, lens, q, k, v, scale, inv_freq, layout, attn_factor, softcap, alibi_slopes, window,
+                prefix_lens, first_keys, out, stream, grown):
+        (T, Hq, D), B = q.shape, len(ids)
+        slots, positions = self._append_tokens(ids, lens, grown)
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
+        if T > 0:
             MB = max(1, max(-(-self.alloc.block_table(i)[1] // self.block_size) for i in ids))
             tables, seq_lens = self.alloc.block_tables(ids, MB)
             # everything of the step in one copy (the host array is staged before the call returns)
-            ints = np.concatenate([np.asarray(positions, np.int32), seq_lens,
-                                   np.concatenate([[0], np.cumsum(lens)]).astype(np.int32), tables.ravel()])
-            host = np.concatenate([np.asarray(slots, np.int64).view(np.int32), ints])
+            ints = np.concatenate([positions, seq_lens, np.concatenate([[0], np.cumsum(lens)]).astype(np.int32),
+                                   tables.ravel()])
+            host = np.concatenate([slots.view(np.int32), ints])
             dev = torch.from_numpy(host).to(self.device)
             slots_d, at = dev[:2 * T].view(torch.int64), 2 * T
             pos_d, lens_d, starts_d, tables_d = (dev[at:at + T], dev[at + T:at + T + B],
                                                  dev[at + T + B:at + T + 2 * B + 1], dev[at + T + 2 * B + 1:])
-            self._copy_pairs(pairs, stream)
             if inv_freq is None:
                 _b.pa_reshape_and_cache(k.contiguous(), v.contiguous(), self.k_pool, self.v_pool, slots_d,
                                         err_flag=self.err, stream=stream)
-                qr = q if q.stride(2) == 1 and q.stride(1) == D else q.contiguous()
+                # as it lies, where the attention can read it so
+                lies = (q.stride(2) == 1 and q.stride(1) == D and q.stride(0) >= Hq * D
+                        and q.stride(0) * q.element_size() % 16 == 0 and q.data_ptr() % 16 == 0)
+                qr = q if lies else q.clone(memory_format=torch.contiguous_format)
             else:
                 qr = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
-                _b.pa_rope_and_cache(qr, q, k, v, self.k_pool, self.v_pool, pos_d.contiguous(), slots_d, inv_freq,
-                                     layout=layout, attn_factor=attn_factor, err_flag=self.err, stream=stream)
+                _b.pa_rope_and_cache(qr, q, k, v, self.k_pool, self.v_pool, pos_d, slots_d, inv_freq, layout=layout,
+                                     attn_factor=attn_factor, err_flag=self.err, stream=stream)
             most = max(lens)
             n = _b.pa_attention_workspace_size(T, B, most, Hq, self.Hkv, D, self.block_size, MB)
             ws = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
-            if out is None:
-                out = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
             _b.pa_attention(out, qr, self.k_pool, self.v_pool, tables_d.view(B, MB), lens_d, starts_d, most, scale,
                             softcap=softcap, alibi_slopes=alibi_slopes, window=window, prefix_lens=prefix_lens,
                             first_keys=first_keys, workspace=ws, err_flag=self.err, stream=stream)

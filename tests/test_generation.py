@@ -127,7 +127,30 @@ def test_extend_is_all_or_nothing():
         cache.extend([0], [3], q.bfloat16(), k, v, 0.1)
     with pytest.raises(ValueError):
         cache.extend([0], [3], q, k, v, 0.1, inv_freq=torch.ones(40, dtype=torch.float64, device="cuda"))
-    assert cache.alloc.num_free() == free
+    # refused by the calls themselves, after the tokens had their slots
+    inv = torch.ones(16, dtype=torch.float64, device="cuda")
+    for kw in (dict(window=-1), dict(softcap=-1.0), dict(alibi_slopes=torch.ones(HQ + 1, device="cuda")),
+               dict(out=torch.empty(3, HQ + 1, D, device="cuda")), dict(inv_freq=inv, layout=7)):
+        with pytest.raises((ValueError, pa.PAError)):
+            cache.extend([0, 7], [2, 1], q, k, v, 0.1, **kw)
+        assert cache.alloc.block_table(0)[1] == 12
+        with pytest.raises(pa.PAError):
+            cache.alloc.block_table(7)
+    with pytest.raises(ValueError):
+        cache.extend([0], [3], q, k.transpose(0, 1).contiguous().transpose(0, 1), v, 0.1, inv_freq=inv)
+    assert cache.alloc.block_table(0)[1] == cache.alloc.block_table(1)[1] == 12
+    assert cache.alloc.num_free() >= free - 1  # (a shared block may have become two)
+    torch.cuda.synchronize()
+    for sid in (0, 1):
+        slots = torch.from_numpy(cache.alloc.seq_slots(sid)).cuda()
+        assert torch.equal(cache.v_pool.view(-1, HKV, D)[slots], first[2])
+    # queries that do not lie as the attention reads them are copied
+    odd = torch.zeros(3 * HQ * D + 1, device="cuda")[1:].view(3, HQ, D).copy_(q)
+    a = cache.extend([0], [3], odd, k, v, 0.1)
+    cache.truncate(0, 12)
+    b = cache.extend([0], [3], q, k, v, 0.1)
+    assert torch.equal(a, b)
+    cache.truncate(0, 12)
     assert cache.extend([0], [0], q[:0], k[:0], v[:0], 0.1).shape == (0, HQ, D)
     cache.check_device_errors()
 
