@@ -481,6 +481,10 @@ pa_status pa_alloc_append_slot(pa_allocator* a, int64_t seq_id, int64_t* slot,
  * for n pairs) and their count to *n_pairs. */
 pa_status pa_alloc_append_slots(pa_allocator* a, const int64_t* seq_ids, int n,
                                 int64_t* slot_mapping, int32_t* cow_pairs, int* n_pairs);
+/* append_slot n times for one sequence (a chunk of a prompt), all or nothing: slots[n], and the
+ * one copy there can be (of a shared last block) or -1. */
+pa_status pa_alloc_append_tokens(pa_allocator* a, int64_t seq_id, int n, int64_t* slots,
+                                 int32_t* cow_src, int32_t* cow_dst);
 /* Drop a sequence; blocks whose refcount reaches 0 return to the free list. */
 pa_status pa_alloc_free_seq(pa_allocator* a, int64_t seq_id);
 /* Keep only the first num_tokens tokens (0 <= num_tokens <= current count), e.g. to roll

@@ -161,6 +161,7 @@ def _load():
         "pa_alloc_fork": (i32, [vp, i64, i64]),
         "pa_alloc_append_slot": (i32, [vp, i64, pi64, pi32, pi32]),
         "pa_alloc_append_slots": (i32, [vp, pi64, i32, pi64, pi32, pint]),
+        "pa_alloc_append_tokens": (i32, [vp, i64, i32, pi64, pi32, pi32]),
         "pa_alloc_free_seq": (i32, [vp, i64]),
         "pa_alloc_truncate": (i32, [vp, i64, i32]),
         "pa_alloc_beam_select": (i32, [vp, pi64, pi32, i32]),
@@ -201,7 +202,8 @@ EXPORTED = (
     "pa_attention_workspace_size", "pa_attention", "pa_beam_topk_workspace_size", "pa_beam_topk",
     "pa_beam_gather", "pa_selftest_bounded_wait", "pa_alloc_create",
     "pa_alloc_create_ordered", "pa_alloc_destroy", "pa_alloc_add_seq", "pa_alloc_fork",
-    "pa_alloc_append_slot", "pa_alloc_append_slots", "pa_alloc_free_seq", "pa_alloc_truncate",
+    "pa_alloc_append_slot", "pa_alloc_append_slots", "pa_alloc_append_tokens", "pa_alloc_free_seq",
+    "pa_alloc_truncate",
     "pa_alloc_beam_select", "pa_alloc_block_table",
     "pa_alloc_block_tables", "pa_alloc_seq_slots", "pa_alloc_refcount", "pa_alloc_num_free",
     "pa_alloc_internal_waste_slots", "pa_alloc_free_list", "pa_alloc_check_append_fits",
@@ -593,21 +595,11 @@ class Allocator:
         return slot.value, src.value, dst.value
 
     def append_tokens(self, seq_id, n):
-        """append_slot n times; (slots int64[n], copy pairs).  Where the pool runs out, the tokens so
-        far stay and the pairs are on the error (``pairs``)."""
-        slot, src, dst = ctypes.c_int64(), ctypes.c_int32(-1), ctypes.c_int32(-1)
-        args = (self._h, seq_id, ctypes.byref(slot), ctypes.byref(src), ctypes.byref(dst))
-        slots, pairs, append = np.empty(n, np.int64), [], lib.pa_alloc_append_slot
-        for i in range(n):
-            st = append(*args)
-            if st:
-                e = PAError(st, "pa_alloc_append_slot")
-                e.pairs = pairs
-                raise e
-            slots[i] = slot.value
-            if src.value >= 0:
-                pairs.append((src.value, dst.value))
-        return slots, pairs
+        """append_slot n times, all or nothing; returns (slots int64[n], copy pairs: none or one)."""
+        slots, src, dst = np.empty(max(n, 1), dtype=np.int64), ctypes.c_int32(), ctypes.c_int32()
+        _check(lib.pa_alloc_append_tokens(self._h, seq_id, n, _i64p(slots), ctypes.byref(src), ctypes.byref(dst)),
+               "pa_alloc_append_tokens")
+        return slots[:n], [(src.value, dst.value)] if src.value >= 0 else []
 
     def append_slots(self, seq_ids, slot_out=None, pairs_out=None):
         """append_slot for every id, all or nothing; returns (slots int64[n], pairs int32[k,2])."""

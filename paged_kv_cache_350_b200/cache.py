@@ -305,9 +305,6 @@ class PagedKVCache:
                 slots.append(new)
                 pairs += copies
                 positions.append(np.arange(have, have + n, dtype=np.int32))
-        except _b.PAError as e:
-            pairs += getattr(e, "pairs", [])
-            raise
         finally:
             # (after an error as well: the copied block is the sequence's own now and keeps its tokens)
             self._copy_pairs(pairs)

@@ -238,6 +238,31 @@ pa_status append_slots_impl(pa_allocator* a, const int64_t* seq_ids, int n,
   return PA_OK;
 }
 
+pa_status append_tokens_impl(pa_allocator* a, int64_t seq_id, int n, int64_t* slots,
+                             int32_t* cow_src, int32_t* cow_dst) {
+  if (!a || n < 0 || (n > 0 && !slots) || !cow_src || !cow_dst) return PA_ERR_INVALID_ARG;
+  auto it = a->seqs.find(seq_id);
+  if (it == a->seqs.end()) return PA_ERR_NOT_FOUND;
+  Seq& s = it->second;
+  const int64_t bs = a->block_size, off = s.ntok % bs;
+  if (s.ntok + n > INT32_MAX) return PA_ERR_INVALID_ARG;
+  const int64_t fresh = (s.ntok + n + bs - 1) / bs - static_cast<int64_t>(s.table.size());
+  const bool copies = n > 0 && off != 0 && a->ref[s.table.back()] > 1;
+  if (fresh + copies > static_cast<int64_t>(a->free_stack.size())) return PA_ERR_OUT_OF_BLOCKS;
+  const size_t size = s.table.size() + static_cast<size_t>(fresh);
+  if (size > s.table.capacity()) s.table.reserve(std::max(size, 2 * s.table.capacity()));
+  *cow_src = *cow_dst = -1;
+  for (int i = 0; i < n; ++i) {  // only the first can find a shared block
+    int32_t src, dst;
+    append_one(a, s, &slots[i], &src, &dst);
+    if (src >= 0) {
+      *cow_src = src;
+      *cow_dst = dst;
+    }
+  }
+  return PA_OK;
+}
+
 // free_stack holds every block at creation, so its capacity covers all pushes: freeing
 // never allocates.
 pa_status free_seq_impl(pa_allocator* a, int64_t seq_id) {
@@ -379,6 +404,11 @@ pa_status pa_alloc_append_slots(pa_allocator* a, const int64_t* seq_ids, int n,
                                 int64_t* slot_mapping, int32_t* cow_pairs, int* n_pairs) {
   return guarded(
       [&] { return append_slots_impl(a, seq_ids, n, slot_mapping, cow_pairs, n_pairs); });
+}
+
+pa_status pa_alloc_append_tokens(pa_allocator* a, int64_t seq_id, int n, int64_t* slots,
+                                 int32_t* cow_src, int32_t* cow_dst) {
+  return guarded([&] { return append_tokens_impl(a, seq_id, n, slots, cow_src, cow_dst); });
 }
 
 pa_status pa_alloc_free_seq(pa_allocator* a, int64_t seq_id) {

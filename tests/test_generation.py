@@ -63,6 +63,28 @@ def close(got, ref):
     assert bool(((got.cpu().double() - out).abs() <= tol).all()), float(((got.cpu().double() - out).abs() / tol).max())
 
 
+@pytest.mark.parametrize("have,n,shared", [(0, 0, False), (0, 1, False), (5, 3, False), (5, 3, True), (8, 17, True),
+                                           (7, 40, True), (3, 0, True)])
+def test_append_tokens_is_append_slot_repeated(have, n, shared):
+    one, many = pa.Allocator(12, 8, shuffle_seed=4), pa.Allocator(12, 8, shuffle_seed=4)
+    for a in (one, many):
+        a.add_seq(1, have)
+        if shared:
+            a.fork(1, 2)
+    steps = [one.append_slot(1) for _ in range(n)]
+    slots, pairs = many.append_tokens(1, n)
+    assert slots.tolist() == [s for s, _, _ in steps]
+    assert pairs == [(s, d) for _, s, d in steps if s >= 0]
+    assert one.block_table(1) == many.block_table(1) and one.free_list() == many.free_list()
+    before = many.block_table(1), many.free_list()
+    for seq, count, status in ((1, 12 * 8 + 1, B.PA_ERR_OUT_OF_BLOCKS), (1, -1, B.PA_ERR_INVALID_ARG),
+                               (9, 1, B.PA_ERR_NOT_FOUND)):
+        with pytest.raises(pa.PAError) as e:
+            many.append_tokens(seq, count)
+        assert e.value.status == status
+    assert (many.block_table(1), many.free_list()) == before
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_prompts_forks_chunks_and_single_tokens(dtype):
