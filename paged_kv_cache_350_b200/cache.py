@@ -60,6 +60,7 @@ class PagedKVCache:
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._ws = None
         self._staging = {}
+        self._table_blocks = 16  # of extend's next block tables, at first
 
     # -- host buffers ------------------------------------------------------------
     def _pinned(self, key, shape, dtype):
@@ -284,38 +285,57 @@ class PagedKVCache:
 
     # -- prompts, chunks and single tokens, device tensors in and out --------------------
     def _append_tokens(self, seq_ids, query_lens, grown):
-        """Slots of query_lens[b] more tokens of every sequence (a new one is registered); returns
-        (slots int64 [T], positions int32 [T]).  A shared last block that is written is copied.  What
-        `_take_back` needs is appended to `grown`."""
-        slots, positions, pairs = [np.empty(0, np.int64)], [np.empty(0, np.int32)], []
+        """Slots (int64 [T]) of query_lens[b] more tokens of every sequence; a new one is registered,
+        and a shared last block that is written is copied.  What `_take_back` needs is appended to
+        `grown`."""
+        if all(n == 1 for n in query_lens):  # a step of single tokens: one call
+            try:
+                slots, pairs = self.alloc.append_slots(seq_ids)
+                grown.extend((sid, 1) for sid in seq_ids)
+                self._copy_pairs(pairs.tolist())
+                return slots
+            except _b.PAError as e:
+                if e.status != _b.PA_ERR_NOT_FOUND:
+                    raise
+        slots, pairs = [np.empty(0, np.int64)], []
         try:
             for sid, n in zip(seq_ids, query_lens):
                 try:
-                    _, have = self.alloc.block_table(sid)
+                    new, copies = self.alloc.append_tokens(sid, n)
+                    grown.append((sid, n))
+                    pairs += copies
                 except _b.PAError as e:
                     if e.status != _b.PA_ERR_NOT_FOUND:
                         raise
                     self.alloc.add_seq(sid, n)
                     grown.append((sid, None))
-                    slots.append(self.alloc.seq_slots(sid))
-                    positions.append(np.arange(n, dtype=np.int32))
-                    continue
-                grown.append((sid, have))
-                new, copies = self.alloc.append_tokens(sid, n)
+                    new = self.alloc.seq_slots(sid)
                 slots.append(new)
-                pairs += copies
-                positions.append(np.arange(have, have + n, dtype=np.int32))
         finally:
             # (after an error as well: the copied block is the sequence's own now and keeps its tokens)
             self._copy_pairs(pairs)
-        return np.concatenate(slots), np.concatenate(positions)
+        return np.concatenate(slots)
 
     def _take_back(self, grown):
-        for sid, have in reversed(grown):
-            if have is None:
+        for sid, n in reversed(grown):
+            if n is None:
                 self.alloc.free_seq(sid)
             else:
-                self.alloc.truncate(sid, have)
+                self.alloc.truncate(sid, self.alloc.block_table(sid)[1] - n)
+
+    def _tables(self, seq_ids):
+        """Block tables, as wide as the longest sequence needs, and lengths of live sequences."""
+        while True:
+            try:
+                tables, lens = self.alloc.block_tables(seq_ids, self._table_blocks)
+            except _b.PAError as e:  # wider than the last ones
+                if e.status != _b.PA_ERR_INVALID_ARG or self._table_blocks >= self.k_pool.shape[0]:
+                    raise
+                self._table_blocks = min(2 * self._table_blocks, self.k_pool.shape[0])
+                continue
+            blocks = max(1, -(-int(lens.max()) // self.block_size))
+            self._table_blocks = blocks + 1
+            return tables[:, :blocks], lens
 
     def _copy_pairs(self, pairs):
         if pairs:
@@ -366,16 +386,16 @@ class PagedKVCache:
     def _extend(self, ids, lens, q, k, v, scale, inv_freq, layout, attn_factor, softcap, alibi_slopes, window,
                 prefix_lens, first_keys, out, stream, grown):
         (T, Hq, D), B = q.shape, len(ids)
-        slots, positions = self._append_tokens(ids, lens, grown)
+        slots = self._append_tokens(ids, lens, grown)
         if out is None:
             out = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
         if T > 0:
-            MB = max(1, max(-(-self.alloc.block_table(i)[1] // self.block_size) for i in ids))
-            tables, seq_lens = self.alloc.block_tables(ids, MB)
+            tables, seq_lens = self._tables(ids)
+            MB = tables.shape[1]
+            starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+            positions = np.arange(T, dtype=np.int32) + np.repeat(seq_lens - starts[1:], lens)
             # everything of the step in one copy (the host array is staged before the call returns)
-            ints = np.concatenate([positions, seq_lens, np.concatenate([[0], np.cumsum(lens)]).astype(np.int32),
-                                   tables.ravel()])
-            host = np.concatenate([slots.view(np.int32), ints])
+            host = np.concatenate([slots.view(np.int32), positions, seq_lens, starts, tables.ravel()])
             dev = torch.from_numpy(host).to(self.device)
             slots_d, at = dev[:2 * T].view(torch.int64), 2 * T
             pos_d, lens_d, starts_d, tables_d = (dev[at:at + T], dev[at + T:at + T + B],
