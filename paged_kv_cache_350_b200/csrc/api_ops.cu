@@ -294,6 +294,11 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
     for (int k = 0; k < 5; ++k) p.cap_poly[k] = static_cast<float>(kTanh[k] * m.softcap * log2e * std::pow(ci, 2 * k + 1));
     const bool usable = std::fabs(ci) >= 1e-3 && std::fabs(ci) <= 1e3 && m.softcap >= 1e-6f && m.softcap <= 1e6f;
     p.cap_small = usable ? static_cast<float>(std::fabs(ci)) : INFINITY;
+    // One reference for all scores within +-cap_out: their weights lie in 2^(top - 2 cap_out) ..
+    // 2^top, so top is as low as keeps the smallest above 2^-80, at most 40; inf: none would keep it
+    // above 2^-105 (products with V and their sums are to stay normal numbers).
+    const float top = std::min(std::max(2.f * p.cap_out - 80.f, 8.f), 40.f);
+    p.cap_ref = 2.f * p.cap_out - top <= 105.f ? p.cap_out - top : INFINITY;
   }
   p.window = m.window;
   p.T = T;

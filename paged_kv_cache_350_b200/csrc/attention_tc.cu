@@ -12,19 +12,22 @@
 // follow.  K and V tiles share a ring of slots in load order (K0 V0 K1 V1 ..), one TMA box per
 // block and 64-column chunk.
 //
-// Tensor memory: S_g at column 128 g, overwritten by its P (bf16 pairs, 64 columns); O_g at
-// column 256 + 128 g.  Products are issued by one thread and run in order, so S_g of the next tile
-// is issued right behind the P.V that reads P_g.  While group 0 works on its S, the products of
-// group 1 run and the other way round.
+// Tensor memory: S_g at column 128 g in two halves of 64 keys, each overwritten by its P (bf16
+// pairs, 32 columns); O_g at column 256 + 128 g.  Products are issued by one thread and run in
+// order, so the next tile's half of S_g is issued right behind the P.V that reads the same half of
+// P_g, and is computed while the softmax works on the other half (S of whole tiles, behind both
+// halves of P.V: 327 us for 305).  While group 0 works on its S, the products of group 1 run and the
+// other way round.
 //
 // Bound by the softmax: 16 exponentials a cycle and SM take as long as the products (2048 cycles for
-// a pair of M tiles and 128 keys), and each group's chain S, weights, P.V, S adds its latencies
-// (about 3700 cycles a pair in all).  A prompt of 8192 tokens, 32/8 heads of 128, with a prefix
-// mask: 648 us, 1070 TFLOP/s; 8 of 2048, causal: 337 us, 815; with capped scores 504 us, 545 (the
-// cap's six operations an element come on top).
+// a pair of M tiles and 128 keys), and each group's chain S, weights, P.V, S adds its latencies.  A
+// prompt of 8192 tokens, 32/8 heads of 128, with a prefix mask: 609 us, 1138 TFLOP/s; 8 of 2048,
+// causal: 305 us, 902; with capped scores 413 us, 665 (the cap's six operations an element come on
+// top).
 //
 // P is rounded to bf16 (half a step, 2^-8 of each weight, as the output is); row sums, maxima and
-// O stay in 32 bits.  The reference maximum moves lazily, by more than 2^8 only.
+// O stay in 32 bits.  The reference maximum moves lazily, by more than 2^8 only; capped scores have
+// a fixed one (api_ops.cu), which saves the search for a maximum (8 x 2048: 504 us for 413).
 //
 // Every wait is bounded in time; on expiry the kernel records PA_DEVERR_TIMEOUT, every role
 // stops, loads and products in flight are drained (bounded) and the tensor memory is freed.
@@ -38,6 +41,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kKT = 128;        // keys per tile
+constexpr int kHalf = kKT / 2;  // and per S, P and their barriers
 constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;  // and 11: the other group's products
@@ -81,7 +85,8 @@ struct Piece {
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t qfull, qempty;
-  uint64_t sfull[2], pfull[2][2], ofull[2];  // per group; P in two halves
+  uint64_t sfull[2][2], pfull[2][2], ofull[2];  // per group; S and P in two halves
+  uint64_t half_done[2];  // a group's product with the first half of a tile's P
   uint64_t pc_full[kPieces], pc_empty[kPieces];
   uint64_t drain_bar[2];
   uint64_t turn[2][4];  // warp w of group g has done its exponentials of a tile
@@ -203,6 +208,16 @@ __device__ __forceinline__ float smallest(const float (&x)[N]) {
   return fminf(fminf(m[0], m[1]), fminf(m[2], m[3]));
 }
 
+template <int N>
+__device__ __forceinline__ float largest_magnitude(const float (&x)[N]) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < N; j += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(fabsf(x[j + 2 * e]), fabsf(x[j + 2 * e + 1])));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 // Elements of columns outside [a, b) become `v`.
 template <int N>
 __device__ __forceinline__ void mask_scores(float (&x)[N], int a, int b, float v) {
@@ -282,7 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_addr(&sh.qfull), 1);
     mbar_init(smem_addr(&sh.qempty), 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&sh.sfull[i]), 1);
+      mbar_init(smem_addr(&sh.sfull[i][0]), 1);
+      mbar_init(smem_addr(&sh.sfull[i][1]), 1);
+      mbar_init(smem_addr(&sh.half_done[i]), 1);
       mbar_init(smem_addr(&sh.pfull[i][0]), 128);
       mbar_init(smem_addr(&sh.pfull[i][1]), 128);
       mbar_init(smem_addr(&sh.ofull[i]), 1);
@@ -495,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // neither waits for the other group's P.  This loop is the latency between a group's P and its
       // next S, so it is kept short: what it needs of a piece lies in (uniform) registers and ring
       // slots are counted.
-      constexpr uint32_t id_s = tc05::instr_desc_bf16(128, kKT, 0);
+      constexpr uint32_t id_s = tc05::instr_desc_bf16(128, kHalf, 0);
       constexpr uint32_t id_pv = tc05::instr_desc_bf16(128, D, 1);
       // (a reduction over the warp tells the compiler that a value is the same in all lanes)
       auto uni = [](int v) { return __reduce_max_sync(kFull, v); };
@@ -503,8 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_base = smem_addr(smem) + g * C::SLOT, ring_base = smem_addr(ring);
       const uint32_t full0 = smem_addr(&sh.full[0]), empty0 = smem_addr(&sh.empty[0]);
       const uint32_t ts = tmem + kColS + g * kGroupCols, to = tmem + kColO + g * kGroupCols;
-      const uint32_t sfull = smem_addr(&sh.sfull[g]), ofull = smem_addr(&sh.ofull[g]);
-      const uint32_t pfull = smem_addr(&sh.pfull[g][0]);
+      const uint32_t sfull = smem_addr(&sh.sfull[g][0]), ofull = smem_addr(&sh.ofull[g]);
+      const uint32_t pfull = smem_addr(&sh.pfull[g][0]), half_done = smem_addr(&sh.half_done[g]);
       bool ok = true;
       int kslot = 0, vslot = 1;
       uint32_t kphase = 0, vphase = 0, ppar = 0;  // parities of K's and V's slots, and of P
@@ -515,15 +532,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1;
         }
       };
-      auto issue_s = [&] {
+      auto issue_s = [&](int h) {  // of 64 keys
         const uint64_t dq = tc05::smem_desc(q_base, 16, 1024);
-        const uint64_t dk = tc05::smem_desc(ring_base + kslot * C::SLOT, 16, 1024);
+        const uint64_t dk = tc05::smem_desc(ring_base + kslot * C::SLOT + h * (kHalf * 128), 16, 1024);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * C::CHUNK + (k & 3) * 32;
-          tc05::mma_ss_warp(ts, dq + (off >> 4), dk + (off >> 4), id_s, k > 0);
+          tc05::mma_ss_warp(ts + h * (kHalf), dq + (off >> 4), dk + (off >> 4), id_s, k > 0);
         }
-        tc05::commit_warp(sfull);
+        tc05::commit_warp(sfull + 8 * h);
       };
       for (int n = 0; ok; ++n) {
         if (!(ok = piece_wait(n))) break;
@@ -538,13 +555,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                    wait_warp(full0 + 8 * kslot, kphase, p.err, abort_flag)))
           break;
         tc05::fence_after_sync();
-        if (ga == 0 && gb > 0) issue_s();
+        if (ga == 0 && gb > 0) {
+          issue_s(0);
+          issue_s(1);
+        }
         tc05::commit_warp(empty0 + 8 * kslot);
         if (cnt == 1) tc05::commit_warp(smem_addr(&sh.qempty));
         next_slot(kslot, kphase);
         for (int j = 0; j < cnt; ++j) {
           // all that can be waited for before P is
-          const bool more = j + 1 < cnt, mine = j >= ga && j < gb;
+          const bool more = j + 1 < cnt, mine = j >= ga && j < gb, next = more && j + 1 >= ga && j + 1 < gb;
           if (!(ok = wait_warp(full0 + 8 * vslot, vphase, p.err, abort_flag))) break;
           const int a = max(lo - j * kKT, 0), z = min(hi - j * kKT, kKT);  // the item's keys within the tile
           if (rare(a > 0 || z < kKT)) {
@@ -566,24 +586,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s0 = a >> 4, s1 = (z + 15) >> 4;
             uint32_t acc = j != ga;  // the group's first tile of the piece overwrites O
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // P comes in two halves
+            for (int h = 0; h < 2; ++h) {  // P comes in two halves, and the next S takes their places
               if (!(ok = wait_warp(pfull + 8 * h, ppar, p.err, abort_flag))) break;
               tc05::fence_after_sync();
 #pragma unroll
               for (int k = 4 * h; k < 4 * h + 4; ++k) {
                 if (k >= s0 && k < s1) {
-                  tc05::mma_ts_warp(to, ts + 8 * k, dv + (k * 2048 >> 4), id_pv, acc);
+                  tc05::mma_ts_warp(to, ts + h * (kHalf) + 8 * (k - 4 * h), dv + (k * 2048 >> 4), id_pv, acc);
                   acc = 1;
                 }
               }
+              if (h == 0) tc05::commit_warp(half_done);
+              if (next) issue_s(h);
             }
             if (!ok) break;
             ppar ^= 1;
             if (j == gb - 1) tc05::commit_warp(ofull);
+          } else if (next) {
+            issue_s(0);
+            issue_s(1);
           }
           tc05::commit_warp(empty0 + 8 * vslot);
           next_slot(vslot, vphase);
-          if (more && j + 1 >= ga && j + 1 < gb) issue_s();
           if (more) {
             tc05::commit_warp(empty0 + 8 * kslot);
             if (j + 2 == cnt) tc05::commit_warp(smem_addr(&sh.qempty));
@@ -636,9 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto mine = [&](const Piece& pc) { return pc.row0 + g * HR + min(r, max(rows_of(pc), 1) - 1); };
     // Warps w of the two groups share a sub-partition and its exponentials: they take turns at them,
     // group 0 first, so that one group's products run while the other computes.  (Left alone they
-    // fall into step, compute at half the rate each and wait for their products together: 703 us
-    // against 648 for a prompt of 8192 tokens.  Where scores are capped or biased the groups' other
-    // arithmetic overlaps the exponentials better without turns: 543 us against 643 for 8 x 2048.)
+    // fall into step, compute at half the rate each and wait for their products together: 645 us
+    // against 618 for a prompt of 8192 tokens.  Where scores are capped or biased the groups' other
+    // arithmetic overlaps the exponentials better without turns: 413 us against 493 for 8 x 2048.)
     // Tiles that one of the groups skips have no turn.
     auto my_turn = [&] {
       if (g == 0 && turns == 0) return true;
@@ -670,73 +694,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         all_hi = min(all_hi, __shfl_xor_sync(kFull, all_hi, off));
         all_pos = min(all_pos, __shfl_xor_sync(kFull, all_pos, off));
       }
-      float m_ref = -INFINITY, l = 0.f;
-      for (int j = ja; j < jb; ++j, ++done) {
-        if (!(ok = wait_warp(smem_addr(&sh.sfull[g]), done & 1, p.err, abort_flag))) break;
-        tc05::fence_after_sync();
+      // (capped scores lie within the cap: their reference is fixed, with no maximum to be found)
+      float m_ref = CAP_ONLY ? p.cap_ref : -INFINITY, l = 0.f;
+      for (int j = ja; j < jb && ok; ++j, ++done) {
         const bool turn = kTurns && j >= turn_lo && j < turn_hi;
-        if (rare(32 * w >= rows)) {  // none of the warp's rows is a row of the item
-          if (turn) {
-            if (!(ok = my_turn())) break;
-            turn_over();
-          }
-          tc05::fence_before_sync();
-          mbar_arrive(smem_addr(&sh.pfull[g][0]));
-          mbar_arrive(smem_addr(&sh.pfull[g][1]));
-          continue;
-        }
-        const int key0 = (pc.kt0 + j) * kKT;
-        uint32_t raw[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc05::ld32(ts + 32 * c, raw[c]);
-        tc05::wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc05::landed(raw[c]);
-        float x[kKT];
-#pragma unroll
-        for (int e = 0; e < kKT; ++e) x[e] = __uint_as_float(raw[e / 32][e % 32]);
-        const bool masked = key0 < all_lo || key0 + kKT > all_hi;
-        float mt;
-        bool small = false;
-        if constexpr (CAP_ONLY) {
-          // the cap is monotone: the extremes of the raw scores give the maximum and the formula,
-          // and the scores are capped half by half below (short code, few registers)
-          if (rare(masked)) mask_scores(x, row.lo - key0, row.hi - key0, __int_as_float(0x7fffffff));
-          const float mx = largest(x), mn = smallest(x);
-          small = cap_is_small(p, fmaxf(fabsf(mx), fabsf(mn)));
-          float top[1] = {p.cap_in >= 0.f ? mx : mn};
-          const bool none = mx == -INFINITY && mn == INFINITY;
-          top[0] = fmaf(-2.f * p.cap_out, rcp_approx(1.f + ex2_approx(top[0] * p.cap_in * (2.f * kLog2e))), p.cap_out);
-          mt = none ? -INFINITY : top[0];
-        } else {
-          mt = modify_scores<C::CAP, C::BIAS>(x, p, row, key0, masked, p.prefix_lens && key0 + kKT - 1 > all_pos) * mul;
-        }
-        const bool raise = mt > m_ref + kRescaleLog2;
-        // (earlier P.V of the group are complete: S was issued behind them)
-        if (rare(__any_sync(kFull, raise))) {
-          const float alpha = raise ? ex2_approx(m_ref - mt) : 1.f;
-          if (j > ja) {
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t v[16];
-              tc05::ld16(to + c, v);
-              tc05::wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-              tc05::st16(to + c, v);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t sfull = smem_addr(&sh.sfull[g][0]);
+          if (!(ok = wait_warp(sfull + 8 * h, done & 1, p.err, abort_flag))) break;
+          tc05::fence_after_sync();
+          const uint32_t tsh = ts + h * kHalf;
+          if (rare(32 * w >= rows)) {  // none of the warp's rows is a row of the item
+            if (turn) {
+              if (!(ok = my_turn())) break;
+              turn_over();
             }
+            tc05::fence_before_sync();
+            mbar_arrive(smem_addr(&sh.pfull[g][h]));
+            continue;
           }
-          l *= alpha;
-          if (raise) m_ref = mt;
-        }
-        if (turn && !(ok = my_turn())) break;
-        const float2 mul2 = splat(mul), ref2 = splat(m_ref == -INFINITY ? 0.f : -m_ref);
-        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
-        auto weights = [&](const float* y64, int h) {
+          const int key0 = (pc.kt0 + j) * kKT + h * kHalf;
+          uint32_t raw[2][32];
+          tc05::ld32(tsh, raw[0]);
+          tc05::ld32(tsh + 32, raw[1]);
+          tc05::wait_ld();
+          tc05::landed(raw[0]);
+          tc05::landed(raw[1]);
+          float x[kHalf];
+#pragma unroll
+          for (int e = 0; e < kHalf; ++e) x[e] = __uint_as_float(raw[e / 32][e % 32]);
+          const bool masked = key0 < all_lo || key0 + kHalf > all_hi;
+          float mt = m_ref;
+          bool small = false;
+          if constexpr (CAP_ONLY) {
+            if (rare(masked)) mask_scores(x, row.lo - key0, row.hi - key0, 0.f);
+            small = cap_is_small(p, largest_magnitude(x));
+          } else {
+            mt = modify_scores<C::CAP, C::BIAS>(x, p, row, key0, masked, p.prefix_lens && key0 + kHalf - 1 > all_pos) *
+                 mul;
+          }
+          const bool raise = mt > m_ref + kRescaleLog2;
+          if (!CAP_ONLY && rare(__any_sync(kFull, raise))) {
+            const float alpha = raise ? ex2_approx(m_ref - mt) : 1.f;
+            if (j > ja || h > 0) {
+              // the group's earlier P.V must be complete: the second half's S is issued behind those
+              // of the tile before
+              if (!(ok = wait_warp(h ? smem_addr(&sh.half_done[g]) : sfull + 8, done & 1, p.err, abort_flag))) break;
+              tc05::fence_after_sync();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t v[16];
+                tc05::ld16(to + c, v);
+                tc05::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                tc05::st16(to + c, v);
+              }
+            }
+            l *= alpha;
+            if (raise) m_ref = mt;
+          }
+          if (turn && !(ok = my_turn())) break;
+          const float2 mul2 = splat(mul), ref2 = splat(!CAP_ONLY && m_ref == -INFINITY ? 0.f : -m_ref);
+          if constexpr (CAP_ONLY) {
+            cap_scores(x, p, small, ref2.x);
+            if (rare(masked)) mask_scores(x, row.lo - key0, row.hi - key0, -INFINITY);
+          }
+          float2 l0 = make_float2(0.f, 0.f), l1 = l0;
           uint32_t v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            float2 y = make_float2(y64[2 * e], y64[2 * e + 1]);
+            float2 y = make_float2(x[2 * e], x[2 * e + 1]);
             // (cap_scores has added the reference)
             if (!CAP_ONLY) y = PLAIN ? __ffma2_rn(y, mul2, ref2) : __fadd2_rn(y, ref2);
             y.x = ex2_approx(y.x);
@@ -744,34 +772,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (e & 1) l1 = __fadd2_rn(l1, y); else l0 = __fadd2_rn(l0, y);
             v[e] = pack_bf16x2(y.x, y.y);
           }
-          tc05::st32(ts + 32 * h, v);
-          // the product of this half runs while the other is computed
+          tc05::st32(tsh, v);
           tc05::wait_st();
           tc05::fence_before_sync();
           mbar_arrive(smem_addr(&sh.pfull[g][h]));
-        };
-        if constexpr (CAP_ONLY) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t again[2][32];
-            tc05::ld32(ts + 64 * h, again[0]);
-            tc05::ld32(ts + 64 * h + 32, again[1]);
-            tc05::wait_ld();
-            tc05::landed(again[0]);
-            tc05::landed(again[1]);
-            float y[64];
-#pragma unroll
-            for (int e = 0; e < 64; ++e) y[e] = __uint_as_float(again[e / 32][e % 32]);
-            cap_scores(y, p, small, ref2.x);
-            if (rare(masked)) mask_scores(y, row.lo - key0 - 64 * h, row.hi - key0 - 64 * h, -INFINITY);
-            weights(y, h);
-          }
-        } else {
-          weights(x, 0);
-          weights(x + 64, 1);
+          if (turn) turn_over();
+          l += (l0.x + l0.y) + (l1.x + l1.y);
         }
-        if (turn) turn_over();
-        l += (l0.x + l0.y) + (l1.x + l1.y);
       }
       if (!ok) break;
 
@@ -872,7 +879,8 @@ int attention_tc_rows(int G) { return 2 * (128 / G) * G; }
 
 template <int D>
 static cudaError_t run_modified(const AttnParams& p, cudaStream_t stream) {
-  const bool cap = p.cap_out > 0.f, bias = p.slopes != nullptr || (!cap && !(p.scale_log2 > 0.f));
+  // a cap too wide for one reference is the general case, as a negative scale is
+  const bool cap = p.cap_out > 0.f, bias = p.slopes != nullptr || (cap ? !(p.cap_ref < INFINITY) : !(p.scale_log2 > 0.f));
   if (cap) return bias ? run<TcAttn<D, true, true>>(p, stream) : run<TcAttn<D, true, false>>(p, stream);
   return bias ? run<TcAttn<D, false, true>>(p, stream) : run<TcAttn<D, false, false>>(p, stream);
 }

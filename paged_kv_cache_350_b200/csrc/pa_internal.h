@@ -191,6 +191,7 @@ struct AttnParams {
   float scale_log2;             // scale * log2(e)
   float cap_in, cap_out;        // with a cap: scale / cap and cap * log2(e); cap_out 0: none
   float cap_poly[5], cap_small; // the tensor-core kernel's polynomial of the cap, and its bound
+  float cap_ref;           // reference of capped scores without a bias; inf: their maximum is found
   int window;                   // 0: none
   int T, B, max_query_len, Hq, Hkv, G, D, block_size, max_blocks, num_blocks;
   int32_t* err;

@@ -324,6 +324,14 @@ def test_negative_and_zero_scales_and_extreme_caps():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cap", [0.5, 5.0, 30.0, 40.0, 50.0, 50.5, 60.0, 400.0])
+@pytest.mark.parametrize("spread", [1.0, 40.0])
+def test_caps_of_all_widths(cap, spread):
+    for kw in ({}, dict(bias=True), dict(window=33)):
+        Case("bf16", [70, 3, 150], [300, 200, 150], 4, 2, 64, 16, softcap=cap, spread=spread, **kw).check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [[1, 1], [70, 1]])
 def test_infinities_behind_a_mask_reach_nobody(dtype, n):
