@@ -22,12 +22,12 @@
 // Bound by the softmax: 16 exponentials a cycle and SM take as long as the products (2048 cycles for
 // a pair of M tiles and 128 keys), and each group's chain S, weights, P.V, S adds its latencies.  A
 // prompt of 8192 tokens, 32/8 heads of 128, with a prefix mask: 609 us, 1138 TFLOP/s; 8 of 2048,
-// causal: 305 us, 902; with capped scores 413 us, 665 (the cap's six operations an element come on
-// top).
+// causal: 305 us, 902; with capped scores 370 us, 744.  (Sustained, at the 1000 W limit, the prompt takes
+// 710 us at 1.65 GHz.)
 //
 // P is rounded to bf16 (half a step, 2^-8 of each weight, as the output is); row sums, maxima and
 // O stay in 32 bits.  The reference maximum moves lazily, by more than 2^8 only; capped scores have
-// a fixed one (api_ops.cu), which saves the search for a maximum (8 x 2048: 504 us for 413).
+// a fixed one (api_ops.cu), which saves the search for a maximum (8 x 2048: 514 us for 413).
 //
 // Every wait is bounded in time; on expiry the kernel records PA_DEVERR_TIMEOUT, every role
 // stops, loads and products in flight are drained (bounded) and the tensor memory is freed.
@@ -140,38 +140,45 @@ __device__ __forceinline__ bool cap_is_small(const AttnParams& p, float top) {
   return __all_sync(kFull, top * p.cap_small <= 0.85f);  // (NaN: no)
 }
 
-// cap * tanh(scale * x / cap) log2(e) + add of N raw scores, in place.
+// cap * tanh(scale * x / cap) log2(e) + add of N raw scores, in place: tanh(t) / t as a polynomial in
+// t^2 (iterated reweighted least squares on |t| <= 0.85, where |t P(t^2) - tanh t| < 6.9e-7 in 32
+// bits): on the FMA pipe alone, the exponentials need the other.  Scale and cap are in the
+// coefficients.
+template <int N>
+__device__ __forceinline__ void cap_polynomial(float (&x)[N], const AttnParams& p, float add) {
+  constexpr int E = 8;  // elements taken step by step, so that the steps of one do not wait
+  const float2 c4 = splat(p.cap_poly[4]), c3 = splat(p.cap_poly[3]), c2 = splat(p.cap_poly[2]),
+               c1 = splat(p.cap_poly[1]), c0 = splat(p.cap_poly[0]), last = splat(add);
+#pragma unroll
+  for (int j = 0; j < N; j += E) {
+    float2 t[E / 2], u[E / 2], y[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) t[e] = make_float2(x[j + 2 * e], x[j + 2 * e + 1]);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) u[e] = __fmul2_rn(t[e], t[e]);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(u[e], c4, c3);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c2);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c1);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c0);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      y[e] = __ffma2_rn(y[e], t[e], last);
+      x[j + 2 * e] = y[e].x;
+      x[j + 2 * e + 1] = y[e].y;
+    }
+  }
+}
+
+// The same by the formula that `small` allows.
 template <int N>
 __device__ __forceinline__ void cap_scores(float (&x)[N], const AttnParams& p, bool small, float add) {
-  constexpr int E = 8;  // elements taken step by step, so that the steps of one do not wait
+  constexpr int E = 8;
   if (__builtin_expect(small, 1)) {
-    // tanh(t) / t as a polynomial in t^2 (iterated reweighted least squares on |t| <= 0.85, where
-    // |t P(t^2) - tanh t| < 6.9e-7 in 32 bits): on the FMA pipe alone, the exponentials need the
-    // other.  Scale and cap are in the coefficients.
-    const float2 c4 = splat(p.cap_poly[4]), c3 = splat(p.cap_poly[3]), c2 = splat(p.cap_poly[2]),
-                 c1 = splat(p.cap_poly[1]), c0 = splat(p.cap_poly[0]), last = splat(add);
-#pragma unroll
-    for (int j = 0; j < N; j += E) {
-      float2 t[E / 2], u[E / 2], y[E / 2];
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) t[e] = make_float2(x[j + 2 * e], x[j + 2 * e + 1]);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) u[e] = __fmul2_rn(t[e], t[e]);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(u[e], c4, c3);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c2);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c1);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) y[e] = __ffma2_rn(y[e], u[e], c0);
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        y[e] = __ffma2_rn(y[e], t[e], last);
-        x[j + 2 * e] = y[e].x;
-        x[j + 2 * e + 1] = y[e].y;
-      }
-    }
+    cap_polynomial(x, p, add);
   } else {
     // tanh t = 1 - 2 / (1 + e^2t)
     const float c2 = p.cap_in * (2.f * kLog2e), m2 = -2.f * p.cap_out, last = p.cap_out + add;
@@ -756,21 +763,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (turn && !(ok = my_turn())) break;
           const float2 mul2 = splat(mul), ref2 = splat(!CAP_ONLY && m_ref == -INFINITY ? 0.f : -m_ref);
-          if constexpr (CAP_ONLY) {
-            cap_scores(x, p, small, ref2.x);
-            if (rare(masked)) mask_scores(x, row.lo - key0, row.hi - key0, -INFINITY);
-          }
           float2 l0 = make_float2(0.f, 0.f), l1 = l0;
           uint32_t v[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float2 y = make_float2(x[2 * e], x[2 * e + 1]);
-            // (cap_scores has added the reference)
-            if (!CAP_ONLY) y = PLAIN ? __ffma2_rn(y, mul2, ref2) : __fadd2_rn(y, ref2);
+          auto weigh = [&](int e, float2 y) {
             y.x = ex2_approx(y.x);
             y.y = ex2_approx(y.y);
             if (e & 1) l1 = __fadd2_rn(l1, y); else l0 = __fadd2_rn(l0, y);
             v[e] = pack_bf16x2(y.x, y.y);
+          };
+          if (CAP_ONLY && __builtin_expect(small && !masked, 1)) {
+            // caps and exponentials in one block: the caps of some scores run on the FMA pipe while
+            // the exponentials of others have theirs (one after the other: 418 us for 370)
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 8) {
+              float y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = x[c + e];
+              cap_polynomial(y, p, ref2.x);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) weigh(c / 2 + e, make_float2(y[2 * e], y[2 * e + 1]));
+            }
+          } else {
+            if constexpr (CAP_ONLY) {
+              cap_scores(x, p, small, ref2.x);
+              if (rare(masked)) mask_scores(x, row.lo - key0, row.hi - key0, -INFINITY);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float2 y = make_float2(x[2 * e], x[2 * e + 1]);
+              // (cap_scores has added the reference)
+              weigh(e, CAP_ONLY ? y : PLAIN ? __ffma2_rn(y, mul2, ref2) : __fadd2_rn(y, ref2));
+            }
           }
           tc05::st32(tsh, v);
           tc05::wait_st();
