@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // group 0 first, so that one group's products run while the other computes.  (Left alone they
     // fall into step, compute at half the rate each and wait for their products together: 645 us
     // against 618 for a prompt of 8192 tokens.  Where scores are capped or biased the groups' other
-    // arithmetic overlaps the exponentials better without turns: 413 us against 493 for 8 x 2048.)
+    // arithmetic overlaps the exponentials better without turns: 366 us against 463 for 8 x 2048.)
     // Tiles that one of the groups skips have no turn.
     auto my_turn = [&] {
       if (g == 0 && turns == 0) return true;
