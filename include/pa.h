@@ -401,7 +401,9 @@ typedef struct pa_attention_mods {
  * need no initialisation, and calls whose kernels may overlap on the GPU must not share one.
  * Any Hq / Hkv, D in {64, 128}, block_size in {4, 8, 16, 32}, bf16 or fp32.  In bf16 with more than
  * 16 (token, head of the group) rows per sequence the softmax weights are rounded to bf16 for their
- * product with V.  A batch whose tile counts could pass 2^31 is PA_ERR_UNSUPPORTED. */
+ * product with V, and with a softcap above 30 V should lie within 2^56 in magnitude (larger values may
+ * overflow; below 2^-20 they lose precision in rows whose scores are all at the negative cap).  A
+ * batch whose tile counts could pass 2^31 is PA_ERR_UNSUPPORTED. */
 size_t pa_attention_workspace_size(int T, int B, int max_query_len, int Hq, int Hkv, int D,
                                    int block_size, int max_blocks);
 pa_status pa_attention(void* out, const void* q, const void* k_pool, const void* v_pool,

@@ -332,6 +332,16 @@ def test_caps_of_all_widths(cap, spread):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cap", [30.0, 50.0])
+@pytest.mark.parametrize("size", [2.0 ** 50, 2.0 ** -15])
+def test_capped_scores_with_large_and_small_values(cap, size):
+    c = Case("bf16", [70, 3], [300, 200], 4, 2, 64, 16, softcap=cap, spread=40.0)
+    c.v_pool *= size   # (a power of two: exact)
+    c.values = [v * size for v in c.values]
+    c.check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [[1, 1], [70, 1]])
 def test_infinities_behind_a_mask_reach_nobody(dtype, n):
