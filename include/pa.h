@@ -399,6 +399,8 @@ typedef struct pa_attention_mods {
  * rows that do not see it.  out must not overlap q; |scale| and |scale| / softcap are at most 1e30.
  * mods may be NULL.  Workspace: pa_attention_workspace_size bytes, 256-byte aligned; its contents
  * need no initialisation, and calls whose kernels may overlap on the GPU must not share one.
+ * A cap's own error: in fp32 a few ulp of the capped score; in bf16 at most 1e-6 of a cap up to 64, and
+ * 2^-20 of the capped score with a wider one (1e30 is as good as none).
  * Any Hq / Hkv, D in {64, 128}, block_size in {4, 8, 16, 32}, bf16 or fp32.  In bf16 with more than
  * 16 (token, head of the group) rows per sequence the softmax weights are rounded to bf16 for their
  * product with V, and with a softcap above 30 V should lie within 2^56 in magnitude (larger values may

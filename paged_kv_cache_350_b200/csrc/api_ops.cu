@@ -292,7 +292,8 @@ pa_status pa_attention(void* out, const void* q, const void* k_pool, const void*
                                     -0.04714450612664223, 0.01063788216561079};
     const double ci = m.softcap > 0.f ? static_cast<double>(scale) / m.softcap : 0.0;
     for (int k = 0; k < 5; ++k) p.cap_poly[k] = static_cast<float>(kTanh[k] * m.softcap * log2e * std::pow(ci, 2 * k + 1));
-    const bool usable = std::fabs(ci) >= 1e-3 && std::fabs(ci) <= 1e3 && m.softcap >= 1e-6f && m.softcap <= 1e6f;
+    p.cap_wide = m.softcap > pa::kWideCap;
+    const bool usable = std::fabs(ci) >= 1e-3 && std::fabs(ci) <= 1e3 && m.softcap >= 1e-6f && !p.cap_wide;
     p.cap_small = usable ? static_cast<float>(std::fabs(ci)) : INFINITY;
     // One reference for all scores within +-cap_out: their weights lie in 2^(top - 2 cap_out) ..
     // 2^top, so top is as low as keeps the smallest above 2^-80, at most 40; inf: none would keep it

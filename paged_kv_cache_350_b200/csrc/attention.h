@@ -67,6 +67,24 @@ __device__ __forceinline__ int attn_query_span(const AttnParams& p, int b, bool 
   return bad ? 0 : s1 - s0;
 }
 
+// cap * tanh(scale * s / cap) * log2 e of a raw score s, by tanh t = 1 - 2 / (1 + e^2t) of t = s * cap_in:
+// the error is absolute, 2^-22 of the cap, as this cancels for small t.
+__device__ __forceinline__ float cap_score(float t, float cap_out) {
+  return fmaf(-2.f * cap_out, rcp_approx(1.f + ex2_approx(t * (2.f * kLog2e))), cap_out);
+}
+
+// The same below |t| = kNearTanh: scale * s times the series of tanh(t) / t up to t^8 (the next term is
+// 2.4e-7 there).  With the other one above it the error is 2^-20 of the result, whatever the cap.
+constexpr float kNearTanh = 0.35f;
+__device__ __forceinline__ float cap_score_near(float s, float t, float scale_log2) {
+  const float u = t * t;
+  float y = fmaf(u, 62.f / 2835.f, -17.f / 315.f);
+  y = fmaf(y, u, 2.f / 15.f);
+  y = fmaf(y, u, -1.f / 3.f);
+  y = fmaf(y, u, 1.f);
+  return s * scale_log2 * y;
+}
+
 // Keys visible to the query token at position pos of a sequence of L tokens: [lo, hi) with
 //   key j visible iff j < L, (j <= pos or j < prefix), j > pos - window (if any), j >= first.
 // A position below 0 (more query tokens than cached ones) sees nothing.

@@ -115,11 +115,12 @@ struct Row {
   float pos, slope;
 };
 
-// Scores of one tile for N rows of a lane.
-template <int N>
+// Scores of one tile for N rows of a lane.  EXACT (fp32): the cap holds to 32 bits (a few ulp of the
+// score); else to 2^-22 of the cap, or to 2^-20 of the score where the cap is wide.
+template <int N, bool EXACT>
 struct TileScores {
   float sl2, cap_in, cap_out;
-  bool biased;
+  bool biased, wide;
   int key0;
   Row row[N];
   __device__ __forceinline__ void init(const AttnParams& p) {
@@ -127,6 +128,7 @@ struct TileScores {
     cap_in = p.cap_in;
     cap_out = p.cap_out;
     biased = p.slopes != nullptr;
+    wide = p.cap_wide;
   }
   // row `which` is row r of unit (sequence s of batch row b, KV head kvh)
   __device__ __forceinline__ void set(const AttnParams& p, int which, const Seq& s, int b, int kvh, int r) {
@@ -139,10 +141,16 @@ struct TileScores {
   __device__ __forceinline__ float operator()(float s, int k, int which) const {
     const Row& r = row[which];
     const int key = key0 + k;
-    // tanh t = 1 - 2 / (1 + e^2t), with the absolute error of the reciprocal, 2^-22 of the cap
-    float x = cap_out > 0.f
-                  ? fmaf(-2.f * cap_out, rcp_approx(1.f + ex2_approx(s * cap_in * (2.f * kLog2e))), cap_out)
-                  : s * sl2;
+    float x = s * sl2;
+    if (cap_out > 0.f) {
+      const float t = s * cap_in;
+      if constexpr (EXACT) {
+        x = cap_out * tanhf(t);
+      } else {
+        x = cap_score(t, cap_out);
+        if (__builtin_expect(wide, 0) && fabsf(t) < kNearTanh) x = cap_score_near(s, t, sl2);
+      }
+    }
     if (biased) x = fmaf(-r.slope, fabsf(r.pos - static_cast<float>(key)), x);
     return key >= r.lo && key < r.hi ? x : -INFINITY;
   }

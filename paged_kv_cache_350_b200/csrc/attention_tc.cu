@@ -55,11 +55,12 @@ constexpr uint32_t kColS = 0, kColO = 256, kGroupCols = 128, kTmemCols = 512;
 constexpr int kPieceUsers = 3 + kSoftWarps;
 
 // CAP, BIAS: what is done to the scores, fixed at compile time so that the loop of a call is short
-// straight code (instruction fetches bound the kernel that decided at run time).
-template <int D_, bool CAP_, bool BIAS_>
+// straight code (instruction fetches bound the kernel that decided at run time).  WIDE: the cap is one
+// past kWideCap (with CAP and BIAS).
+template <int D_, bool CAP_, bool BIAS_, bool WIDE_ = false>
 struct TcAttn {
   static constexpr int D = D_;
-  static constexpr bool CAP = CAP_, BIAS = BIAS_;
+  static constexpr bool CAP = CAP_, BIAS = BIAS_, WIDE = WIDE_;
   static constexpr int MT = 2;                        // M tiles of an item
   static constexpr int DCH = D / 64;
   static constexpr int CHUNK = kKT * 128;             // one 64-column chunk of 128 rows
@@ -235,11 +236,17 @@ __device__ __forceinline__ void mask_scores(float (&x)[N], int a, int b, float v
 // Turn the N raw scores of a row (keys key0 ..) into log2-domain scores in place and return their
 // maximum.  The plain case keeps raw scores, so that the scale and the subtraction of the maximum
 // become one operation.  `ahead`: some of the keys may lie behind the row's position and count.
-template <bool CAP, bool BIAS, int N>
+template <bool CAP, bool BIAS, bool WIDE, int N>
 __device__ __forceinline__ float modify_scores(float (&x)[N], const AttnParams& p, const Row& r, int key0,
                                                bool masked, bool ahead) {
   constexpr int E = 8;
-  if constexpr (CAP) {
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {  // (both, and a choice: branches in this loop take 1138 us for 8 x 2048, not 813)
+      const float t = x[j] * p.cap_in, near = cap_score_near(x[j], t, p.scale_log2), far = cap_score(t, p.cap_out);
+      x[j] = fabsf(t) < kNearTanh ? near : far;
+    }
+  } else if constexpr (CAP) {
     if (rare(masked)) mask_scores(x, r.lo - key0, r.hi - key0, 0.f);  // what lies there must not choose the formula
     cap_scores(x, p, cap_is_small(p, fmaxf(largest(x), -smallest(x))), 0.f);
   }
@@ -737,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (rare(masked)) mask_scores(x, row.lo - key0, row.hi - key0, 0.f);
             small = cap_is_small(p, largest_magnitude(x));
           } else {
-            mt = modify_scores<C::CAP, C::BIAS>(x, p, row, key0, masked, p.prefix_lens && key0 + kHalf - 1 > all_pos) *
+            mt = modify_scores<C::CAP, C::BIAS, C::WIDE>(x, p, row, key0, masked, p.prefix_lens && key0 + kHalf - 1 > all_pos) *
                  mul;
           }
           const bool raise = mt > m_ref + kRescaleLog2;
@@ -904,6 +911,7 @@ template <int D>
 static cudaError_t run_modified(const AttnParams& p, cudaStream_t stream) {
   // a cap too wide for one reference is the general case, as a negative scale is
   const bool cap = p.cap_out > 0.f, bias = p.slopes != nullptr || (cap ? !(p.cap_ref < INFINITY) : !(p.scale_log2 > 0.f));
+  if (p.cap_wide) return run<TcAttn<D, true, true, true>>(p, stream);
   if (cap) return bias ? run<TcAttn<D, true, true>>(p, stream) : run<TcAttn<D, true, false>>(p, stream);
   return bias ? run<TcAttn<D, false, true>>(p, stream) : run<TcAttn<D, false, false>>(p, stream);
 }

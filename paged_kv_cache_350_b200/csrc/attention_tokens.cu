@@ -41,7 +41,7 @@ size_t tokens_smem(int B) {
 }
 
 // Scores of one tile for this lane's two rows (tc_tile.cuh).
-struct Modified : TileScores<2> {
+struct Modified : TileScores<2, false> {
   static constexpr bool kEmptyRows = true;
 };
 

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   float* out = static_cast<float*>(p.out);
   const float* qp = static_cast<const float*>(p.q);
-  TileScores<NV> score;
+  TileScores<NV, true> score;
   score.init(p);
   int4 own = make_int4(0, 0, 0, 0);  // as in attention_tokens.cu
   int i = 0, gpos = beg;

@@ -175,6 +175,9 @@ struct RopeParams {
 cudaError_t launch_rope(const RopeParams& p, pa_dtype dtype, cudaStream_t stream);
 
 // Attention of ragged query tokens (attention.cu, attention_tc.cu, attention_tokens.cu).
+// The formulas for the usual caps are off by up to 6.9e-7 (bf16 prompts' polynomial) of the cap, whatever
+// the score: 4.4e-5 here, which is little beside the weights' rounding to bf16, and worse for each wider cap.
+constexpr float kWideCap = 64.f;
 struct AttnItem;
 struct AttnStart;
 struct AttnParams {
@@ -191,6 +194,7 @@ struct AttnParams {
   float scale_log2;             // scale * log2(e)
   float cap_in, cap_out;        // with a cap: scale / cap and cap * log2(e); cap_out 0: none
   float cap_poly[5], cap_small; // the tensor-core kernel's polynomial of the cap, and its bound
+  int cap_wide;                 // a cap past kWideCap: its error is relative to the score (attention.h)
   float cap_ref;           // reference of capped scores without a bias; inf: their maximum is found
   int window;                   // 0: none
   int T, B, max_query_len, Hq, Hkv, G, D, block_size, max_blocks, num_blocks;
