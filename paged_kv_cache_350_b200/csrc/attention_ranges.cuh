@@ -112,7 +112,8 @@ __device__ __forceinline__ void scan_units(const AttnParams& p, int tile, int* P
 
 struct Row {
   int lo, hi;  // visible keys
-  float pos, slope;
+  int pos;
+  float slope;
 };
 
 // Scores of one tile for N rows of a lane.  EXACT (fp32): the cap holds to 32 bits (a few ulp of the
@@ -135,7 +136,7 @@ struct TileScores {
     const int pre = p.prefix_lens ? __ldg(p.prefix_lens + b) : 0, tok = r / p.G;
     Row& w = row[which];
     attn_visible(p, s.L - s.n + tok, s.L, pre, p.first_keys ? __ldg(p.first_keys + s.q0 + tok) : 0, w.lo, w.hi);
-    w.pos = static_cast<float>(s.L - s.n + tok);
+    w.pos = s.L - s.n + tok;
     w.slope = p.slopes ? __ldg(p.slopes + kvh * p.G + (r - tok * p.G)) * kLog2e : 0.f;
   }
   __device__ __forceinline__ float operator()(float s, int k, int which) const {
@@ -151,7 +152,8 @@ struct TileScores {
         if (__builtin_expect(wide, 0) && fabsf(t) < kNearTanh) x = cap_score_near(s, t, sl2);
       }
     }
-    if (biased) x = fmaf(-r.slope, fabsf(r.pos - static_cast<float>(key)), x);
+    // (the positions' difference in whole numbers: past 2^24 a float does not tell neighbours apart)
+    if (biased) x = fmaf(-r.slope, fabsf(static_cast<float>(r.pos - key0) - static_cast<float>(k)), x);
     return key >= r.lo && key < r.hi ? x : -INFINITY;
   }
 };

@@ -1,11 +1,12 @@
-"""Attention with caps over their whole range, against the formula in 64 bits with a tolerance
-that does not grow with the cap."""
+"""Attention with caps over their whole range and with far positions, against the formula in 64
+bits: tolerances grow neither with the cap nor with the position."""
 
 import math
 
 import pytest
 import torch
 
+import paged_kv_cache_350_b200 as pa
 from test_attention import Case
 
 ULP = 2.0 ** -24   # half a step of 32 bits
@@ -76,3 +77,44 @@ def test_a_cap_past_all_scores_is_no_cap(dtype, n):
     c = Capped(dtype, n, [300, 90], 8, 2, 128, 16, softcap=1e4)
     c.scale = -c.scale
     c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,Hq", [(1, 4), (3, 4), (20, 4)])
+def test_a_bias_past_2_24_positions(dtype, n, Hq):
+    """A sequence of 2^25 keys over a table that goes round a few blocks: neighbouring keys are told
+    apart by their distances."""
+    bs, D, blocks, tail = 32, 64, 5, 4096
+    L = (1 << 25) + 77
+    g = torch.Generator().manual_seed(n)
+    kp, vp = (torch.randn(blocks, bs, 1, D, generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(n, Hq, D, generator=g).to(dtype)
+    slopes = torch.tensor([1.0, 0.5, 0.25, 0.125][:Hq])
+    MB = -(-L // bs)
+    table = (torch.arange(MB, dtype=torch.int32) % blocks)[None]
+    out = torch.empty(n, Hq, D, dtype=dtype, device="cuda")
+    ws = torch.empty(pa.pa_attention_workspace_size(n, 1, n, Hq, 1, D, bs, MB), dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_attention(out, q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), torch.tensor([L], dtype=torch.int32).cuda(),
+                    torch.tensor([0, n], dtype=torch.int32).cuda(), n, D ** -0.5, alibi_slopes=slopes.cuda(),
+                    workspace=ws, err_flag=err)
+    got = out.cpu().double()
+    assert int(err.item()) == 0
+    # keys before the last `tail` weigh less than e^(largest score difference - slope * tail) each
+    key = torch.arange(L - tail, L)
+    rows = key // bs % blocks * bs + key % bs
+    k, v = kp.view(-1, D)[rows].double(), vp.view(-1, D)[rows].double()
+    pos = torch.arange(L - n, L)[:, None]
+    for h in range(Hq):
+        x = q[:, h].double() @ k.T * D ** -0.5
+        assert L * math.exp(2 * float(x.abs().max()) - 0.125 * (tail - n)) < 1e-100
+        bias = float(slopes[h]) * (pos - key).abs().double()
+        d = q[:, h].double().abs() @ k.abs().T * D ** -0.5 * (D + 4) * 2.0 ** -22 + (x.abs() + 2 * bias) * 4 * ULP
+        w = torch.softmax((x - bias).masked_fill(key > pos, -math.inf), -1)
+        ref, size = w @ v, w @ v.abs()
+        off = torch.expm1((w * d).sum(-1, keepdim=True) + (w * d).amax(-1, keepdim=True))
+        half = torch.finfo(dtype).eps / 2
+        # weights rounded to bf16 for their product, the output; sums over the keys that have a weight
+        tol = size * (2 * off + (tail + 8) * ULP + 2.0 ** -20 + (half if dtype == torch.bfloat16 else 0)) + ref.abs() * half
+        assert bool(((got[:, h] - ref).abs() <= tol).all()), float(((got[:, h] - ref).abs() / tol).max())
