@@ -489,6 +489,13 @@ pa_status pa_alloc_append_slots(pa_allocator* a, const int64_t* seq_ids, int n,
  * one copy there can be (of a shared last block) or -1. */
 pa_status pa_alloc_append_tokens(pa_allocator* a, int64_t seq_id, int n, int64_t* slots,
                                  int32_t* cow_src, int32_t* cow_dst);
+/* Take back the last n tokens that an append gave the sequence: blocks past the tokens left are
+ * released, the last first (refcount - 1; free at 0).  cow_src >= 0: the append replaced a shared
+ * last block; the sequence shares cow_src again and cow_dst, which must be its last block and no one
+ * else's, is freed.  Appends taken back in reverse order leave tables, refcounts and the free list as
+ * they were before. */
+pa_status pa_alloc_undo_append(pa_allocator* a, int64_t seq_id, int n, int32_t cow_src,
+                               int32_t cow_dst);
 /* Drop a sequence; blocks whose refcount reaches 0 return to the free list. */
 pa_status pa_alloc_free_seq(pa_allocator* a, int64_t seq_id);
 /* Keep only the first num_tokens tokens (0 <= num_tokens <= current count), e.g. to roll

@@ -162,6 +162,7 @@ def _load():
         "pa_alloc_append_slot": (i32, [vp, i64, pi64, pi32, pi32]),
         "pa_alloc_append_slots": (i32, [vp, pi64, i32, pi64, pi32, pint]),
         "pa_alloc_append_tokens": (i32, [vp, i64, i32, pi64, pi32, pi32]),
+        "pa_alloc_undo_append": (i32, [vp, i64, i32, i32, i32]),
         "pa_alloc_free_seq": (i32, [vp, i64]),
         "pa_alloc_truncate": (i32, [vp, i64, i32]),
         "pa_alloc_beam_select": (i32, [vp, pi64, pi32, i32]),
@@ -203,7 +204,7 @@ EXPORTED = (
     "pa_beam_gather", "pa_selftest_bounded_wait", "pa_alloc_create",
     "pa_alloc_create_ordered", "pa_alloc_destroy", "pa_alloc_add_seq", "pa_alloc_fork",
     "pa_alloc_append_slot", "pa_alloc_append_slots", "pa_alloc_append_tokens", "pa_alloc_free_seq",
-    "pa_alloc_truncate",
+    "pa_alloc_undo_append", "pa_alloc_truncate",
     "pa_alloc_beam_select", "pa_alloc_block_table",
     "pa_alloc_block_tables", "pa_alloc_seq_slots", "pa_alloc_refcount", "pa_alloc_num_free",
     "pa_alloc_internal_waste_slots", "pa_alloc_free_list", "pa_alloc_check_append_fits",
@@ -600,6 +601,11 @@ class Allocator:
         _check(lib.pa_alloc_append_tokens(self._h, seq_id, n, _i64p(slots), ctypes.byref(src), ctypes.byref(dst)),
                "pa_alloc_append_tokens")
         return slots[:n], [(src.value, dst.value)] if src.value >= 0 else []
+
+    def undo_append(self, seq_id, n, pair=None):
+        """Take back the last n tokens of an append, and the copy pair that it reported."""
+        src, dst = pair or (-1, -1)
+        _check(lib.pa_alloc_undo_append(self._h, seq_id, n, src, dst), "pa_alloc_undo_append")
 
     def append_slots(self, seq_ids, slot_out=None, pairs_out=None):
         """append_slot for every id, all or nothing; returns (slots int64[n], pairs int32[k,2])."""

@@ -285,43 +285,41 @@ class PagedKVCache:
 
     # -- prompts, chunks and single tokens, device tensors in and out --------------------
     def _append_tokens(self, seq_ids, query_lens, grown):
-        """Slots (int64 [T]) of query_lens[b] more tokens of every sequence; a new one is registered,
-        and a shared last block that is written is copied.  What `_take_back` needs is appended to
-        `grown`."""
+        """Slots (int64 [T]) of query_lens[b] more tokens of every sequence, a new one being registered,
+        and the copies (src, dst) of shared last blocks that this calls for.  What `_take_back` needs is
+        appended to `grown`: (sequence, tokens, its copy, whether it is new).  Host state alone."""
         if all(n == 1 for n in query_lens):  # a step of single tokens: one call
             try:
                 slots, pairs = self.alloc.append_slots(seq_ids)
-                grown.extend((sid, 1) for sid in seq_ids)
-                self._copy_pairs(pairs.tolist())
-                return slots
             except _b.PAError as e:
                 if e.status != _b.PA_ERR_NOT_FOUND:
                     raise
+            else:
+                pairs = [tuple(p) for p in pairs.tolist()]
+                copied = {p[1]: p for p in pairs}   # (a copied block is where the token went)
+                grown.extend((sid, 1, copied.get(b), False)
+                             for sid, b in zip(seq_ids, (slots // self.block_size).tolist()))
+                return slots, pairs
         slots, pairs = [np.empty(0, np.int64)], []
-        try:
-            for sid, n in zip(seq_ids, query_lens):
-                try:
-                    new, copies = self.alloc.append_tokens(sid, n)
-                    grown.append((sid, n))
-                    pairs += copies
-                except _b.PAError as e:
-                    if e.status != _b.PA_ERR_NOT_FOUND:
-                        raise
-                    self.alloc.add_seq(sid, n)
-                    grown.append((sid, None))
-                    new = self.alloc.seq_slots(sid)
-                slots.append(new)
-        finally:
-            # (after an error as well: the copied block is the sequence's own now and keeps its tokens)
-            self._copy_pairs(pairs)
-        return np.concatenate(slots)
+        for sid, n in zip(seq_ids, query_lens):
+            try:
+                new, copies = self.alloc.append_tokens(sid, n)
+                grown.append((sid, n, copies[0] if copies else None, False))
+                pairs += copies
+            except _b.PAError as e:
+                if e.status != _b.PA_ERR_NOT_FOUND:
+                    raise
+                self.alloc.add_seq(sid, n)
+                grown.append((sid, n, None, True))
+                new = self.alloc.seq_slots(sid)
+            slots.append(new)
+        return np.concatenate(slots), pairs
 
     def _take_back(self, grown):
-        for sid, n in reversed(grown):
-            if n is None:
+        for sid, n, pair, new in reversed(grown):
+            self.alloc.undo_append(sid, n, pair)
+            if new:
                 self.alloc.free_seq(sid)
-            else:
-                self.alloc.truncate(sid, self.alloc.block_table(sid)[1] - n)
 
     def _tables(self, seq_ids):
         """Block tables, as wide as the longest sequence needs, and lengths of live sequences."""
@@ -353,7 +351,8 @@ class PagedKVCache:
         (float64 device tensor, ``pa_rope_frequencies``) q and k are rotated by the tokens'
         positions first.  softcap, alibi_slopes, window, prefix_lens and first_keys as in
         ``pa_attention`` (device tensors).  Copy on write as in ``step``.  Returns out [T,Hq,D];
-        the work is queued on the stream.  A call that raises leaves every sequence as it was.
+        the work is queued on the stream.  A call that raises leaves every sequence as it was, its blocks
+        and their sharing included.
         """
         lens = [int(n) for n in query_lens]
         ids = [int(i) for i in seq_ids]
@@ -386,7 +385,8 @@ class PagedKVCache:
     def _extend(self, ids, lens, q, k, v, scale, inv_freq, layout, attn_factor, softcap, alibi_slopes, window,
                 prefix_lens, first_keys, out, stream, grown):
         (T, Hq, D), B = q.shape, len(ids)
-        slots = self._append_tokens(ids, lens, grown)
+        slots, pairs = self._append_tokens(ids, lens, grown)
+        self._copy_pairs(pairs)
         if out is None:
             out = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
         if T > 0:

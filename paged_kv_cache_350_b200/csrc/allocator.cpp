@@ -263,6 +263,32 @@ pa_status append_tokens_impl(pa_allocator* a, int64_t seq_id, int n, int64_t* sl
   return PA_OK;
 }
 
+pa_status undo_append_impl(pa_allocator* a, int64_t seq_id, int n, int32_t cow_src, int32_t cow_dst) {
+  if (!a || n < 0) return PA_ERR_INVALID_ARG;
+  auto it = a->seqs.find(seq_id);
+  if (it == a->seqs.end()) return PA_ERR_NOT_FOUND;
+  Seq& s = it->second;
+  if (n > s.ntok) return PA_ERR_INVALID_ARG;
+  const int64_t left = s.ntok - n, bs = a->block_size;
+  const size_t keep = static_cast<size_t>((left + bs - 1) / bs);
+  if (cow_src >= 0 && (left % bs == 0 || cow_src >= a->num_blocks || cow_src == cow_dst ||
+                       s.table[keep - 1] != cow_dst || a->ref[cow_dst] != 1 || a->ref[cow_src] < 1))
+    return PA_ERR_INVALID_ARG;
+  while (s.table.size() > keep) {
+    const int32_t b = s.table.back();
+    s.table.pop_back();
+    if (--a->ref[b] == 0) a->free_stack.push_back(b);
+  }
+  if (cow_src >= 0) {
+    s.table.back() = cow_src;
+    a->ref[cow_src] += 1;
+    a->ref[cow_dst] = 0;
+    a->free_stack.push_back(cow_dst);
+  }
+  s.ntok = left;
+  return PA_OK;
+}
+
 // free_stack holds every block at creation, so its capacity covers all pushes: freeing
 // never allocates.
 pa_status free_seq_impl(pa_allocator* a, int64_t seq_id) {
@@ -409,6 +435,10 @@ pa_status pa_alloc_append_slots(pa_allocator* a, const int64_t* seq_ids, int n,
 pa_status pa_alloc_append_tokens(pa_allocator* a, int64_t seq_id, int n, int64_t* slots,
                                  int32_t* cow_src, int32_t* cow_dst) {
   return guarded([&] { return append_tokens_impl(a, seq_id, n, slots, cow_src, cow_dst); });
+}
+
+pa_status pa_alloc_undo_append(pa_allocator* a, int64_t seq_id, int n, int32_t cow_src, int32_t cow_dst) {
+  return guarded([&] { return undo_append_impl(a, seq_id, n, cow_src, cow_dst); });
 }
 
 pa_status pa_alloc_free_seq(pa_allocator* a, int64_t seq_id) {
