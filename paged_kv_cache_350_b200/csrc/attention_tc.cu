@@ -731,9 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t raw[2][32];
           tc05::ld32(tsh, raw[0]);
           tc05::ld32(tsh + 32, raw[1]);
-          tc05::wait_ld();
-          tc05::landed(raw[0]);
-          tc05::landed(raw[1]);
+          tc05::wait_ld(raw[0], raw[1]);
           float x[kHalf];
 #pragma unroll
           for (int e = 0; e < kHalf; ++e) x[e] = __uint_as_float(raw[e / 32][e % 32]);
@@ -759,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < D; c += 16) {
                 uint32_t v[16];
                 tc05::ld16(to + c, v);
-                tc05::wait_ld();
+                tc05::wait_ld(v);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
                 tc05::st16(to + c, v);
@@ -837,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[32];
           if (active) {
             tc05::ld32(to + c, v);
-            tc05::wait_ld();
+            tc05::wait_ld(v);
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = 0u;

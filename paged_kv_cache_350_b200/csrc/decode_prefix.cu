@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live) {
         uint32_t v[32];
         tc05::ld_pair32(sbuf + 64 * grp, v);
-        tc05::wait_ld();
+        tc05::wait_ld(v);
         // a column past its chunk's valid tokens, an own chunk of another member, or a
         // chunk the tile does not have is masked (the per-chunk fields are read from the
         // stage's record, which stays until the stage is released after this tile's P.V);
@@ -922,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < D; c += 64) {
           uint32_t v[32];
           tc05::ld_pair32(oa + c, v);  // this half's 32 of the 64 columns
-          tc05::wait_ld();
+          tc05::wait_ld(v);
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
           tc05::st_pair32(oa + c, v);
@@ -1023,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc05::ld_pair16(tmem + kColO0 + lane_addr + c, a0);
             tc05::ld_pair16(tmem + kColO1 + lane_addr + c, a1);
           }
-          tc05::wait_ld();
+          tc05::wait_ld(a0, a1);
           const int col = c + W * h;  // this thread's W columns
           float vv[W];
 #pragma unroll

@@ -220,12 +220,23 @@ __device__ __forceinline__ void st_pair16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// After wait_ld: what was loaded into v is used from here on only (no instruction; the loads write
-// their registers asynchronously, which the compiler does not know of an asm statement).
-__device__ __forceinline__ void landed(uint32_t (&v)[32]) {
-  asm volatile("" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
-  asm volatile("" : "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]));
+// v's registers are used from here on only (no instruction).
+__device__ __forceinline__ void landed16(uint32_t* v) {
+  asm volatile("" : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                    "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
+}
+// Wait for this thread's loads, which went to v (all arrays loaded since the last wait).  The loads write
+// their registers asynchronously, which the compiler does not know of an asm statement, and a memory
+// clobber does not hold back arithmetic on registers: so the wait names them.
+template <int... N>
+__device__ __forceinline__ void wait_ld(uint32_t (&... v)[N]) {
+  static_assert(sizeof...(N) > 0 && ((N % 16 == 0) && ...), "what was loaded");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  auto land = [](uint32_t* a, int n) {
+#pragma unroll
+    for (int i = 0; i < n; i += 16) landed16(a + i);
+  };
+  (land(v, N), ...);
 }
 
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
