@@ -296,9 +296,12 @@ class PagedKVCache:
                     raise
             else:
                 pairs = [tuple(p) for p in pairs.tolist()]
-                copied = {p[1]: p for p in pairs}   # (a copied block is where the token went)
-                grown.extend((sid, 1, copied.get(b), False)
-                             for sid, b in zip(seq_ids, (slots // self.block_size).tolist()))
+                if pairs:  # (a copied block is where the token went)
+                    copied = {p[1]: p for p in pairs}
+                    grown.extend((sid, 1, copied.get(b), False)
+                                 for sid, b in zip(seq_ids, (slots // self.block_size).tolist()))
+                else:
+                    grown.extend([(sid, 1, None, False) for sid in seq_ids])
                 return slots, pairs
         slots, pairs = [np.empty(0, np.int64)], []
         for sid, n in zip(seq_ids, query_lens):
@@ -335,11 +338,6 @@ class PagedKVCache:
             self._table_blocks = blocks + 1
             return tables[:, :blocks], lens
 
-    def _copy_pairs(self, pairs):
-        if pairs:
-            d = torch.tensor(pairs, dtype=torch.int32).to(self.device)
-            _b.pa_copy_blocks(self.k_pool, self.v_pool, d, err_flag=self.err)
-
     def extend(self, seq_ids, query_lens, q, k, v, scale, inv_freq=None, layout=_b.PA_ROPE_HALF,
                attn_factor=1.0, softcap=0.0, alibi_slopes=None, window=0, prefix_lens=None,
                first_keys=None, out=None, stream=None):
@@ -351,8 +349,9 @@ class PagedKVCache:
         (float64 device tensor, ``pa_rope_frequencies``) q and k are rotated by the tokens'
         positions first.  softcap, alibi_slopes, window, prefix_lens and first_keys as in
         ``pa_attention`` (device tensors).  Copy on write as in ``step``.  Returns out [T,Hq,D];
-        the work is queued on the stream.  A call that raises leaves every sequence as it was, its blocks
-        and their sharing included.
+        the work is queued on the stream and not waited for (it cannot be captured into a graph: slots
+        and tables are this one step's).  A call that raises leaves every sequence as it was, its blocks and
+        their sharing included.
         """
         lens = [int(n) for n in query_lens]
         ids = [int(i) for i in seq_ids]
@@ -384,22 +383,28 @@ class PagedKVCache:
 
     def _extend(self, ids, lens, q, k, v, scale, inv_freq, layout, attn_factor, softcap, alibi_slopes, window,
                 prefix_lens, first_keys, out, stream, grown):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("extend: a step cannot be captured into a graph")
         (T, Hq, D), B = q.shape, len(ids)
         slots, pairs = self._append_tokens(ids, lens, grown)
-        self._copy_pairs(pairs)
         if out is None:
             out = torch.empty((T, Hq, D), dtype=q.dtype, device=self.device)
         if T > 0:
             tables, seq_lens = self._tables(ids)
-            MB = tables.shape[1]
+            MB, P = tables.shape[1], len(pairs)
             starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
             positions = np.arange(T, dtype=np.int32) + np.repeat(seq_lens - starts[1:], lens)
-            # everything of the step in one copy (the host array is staged before the call returns)
-            host = np.concatenate([slots.view(np.int32), positions, seq_lens, starts, tables.ravel()])
-            dev = torch.from_numpy(host).to(self.device)
-            slots_d, at = dev[:2 * T].view(torch.int64), 2 * T
-            pos_d, lens_d, starts_d, tables_d = (dev[at:at + T], dev[at + T:at + T + B],
-                                                 dev[at + T + B:at + T + 2 * B + 1], dev[at + T + 2 * B + 1:])
+            # everything of the step in one copy, which does not wait: the pinned buffer goes back to
+            # torch's pool of them, which hands it out again once the copy is done
+            sizes = [2 * T, T, B, B + 1, B * MB, 2 * P]
+            host = torch.empty(sum(sizes), dtype=torch.int32, pin_memory=True)
+            np.concatenate([slots.view(np.int32), positions, seq_lens, starts, tables.ravel(),
+                            np.array(pairs, dtype=np.int32).ravel()], out=host.numpy())
+            dev = host.to(self.device, non_blocking=True)
+            slots_d, pos_d, lens_d, starts_d, tables_d, pairs_d = dev.split(sizes)
+            slots_d = slots_d.view(torch.int64)
+            if P:
+                _b.pa_copy_blocks(self.k_pool, self.v_pool, pairs_d.view(P, 2), err_flag=self.err, stream=stream)
             if inv_freq is None:
                 _b.pa_reshape_and_cache(k.contiguous(), v.contiguous(), self.k_pool, self.v_pool, slots_d,
                                         err_flag=self.err, stream=stream)

@@ -102,3 +102,64 @@ def test_a_step_that_fails_on_its_way_loses_nothing(monkeypatch, lens, broken):
         assert torch.equal(cache.v_pool.view(-1, HKV, D)[slots], torch.cat([first[2], more[2][t:t + n]]))
         t += n
     cache.check_device_errors()
+
+
+def steps(cache, data, gate=None, **kw):
+    """A prompt, forks of it, and single tokens with a chunk among them; their outputs."""
+    outs = [cache.extend([0], [13], *data[0], 0.1, **kw)]
+    for i in (1, 2):
+        cache.fork(0, i)
+    if gate is not None:
+        gate()
+    for d in data[1:]:
+        outs.append(cache.extend([0, 1, 2], [1, 1, d[0].shape[0] - 2], *d, 0.1, **kw))
+    return outs
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("on_stream", [False, True])
+def test_the_host_goes_on_while_the_gpu_works(rotated, on_stream):
+    """32 steps are queued behind a kernel that still runs when the last call returns."""
+    g = torch.Generator().manual_seed(2)
+    data = [tuple(torch.randn(T, h, D, generator=g).cuda() for h in (HQ, HKV, HKV)) for T in [13] + [3, 8] * 16]
+    inv = torch.from_numpy(pa.pa_rope_frequencies(D)[0]).cuda() if rotated else None
+    stream = torch.cuda.Stream() if on_stream else torch.cuda.current_stream()
+    kw = dict(inv_freq=inv, softcap=30.0, stream=stream)
+    torch.cuda.synchronize()
+    mk = lambda: pa.PagedKVCache(200, BS, HKV, D, dtype=torch.float32, shuffle_seed=9)  # noqa: E731
+    want = steps(mk(), data, **kw)
+    torch.cuda.synchronize()
+    done = torch.cuda.Event()
+
+    def gate():
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(1_000_000_000)   # (about half a second)
+            done.record(stream)
+    cache = mk()
+    torch.cuda.synchronize()
+    got = steps(cache, data, gate, **kw)
+    assert not done.query()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    cache.check_device_errors()
+
+
+@pytest.mark.gpu
+def test_a_step_is_not_captured():
+    cache = pa.PagedKVCache(16, BS, HKV, D, dtype=torch.float32)
+    mk = lambda T: tuple(torch.randn(T, h, D, device="cuda") for h in (HQ, HKV, HKV))  # noqa: E731
+    cache.extend([0], [5], *mk(5), 0.1)
+    more, before = mk(1), state(cache.alloc, [0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    x = torch.zeros(4, device="cuda")
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="captured"):
+            cache.extend([0], [1], *more, 0.1)
+        x += 1
+    assert state(cache.alloc, [0]) == before
+    graph.replay()
+    torch.cuda.synchronize()
+    assert x.tolist() == [1.0] * 4
