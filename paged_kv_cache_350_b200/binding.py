@@ -500,21 +500,31 @@ def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=PA_ROPE_SCALE_NONE, fa
 
 
 # The step calls are in a module of their own (csrc/calls.cpp): the same checks and errors as here,
-# at a tenth of the time.
-try:
-    import torch as _torch  # noqa: F401  (its libraries, before the module that uses them)
+# at a tenth of the time.  It needs torch and is loaded at the first use of one of them, so that what
+# works on host memory (the allocator, workspace sizes, frequencies) needs the C library alone.
+_STEP_CALLS = ("pa_rope_and_cache", "pa_attention", "pa_beam_topk", "pa_beam_gather")
 
-    from . import _calls
-except ImportError as e:
-    raise ImportError("the step calls (_calls.so) are not built; build them with "
-                      "`python -m paged_kv_cache_350_b200.build`") from e
 
-_calls.bind(PAError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
-    lib.pa_rope_and_cache, lib.pa_attention, lib.pa_beam_topk, lib.pa_beam_gather)))
-pa_rope_and_cache = _calls.pa_rope_and_cache
-pa_attention = _calls.pa_attention
-pa_beam_topk = _calls.pa_beam_topk
-pa_beam_gather = _calls.pa_beam_gather
+def _load_step_calls():
+    try:
+        import torch  # noqa: F401  (its libraries, before the module that uses them)
+
+        from . import _calls
+    except ImportError as e:
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_calls.so")
+        why = (f"do not load ({e}): they are built for one torch and one Python" if os.path.exists(path)
+               else "are not built")
+        raise ImportError(f"the step calls (_calls.so) {why}; build them with "
+                          "`python -m paged_kv_cache_350_b200.build`") from e
+    _calls.bind(PAError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in _STEP_CALLS))
+    globals().update({f: getattr(_calls, f) for f in _STEP_CALLS})
+
+
+def __getattr__(name):
+    if name in _STEP_CALLS:
+        _load_step_calls()
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def pa_attention_workspace_size(T, B, max_query_len, Hq, Hkv, D, block_size, max_blocks):

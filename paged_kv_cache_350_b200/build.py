@@ -6,13 +6,16 @@ Compiles every source under ``csrc/`` with nvcc (``-gencode
 arch=compute_100a,code=sm_100a -lineinfo -O3``), links one shared library with
 the CUDA runtime linked statically, and places it next to this file, where the
 Python binding loads it.  ``_calls.so``, the Python module with the step calls on torch
-tensors, is compiled beside it with the host compiler.  Objects go to ``_build/`` at the repository root.
+tensors, is compiled beside it with the host compiler against the installed torch (without one it is left
+out).  Objects go to ``_build/`` at the repository root.
 Rebuilds only what changed unless ``--force``.
 """
 
 from __future__ import annotations
 
 import argparse
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -26,6 +29,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
 CALLS = os.path.join(PKG, "_calls.so")  # the step calls on torch tensors (csrc/calls.cpp)
+CALLS_STAMP = os.path.join(BUILD, "_calls.made_for")
 
 SOURCES = ["api.cu", "decode_tc.cu", "decode_stream.cu", "decode_generic.cu", "cache_ops.cu", "allocator.cpp",
            "decode_noalloc.cu", "decode_prefix.cu", "selftest.cu", "pipeline.cpp",
@@ -96,10 +100,33 @@ def build(force=False, verbose=False, extra_flags=(), out=None, build_dir=None):
     return lib_path
 
 
+def _calls_made_for():
+    """The torch and the Python that _calls.so is built against (None without torch); imports neither."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    return "\n".join([importlib.metadata.version("torch"), spec.origin, sys.version])
+
+
+def calls_stale():
+    """Whether _calls.so is older than its sources, or made for another torch or Python."""
+    if _stale(CALLS, [os.path.join(CSRC, "calls.cpp"), os.path.join(INCLUDE, "pa.h")]):
+        return True
+    try:
+        with open(CALLS_STAMP) as f:
+            return f.read() != _calls_made_for()
+    except FileNotFoundError:
+        return True
+
+
 def build_calls(force=False, verbose=False):
     """The Python extension module with the step calls: host code against torch's headers."""
     src = os.path.join(CSRC, "calls.cpp")
-    if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "pa.h")]):
+    made_for = _calls_made_for()
+    if made_for is None:
+        sys.stderr.write("torch is not installed: the step calls (_calls.so) are not built\n")
+        return None
+    if not force and not calls_stale():
         return CALLS
     import sysconfig
 
@@ -120,6 +147,9 @@ def build_calls(force=False, verbose=False):
     if r.returncode:
         raise RuntimeError("compiling _calls.so failed")
     os.replace(tmp, CALLS)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(made_for)
     return CALLS
 
 
