@@ -345,8 +345,8 @@ pa_status pa_rope_frequencies(int rotary_dim, double base, pa_rope_scaling scali
  * the first rotary_dim elements of every head of q[t] and k[t] become
  *   f * (a cos theta_i - b sin theta_i, a sin theta_i + b cos theta_i)
  * and the elements from rotary_dim on stay.  q goes to q_out[t] ([T][Hq][D], contiguous; may be
- * q itself where q is contiguous, and must not overlap q otherwise), k and the unchanged v to slot slot_mapping[t] of the pools
- * (as pa_reshape_and_cache; a slot < 0 rotates q only).  Angles are formed and reduced in 64
+ * q itself where q is contiguous, and must overlap neither q otherwise nor k and v), k and the unchanged
+ * v to slot slot_mapping[t] of the pools (as pa_reshape_and_cache; a slot < 0 rotates q only).  Angles are formed and reduced in 64
  * bits; the rotation is fp32, rounded once.
  *   inv_freq      [rotary_dim / 2] DEVICE array (pa_rope_frequencies, copied there once)
  *   positions     [T] int32 device

@@ -19,11 +19,13 @@
 // halves of P.V: 327 us for 305).  While group 0 works on its S, the products of group 1 run and the
 // other way round.
 //
-// Bound by the softmax: 16 exponentials a cycle and SM take as long as the products (2048 cycles for
-// a pair of M tiles and 128 keys), and each group's chain S, weights, P.V, S adds its latencies.  A
-// prompt of 8192 tokens, 32/8 heads of 128, with a prefix mask: 609 us, 1138 TFLOP/s; 8 of 2048,
-// causal: 305 us, 902; with capped scores 370 us, 744.  (Sustained, at the 1000 W limit, the prompt takes
-// 710 us at 1.65 GHz.)
+// Bound by latencies: the exponentials take as long as the products (2048 cycles for a pair of M tiles
+// and 128 keys, at 16 a cycle and SM), but no pipe is busy half of the time (8 x 2048 plain: tensor 46 %,
+// exponentials 48, issue 42; capped: 39, 40, 48, and FMA 38).  With two softmax warps a scheduler each
+// group's chain S, weights, P.V, S is not hidden by the other group's.  A prompt of 8192 tokens, 32/8
+// heads of 128, with a prefix mask: 615 us, 1127 TFLOP/s; 8 of 2048, causal: 305 us, 902; with capped
+// scores 370 us, 744 (caps past 50, whose maximum is found: 620 us; past 64: 815 us); with a bias 450 us.
+// (Sustained, at the 1000 W limit, the prompt takes 710 us at 1.65 GHz.)
 //
 // P is rounded to bf16 (half a step, 2^-8 of each weight, as the output is); row sums, maxima and
 // O stay in 32 bits.  The reference maximum moves lazily, by more than 2^8 only; capped scores have

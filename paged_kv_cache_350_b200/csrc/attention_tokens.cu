@@ -9,8 +9,9 @@
 // A tile is one m16n8k16 product chain over the rows (tc_tile.cuh), whose scores the Modified
 // functor caps, biases and masks; P enters P.V as two bf16 parts, so it keeps ~16 bits.  Caps
 // and biases cost about 20 instructions a tile and lane beside ~150, which the loads hide: 256
-// tokens with 1000 cached, 32/8 heads of 128, take 168 us (6.26 TB/s) capped and 167 plain; 8
-// contexts of 32K to 128K with a bias 310 us (6.6 TB/s, the rate of a copy).
+// tokens with 1000 cached, 32/8 heads of 128, take 171 us (6.15 TB/s) capped and plain; 8
+// contexts of 32K to 128K with a bias 312 us (6.5 TB/s, the rate of a copy).  With heads of 64 a tile has
+// half the bytes and nearly the same instructions outside its products: 135 us, 3.9 TB/s.
 //
 // Every CTA scans the units' tile counts itself (B loads), so there is no plan kernel: for a
 // single request the launches are most of the time.  Units cut by a range boundary leave partials

@@ -6,9 +6,11 @@
 // conflicts, for all rows.  The lanes' partial scores, 8 R of them, are summed by a butterfly
 // that halves the values at every step (31 shuffles for 32 sums where 32 reductions would take
 // 160) and leaves lane l with the score of row l / 8 (+ 4, + 8, ..), key l % 8; weights go back by
-// shuffles.  With R = 4 that is about 60 instructions a key and warp for its 1024 bytes (D = 128):
-// bound by memory up to 8 rows (256 tokens, 32/8 heads of 128, cap and window: 218 us, 5.4 TB/s), by
-// issue at 16 (2.2 TB/s).
+// shuffles.  With R = 4 that is about 60 instructions a key and warp for its 1024 bytes (D = 128).
+// 256 tokens with 1000 cached, 8 KV heads of 128: 6.0 TB/s with up to 4 rows, 5.1 with 8, 2.6 with 16,
+// where the rows' own products and shuffles take longer than the memory; with heads of 64, where the
+// butterfly is the same for half the bytes, 3.9 TB/s with up to 4 rows, 3.1 and 1.9.  With cap and
+// window, lengths from 63 to 4095, heads of 128 and 4 rows: 220 us, 5.4 TB/s.
 
 #include "attention_ranges.cuh"
 

@@ -14,8 +14,9 @@
 // the lanes' maxima, so few values are ever inserted.  A second, small kernel forms the scores of
 // the W * chunks * k values kept, spread over its warps, and keeps the best k of them.  Lists are
 // merged by bitonic steps across the lanes.  64 requests of 4 beams over 131072 fp32 logits: 31 us
-// (4.3 TB/s, issue at 54 %: an exponential and six more operations a logit) and 5 us for the join;
-// one request of 4 x 32000: 11 us with the gather, which is launches.
+// (4.3 TB/s) and 5 us for the join; an exponential and six more operations a logit, issue at 56 % on
+// average but from 42 to 74 % by SM: 512 CTAs are three or four for each, for the whole time.
+// One request of 4 x 32000: 11 us with the gather, which is launches.
 //
 // lse and scores are 64-bit from the chunk sums on: the chosen indices compare scores of
 // different beams, which a 32-bit subtraction would round into ties.

@@ -21,9 +21,10 @@
 // overlap.  Three forms by where a pair lies: in two vectors R / 2 apart (half layout, R / 2 a
 // whole number of vectors), within one vector (interleaved), or anywhere (half layout otherwise:
 // the token's rows pass through shared memory).  Where a stride is not a multiple of 16 bytes a
-// scalar form runs.  16384 tokens, 32/8 heads of 128 in bf16: 64 us (6.3 TB/s) with 64 elements
-// interleaved, 69 us with whole heads in halves, 107 us with 50 elements in halves (staged); 256
-// tokens: 3 us.
+// scalar form runs.  16384 tokens, 32/8 heads of 128 in bf16: 65 us (6.2 TB/s) with 64 elements
+// interleaved, 61 us with whole heads in halves, 95 us with 50 elements in halves (staged: each
+// element's partner is read by itself from shared memory, and a barrier stands between the loads and the
+// stores), 206 us with whole heads in the scalar form; 256 tokens: 3 us.
 
 #include <cuda_bf16.h>
 
