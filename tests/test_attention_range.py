@@ -38,6 +38,8 @@ class Capped(Case):
         size, dx = torch.zeros_like(out), torch.zeros(T, self.Hq, 1, dtype=torch.float64)
         for b, n in enumerate(self.n):
             t0, L = int(self.starts[b]), self.L[b]
+            if n == 0:
+                continue
             pos, key = torch.arange(L - n, L)[:, None], torch.arange(L)[None, :]
             for h in range(self.Hq):
                 q, k, v = self.q[t0:t0 + n, h].double(), self.keys[b][:, h // G], self.values[b][:, h // G]
@@ -118,3 +120,15 @@ def test_a_bias_past_2_24_positions(dtype, n, Hq):
         # weights rounded to bf16 for their product, the output; sums over the keys that have a weight
         tol = size * (2 * off + (tail + 8) * ULP + 2.0 ** -20 + (half if dtype == torch.bfloat16 else 0)) + ref.abs() * half
         assert bool(((got[:, h] - ref).abs() <= tol).all()), float(((got[:, h] - ref).abs() / tol).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap", [1e3, 1e6, 1e30])
+def test_wide_caps_of_wide_groups_and_of_large_batches(cap):
+    """The CUDA-core kernel: more than 128 heads a group, and fp32 batches of more sequences than are scanned."""
+    Capped("bf16", [3, 1], [50, 200], 130, 1, 64, 16, softcap=cap, spreads=(1.0, 300.0)).check()
+    Capped("f32", [1] * 2100, [1 + i % 40 for i in range(2100)], 2, 1, 64, 8, softcap=cap).check()
+    # and the tensor cores, where units are taken one by one
+    n = [33 if i % 7 else 0 for i in range(190)]
+    Capped("bf16", n, [a + (i * 37) % 150 for i, a in enumerate(n)], 16, 8, 64, 16, softcap=cap,
+           spreads=(1.0, 300.0)).check()
