@@ -105,7 +105,11 @@ def _calls_made_for():
     spec = importlib.util.find_spec("torch")
     if spec is None:
         return None
-    return "\n".join([importlib.metadata.version("torch"), spec.origin, sys.version])
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # (not an installed package: a tree on the path)
+        version = str(os.path.getmtime(spec.origin))
+    return "\n".join([version, spec.origin, sys.version])
 
 
 def calls_stale():

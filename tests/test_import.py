@@ -66,3 +66,12 @@ def test_step_calls_are_built_anew_for_another_torch(monkeypatch):
     monkeypatch.undo()
     monkeypatch.setattr(bld, "CALLS_STAMP", bld.CALLS_STAMP + ".missing")
     assert bld.calls_stale()
+
+
+def test_a_torch_without_package_metadata_is_known_by_its_files(monkeypatch):
+    def none(name):
+        raise bld.importlib.metadata.PackageNotFoundError(name)
+    known = bld._calls_made_for()
+    monkeypatch.setattr(bld.importlib.metadata, "version", none)
+    assert bld._calls_made_for() not in (None, known)
+    assert bld._calls_made_for() == bld._calls_made_for()
